@@ -45,7 +45,8 @@
  *    y, dX, the saved activations and the weight gradients are bf16) or
  *    MOE_MXFP8 (the same with MXFP8 operands: E4M3FN codes with one
  *    power-of-two E8M0 scale byte per 32 values -- see "MXFP8 expert GEMMs"
- *    below).  Router
+ *    below).  MOE_MXFP4 and MOE_MXFP4_A8 run the forward alone, with 4-bit
+ *    expert weights ("MXFP4 experts" below) and bf16 x and y.  Router
  *    logits and probabilities are always fp32 (German summary, section 2 E:
  *    the router stays in high precision).
  */
@@ -67,7 +68,14 @@ typedef enum {
   MOE_ERR_HIP = 4           /* a HIP runtime call or kernel launch failed */
 } moe_status;
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_E4M3 = 2, MOE_MXFP8 = 3 } moe_dtype;
+typedef enum {
+  MOE_F32 = 0,
+  MOE_BF16 = 1,
+  MOE_E4M3 = 2,
+  MOE_MXFP8 = 3,
+  MOE_MXFP4 = 4,    /* forward only: MXFP4 weights and activations */
+  MOE_MXFP4_A8 = 5  /* forward only: MXFP4 weights, MXFP8 activations */
+} moe_dtype;
 
 typedef struct {
   int64_t T, d, E, k, f;
@@ -280,6 +288,10 @@ typedef struct {
      / moe_grouped_gemm_bwd_gather), so xp is neither written nor read and
      may be NULL; needs T * d * element bytes below 2^31 - 4096 */
   int32_t fused_permute;
+  /* MXFP4 layers (sh->dtype == MOE_MXFP4 or MOE_MXFP4_A8; moe_layer_fwd only):
+     the quantised weights; xq holds the codes of x ([T][d/2], MXFP4_A8 [T][d])
+     and xs its scale bytes [T][d/32].  xp, xpq, xps, ab and h are not used */
+  const struct moe_mx4_weights* wmx4;
 } moe_layer_io;
 
 /*
@@ -289,7 +301,9 @@ typedef struct {
  * moe_unpermute in sequence on one stream.  For MOE_E4M3: moe_route,
  * moe_quantize_rows of x into xq/xs, moe_permute_e4m3 into xpq/xps,
  * moe_grouped_gemm_fwd_e4m3, moe_unpermute (MOE_MXFP8: the _mx calls, weights
- * io->wmx).  With io->aux_loss set, the routing is moe_route_aux and
+ * io->wmx).  For MOE_MXFP4 / MOE_MXFP4_A8: moe_route, the permutation's map,
+ * moe_quantize_rows_mx4 / _mx of x, moe_grouped_gemm_fwd_mx4 reading x through
+ * token_of, moe_unpermute (io->memory_efficient must be 0).  With io->aux_loss set, the routing is moe_route_aux and
  * moe_aux_loss_final (alpha = io->aux_alpha) follows the permutation;
  * ws_bytes then needs MOE_WS_AUX_LOSS more bytes.  With io->memory_efficient:
  * moe_row_probs into io->row_prob, the row-scaled expert forward (bf16:
@@ -627,6 +641,80 @@ int moe_grouped_gemm_bwd_mx(const moe_shape* sh, const int32_t* offsets, const i
                             const void* x, const void* ab, const void* h, const void* dO,
                             const moe_mx_weights* w, void* dab, void* dXp, void* dW1, void* dW3,
                             void* dW2, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * MXFP4 experts
+ * -------------
+ * The pages credit FP4 beside MXFP8 for the Blackwell results (German summary,
+ * results table) without a definition; the storage is the OCP Microscaling one:
+ * E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two to a byte
+ * with the lower index in the low nibble, and one E8M0 scale byte s + 127 per
+ * 32 consecutive values along a product's contraction axis.  s is the smallest
+ * integer with max|v| <= 6 * 2^s (nothing saturates; at least -126; 0 for an
+ * all-zero block, whose codes are zeros), codes are E2M1(v * 2^-s), round to
+ * nearest even, sign kept.  A block that holds a NaN or an infinity has scale
+ * byte 255, E8M0's NaN: every product it enters is NaN.  Forward only: there
+ * are no weight gradients in this format (moe_layer_bwd returns
+ * MOE_ERR_UNSUPPORTED).  moe_dequantize_weights_mx4 gives the bf16 weights that
+ * the codes stand for, for a bf16 backward on the weights the forward used.
+ *
+ * Weight layout.  A matrix with R rows (the contraction) and N columns is
+ * stored in tiles of 128 rows x 16 columns, 1 KB each:
+ *   codes  [E][N/16][R/128][4][16][16]: byte b of (group g, column c) of tile
+ *          (nt, kt) holds rows 128 kt + 32 g + 2 b (low nibble) and + 1 of
+ *          column 16 nt + c;
+ *   scales [E][N/64][R/128][4][16][4]: byte j of (g, c) of (nb, kt) is the scale
+ *          of rows 128 kt + 32 g .. + 31 of column 64 nb + 16 j + c.
+ * W1 and W3 form one matrix W13 of N = 2f columns whose 16-column groups
+ * alternate (group 2 i: columns 16 i .. of W1, group 2 i + 1: of W3).
+ * d and f must be multiples of 128, no shared expert.
+ */
+
+/* Quantised expert weights as written by moe_quantize_weights_mx4. */
+typedef struct moe_mx4_weights {
+  const uint8_t *W13, *W2;   /* codes of [E][d][2f] (W1 with W_pair = W3) and [E][f][d] */
+  const uint8_t *W13s, *W2s; /* their scale bytes */
+} moe_mx4_weights;
+
+/* moe_quantize_rows_mx4 -- 1 x 32 blocks along each row of src [rows][cols]
+ * (MOE_BF16 or MOE_F32, cols a multiple of 32): codes [rows][cols/2], scale
+ * bytes [rows][cols/32]. */
+int moe_quantize_rows_mx4(const void* src, int32_t src_dtype, int64_t rows, int64_t cols,
+                          uint8_t* codes, uint8_t* scales, void* stream);
+
+/* moe_quantize_weights_mx4 -- E matrices W [E][R][C] (MOE_F32 masters or
+ * MOE_BF16; R, C multiples of 128) into the layout above, N = C; with W_pair
+ * (a second [E][R][C], same type) N = 2C and the 16-column groups of W and
+ * W_pair alternate.  One pass over the source. */
+int moe_quantize_weights_mx4(const void* W, const void* W_pair, int32_t src_dtype, int64_t E,
+                             int64_t R, int64_t C, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* moe_dequantize_weights_mx4 -- the values that the codes and scales stand for,
+ * bf16 [E][R][C] (exact unless below bf16's range), W_pair NULL for a single
+ * matrix. */
+int moe_dequantize_weights_mx4(const uint8_t* codes, const uint8_t* scales, int64_t E, int64_t R,
+                               int64_t C, void* W, void* W_pair, void* stream);
+
+/*
+ * moe_grouped_gemm_fwd_mx4 -- the experts' forward on quantised rows: for
+ * expert e and its rows r in [offsets[e], offsets[e+1])
+ *   [a|b] = xq_r W13_e, h = silu(a) b, o = Q(h) W2_e
+ * with fp32 accumulation; Q rounds h once, from fp32, to MXFP4 (MOE_MXFP4) or
+ * MXFP8 (MOE_MXFP4_A8, the rule of "MXFP8 expert GEMMs" with s at least -126
+ * and NaN blocks as above) and o [P][d] is bf16.  xq, xs are rows as
+ * moe_quantize_rows_mx4 (MOE_MXFP4) or moe_quantize_rows_mx (MOE_MXFP4_A8)
+ * writes them: row r is row token_of[r] of [T] rows, or, token_of NULL, row r
+ * of [P] permuted rows.  Rows of o from offsets[E] on are not written.
+ * ws_bytes >= moe_workspace_bytes(sh, MOE_WS_GEMM_FWD).  Errors: MOE_ERR_INVALID
+ * for another dtype; MOE_ERR_UNSUPPORTED for d or f not a multiple of 128,
+ * P * max(d, f) >= 2^31 - 4096 or d * f >= 2^31.
+ * (With E4M3 rows the matrix instruction itself cuts the products of each 8
+ * consecutive k to multiples of 2^-13 of the largest before it adds them in
+ * fp32; E2M1 products are added exactly.)
+ */
+int moe_grouped_gemm_fwd_mx4(const moe_shape* sh, const int32_t* offsets, const int32_t* token_of,
+                             const uint8_t* xq, const uint8_t* xs, const moe_mx4_weights* w,
+                             void* o, void* ws, size_t ws_bytes, void* stream);
 
 /* moe_probe_mfma -- measurement helper, not a step of the layer: the dense
  * matrix-core rate and the shader clock this GPU sustains under MFMAs alone,

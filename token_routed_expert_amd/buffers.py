@@ -4,8 +4,8 @@ from __future__ import annotations
 import torch
 
 from . import _native as N
-from .ops import (E4M3Weights, MXWeights, make_shape, moe_quantize_weights,
-                  moe_quantize_weights_mx, moe_workspace_bytes)
+from .ops import (E4M3Weights, MX4Weights, MXWeights, make_shape, moe_quantize_weights,
+                  moe_quantize_weights_mx, moe_quantize_weights_mx4, moe_workspace_bytes)
 
 
 def layer_buffers(T, d, E, k, f, f_shared=0, dtype="bf16", device="cuda", inputs=None,
@@ -49,6 +49,13 @@ def layer_buffers(T, d, E, k, f, f_shared=0, dtype="bf16", device="cuda", inputs
                  xpq=z(P, d, dtype=u8), xps=z(P, d // 32, dtype=u8))
         if "W1" in b and b["W1"].dtype == torch.float32:
             b["wmx"] = quantized_weights_mx(b["W1"], b["W3"], b["W2"])
+    if dtype in ("mxfp4", "mxfp4_a8"):
+        u8 = torch.uint8
+        for n in ("xp", "ab", "h", "dO", "dab", "dXp", "dX", "dW1", "dW3", "dW2"):  # forward only
+            b.pop(n)
+        b.update(xq=z(T, d // 2 if dtype == "mxfp4" else d, dtype=u8), xs=z(T, d // 32, dtype=u8))
+        if "W1" in b:
+            b["wmx4"] = quantized_weights_mx4(b["W1"], b["W3"], b["W2"])
     if fused_permute:
         b.pop("xp", None)
         b["fused_permute"] = 1
@@ -112,3 +119,17 @@ def quantized_weights_mx(W1, W3, W2, stream=None) -> MXWeights:
     wq = MXWeights(t)
     requantize_weights(wq, W1, W3, W2, stream)
     return wq
+
+
+def quantized_weights_mx4(W1, W3, W2, stream=None) -> MX4Weights:
+    """MXFP4 codes and E8M0 scale bytes of bf16 or fp32 expert weights (W1, W3
+    [E][d][f], W2 [E][f][d]), made by moe_quantize_weights_mx4."""
+    E, d, f = W1.shape
+    t = {}
+    for name, W, pair, N_ in (("W13", W1, W3, 2 * f), ("W2", W2, None, d)):
+        R = W.shape[1]
+        t[name] = torch.empty(E, N_ // 16, R // 128, 4, 16, 16, dtype=torch.uint8, device=W.device)
+        t[name + "s"] = torch.empty(E, N_ // 64, R // 128, 4, 16, 4, dtype=torch.uint8,
+                                    device=W.device)
+        moe_quantize_weights_mx4(W, pair, t[name], t[name + "s"], stream)
+    return MX4Weights(t)

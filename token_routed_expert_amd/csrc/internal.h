@@ -154,6 +154,31 @@ int quant_tokblk_launch(const void* src, const int32_t* src_row, const int32_t* 
                         const int32_t* blk, int E, int64_t P, int64_t C, uint8_t* codes,
                         float* scales, hipStream_t s, uint8_t* rcodes = nullptr,
                         float* rscales = nullptr);
+// quant_mx4.hip: MXFP4 (E2M1 codes, E8M0 bytes per 32 values): rows [rows][cols]
+// -> codes [rows][cols/2] + bytes [rows][cols/32]; weights [E][R][C] (Wp: a
+// second matrix whose 16-column groups alternate with W's) -> the products'
+// tile layout, and back to bf16
+int quant_rows_mx4_launch(const void* src, bool src_f32, int64_t rows, int64_t cols,
+                          uint8_t* codes, uint8_t* sb, hipStream_t s);
+int quant_weights_mx4_launch(const void* W, const void* Wp, bool src_f32, int64_t E, int64_t R,
+                             int64_t C, uint8_t* codes, uint8_t* sb, hipStream_t s);
+int dequant_weights_mx4_launch(const uint8_t* codes, const uint8_t* sb, int64_t E, int64_t R,
+                               int64_t C, void* W, void* Wp, hipStream_t s);
+
+// gemm_mx4.hip: one product of the experts' forward with MXFP4 weights.  fc 1:
+// a/as = quantised x rows (row token_of[r] of them when token_of is set), w/ws
+// = W13, writes hq/hs; fc 2: a/as = hq/hs, w/ws = W2, writes o (bf16 [P][d]).
+struct Mx4Args {
+  const int32_t* offsets;
+  const int32_t* token_of;
+  int E, d, f, P, T;
+  const uint8_t *a, *as;
+  const uint8_t *w, *ws;
+  uint8_t *hq, *hs;
+  void* o;
+};
+int gemm_mx4_launch(int fc, bool a8, const Mx4Args& a, hipStream_t s);
+
 // permute.hip: rows of e4m3 codes [T][d] and their scales [T][d/128]
 int permute_e4m3_launch(const uint8_t* codes, const float* scales, const int32_t* row_of, int T,
                         int k, int d, uint8_t* dst_codes, float* dst_scales, hipStream_t s);

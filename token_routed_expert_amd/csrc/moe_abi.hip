@@ -19,6 +19,8 @@ __global__ void fill_offsets_kernel(int32_t* off, int32_t T) {
 int elem_bytes(const moe_shape* sh) { return sh->dtype == MOE_F32 ? 4 : 2; }
 // e4m3 or MXFP8 expert GEMMs (bf16 activations)
 bool is_fp8(const moe_shape* sh) { return sh->dtype == MOE_E4M3 || sh->dtype == MOE_MXFP8; }
+// MXFP4 expert weights (forward only; bf16 x and y)
+bool is_mx4(const moe_shape* sh) { return sh->dtype == MOE_MXFP4 || sh->dtype == MOE_MXFP4_A8; }
 
 // Shape checks shared by every call.  Returns MOE_OK or an error code.
 int check_shape(const moe_shape* sh) {
@@ -27,9 +29,9 @@ int check_shape(const moe_shape* sh) {
     return MOE_ERR_INVALID;
   if (sh->k > sh->E || sh->reserved != 0) return MOE_ERR_INVALID;
   if (sh->dtype != MOE_F32 && sh->dtype != MOE_BF16 && sh->dtype != MOE_E4M3 &&
-      sh->dtype != MOE_MXFP8)
+      sh->dtype != MOE_MXFP8 && !is_mx4(sh))
     return MOE_ERR_UNSUPPORTED;
-  if (is_fp8(sh) && sh->f_shared != 0) return MOE_ERR_UNSUPPORTED;
+  if ((is_fp8(sh) || is_mx4(sh)) && sh->f_shared != 0) return MOE_ERR_UNSUPPORTED;
   if (sh->E > kMaxE) return MOE_ERR_UNSUPPORTED;
   if (sh->T * sh->k >= ((int64_t)1 << 31) || sh->d >= (1 << 30) || sh->f >= (1 << 30) ||
       sh->f_shared >= (1 << 30))
@@ -126,6 +128,37 @@ bool weights_ok(const moe_e4m3_weights* w) {
 bool weights_ok(const moe_mx_weights* w) {
   return w && w->W1 && w->W3 && w->W2 && w->W1t && w->W3t && w->W2t && w->W1s && w->W3s &&
          w->W2s && w->W1ts && w->W3ts && w->W2ts;
+}
+
+// MXFP4: the quantised h, codes and scale bytes
+struct Mx4Ws {
+  uint8_t *hq, *hs;
+};
+Mx4Ws carve_mx4(const moe_shape* sh, void* ws, size_t* bytes) {
+  const size_t P = (size_t)(sh->T * sh->k), f = (size_t)sh->f;
+  Carver c{(char*)ws};
+  Mx4Ws w;
+  w.hq = c.take<uint8_t>(sh->dtype == MOE_MXFP4 ? P * f / 2 : P * f);
+  w.hs = c.take<uint8_t>(P * (f / 32));
+  *bytes = c.used;
+  return w;
+}
+size_t mx4_ws_bytes(const moe_shape* sh) {
+  size_t b;
+  carve_mx4(sh, nullptr, &b);
+  return b;
+}
+bool weights_ok(const moe_mx4_weights* w) { return w && w->W13 && w->W2 && w->W13s && w->W2s; }
+// MXFP4 products: 128-wide scale groups, 32-bit byte offsets into the rows of
+// one operand (a row past an expert's end is given an offset past that range)
+// and into one expert's matrix
+int check_mx4_dims(const moe_shape* sh) {
+  if (!is_mx4(sh)) return MOE_ERR_INVALID;
+  if (sh->d % 128 != 0 || sh->f % 128 != 0) return MOE_ERR_UNSUPPORTED;
+  const int64_t lim = (int64_t)1 << 31;
+  if (sh->T * sh->k * std::max(sh->d, sh->f) >= lim - 4096 || sh->d * sh->f >= lim)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
 }
 
 // The weight operands of the fp8 products: codes in both orientations and
@@ -232,6 +265,8 @@ int bwd_sequence(const moe_shape* sh, GemmArgs a, hipStream_t s) {
   return run_gemm(sh, OP_FC1_WGRAD, a, s);
 }
 
+int layer_fwd_mx4(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t ws_bytes,
+                  void* stream);
 int layer_fwd_e4m3(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t ws_bytes,
                    void* stream);
 int layer_bwd_e4m3(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t ws_bytes,
@@ -374,6 +409,15 @@ size_t moe_workspace_bytes(const moe_shape* sh, int kind) {
     }
     return 0;
   }
+  if (is_mx4(sh)) {
+    switch (kind) {
+      case MOE_WS_AUX_LOSS: return aux_ws_bytes(sh->T, sh->E);
+      case MOE_WS_PERMUTE: return permute_ws_bytes(sh->T, sh->E);
+      case MOE_WS_GEMM_FWD: return mx4_ws_bytes(sh);
+      case MOE_WS_LAYER_FWD: return permute_ws_bytes(sh->T, sh->E) + mx4_ws_bytes(sh);
+    }
+    return 0;
+  }
   switch (kind) {
     case MOE_WS_AUX_LOSS: return aux_ws_bytes(sh->T, sh->E);
     case MOE_WS_PERMUTE: return permute_ws_bytes(sh->T, sh->E);
@@ -456,7 +500,7 @@ int moe_grouped_gemm_fwd(const moe_shape* sh, const int32_t* offsets, const void
   int st = check_shape(sh);
   if (st) return st;
   if ((st = check_gemm_dims(sh, sh->T * sh->k, sh->f))) return st;
-  if (is_fp8(sh)) return MOE_ERR_UNSUPPORTED;  // moe_grouped_gemm_fwd_e4m3 / _mx
+  if (is_fp8(sh) || is_mx4(sh)) return MOE_ERR_UNSUPPORTED;  // moe_grouped_gemm_fwd_e4m3 / _mx / _mx4
   if (!offsets || !xp || !W1 || !W3 || !W2 || !ab || !h || !o) return MOE_ERR_INVALID;
   GemmArgs a = expert_args(sh, offsets);
   a.xp = xp; a.W1 = W1; a.W3 = W3; a.W2 = W2;
@@ -473,7 +517,7 @@ int moe_grouped_gemm_bwd(const moe_shape* sh, const int32_t* offsets, const void
   int st = check_shape(sh);
   if (st) return st;
   if ((st = check_gemm_dims(sh, sh->T * sh->k, sh->f))) return st;
-  if (is_fp8(sh)) return MOE_ERR_UNSUPPORTED;  // moe_grouped_gemm_bwd_e4m3 / _mx
+  if (is_fp8(sh) || is_mx4(sh)) return MOE_ERR_UNSUPPORTED;  // moe_grouped_gemm_bwd_e4m3 / _mx
   if (!offsets || !xp || !ab || !h || !dO || !W1 || !W3 || !W2 || !dab || !dXp || !dW1 || !dW3 ||
       !dW2)
     return MOE_ERR_INVALID;
@@ -847,10 +891,75 @@ int moe_permute_mx(const moe_shape* sh, const uint8_t* codes, const uint8_t* sca
                           row_of, token_of, dst_codes, (float*)dst_scales, ws, ws_bytes, stream);
 }
 
+int moe_quantize_rows_mx4(const void* src, int32_t src_dtype, int64_t rows, int64_t cols,
+                          uint8_t* codes, uint8_t* scales, void* stream) {
+  if (!src || !codes || !scales || rows < 0 || cols < 0) return MOE_ERR_INVALID;
+  if (src_dtype != MOE_BF16 && src_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  // (a block of threads takes 64 scale blocks; the grid stays below 2^31)
+  if (cols % 32 != 0 || rows >= ((int64_t)1 << 40) || cols >= (1 << 30) ||
+      (cols > 0 && rows > ((int64_t)1 << 36) / (cols / 32)))
+    return MOE_ERR_UNSUPPORTED;
+  return quant_rows_mx4_launch(src, src_dtype == MOE_F32, rows, cols, codes, scales,
+                               (hipStream_t)stream);
+}
+
+namespace {
+// E matrices of R x C that the weight quantisers' grids cover
+int check_mx4_matrix(int64_t E, int64_t R, int64_t C, bool pair) {
+  if (E < 0 || R < 0 || C < 0) return MOE_ERR_INVALID;
+  if (R % 128 != 0 || C % 128 != 0) return MOE_ERR_UNSUPPORTED;
+  if (R >= (1 << 30) || C >= (1 << 30) || E > 65535 / (pair ? 2 : 1) || R / 128 > 65535)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+}  // namespace
+
+int moe_quantize_weights_mx4(const void* W, const void* W_pair, int32_t src_dtype, int64_t E,
+                             int64_t R, int64_t C, uint8_t* codes, uint8_t* scales, void* stream) {
+  if (!W || !codes || !scales) return MOE_ERR_INVALID;
+  int st = check_mx4_matrix(E, R, C, W_pair != nullptr);
+  if (st) return st;
+  if (src_dtype != MOE_BF16 && src_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  return quant_weights_mx4_launch(W, W_pair, src_dtype == MOE_F32, E, R, C, codes, scales,
+                                  (hipStream_t)stream);
+}
+
+int moe_dequantize_weights_mx4(const uint8_t* codes, const uint8_t* scales, int64_t E, int64_t R,
+                               int64_t C, void* W, void* W_pair, void* stream) {
+  if (!W || !codes || !scales) return MOE_ERR_INVALID;
+  int st = check_mx4_matrix(E, R, C, W_pair != nullptr);
+  if (st) return st;
+  return dequant_weights_mx4_launch(codes, scales, E, R, C, W, W_pair, (hipStream_t)stream);
+}
+
+int moe_grouped_gemm_fwd_mx4(const moe_shape* sh, const int32_t* offsets, const int32_t* token_of,
+                             const uint8_t* xq, const uint8_t* xs, const moe_mx4_weights* w,
+                             void* o, void* ws, size_t ws_bytes, void* stream) {
+  int st = check_shape(sh);
+  if (st) return st;
+  if ((st = check_mx4_dims(sh))) return st;
+  if (!offsets || !xq || !xs || !weights_ok(w) || !o) return MOE_ERR_INVALID;
+  size_t need;
+  const Mx4Ws W = carve_mx4(sh, ws, &need);
+  if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  const bool a8 = sh->dtype == MOE_MXFP4_A8;
+  Mx4Args a = {};
+  a.offsets = offsets; a.token_of = token_of;
+  a.E = (int)sh->E; a.d = (int)sh->d; a.f = (int)sh->f; a.P = (int)(sh->T * sh->k); a.T = (int)sh->T;
+  a.a = xq; a.as = xs; a.w = w->W13; a.ws = w->W13s;
+  a.hq = W.hq; a.hs = W.hs;
+  if ((st = gemm_mx4_launch(1, a8, a, (hipStream_t)stream))) return st;
+  a.token_of = nullptr;
+  a.a = W.hq; a.as = W.hs; a.w = w->W2; a.ws = w->W2s;
+  a.o = o;
+  return gemm_mx4_launch(2, a8, a, (hipStream_t)stream);
+}
+
 int moe_layer_fwd(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t ws_bytes,
                   void* stream) {
   int st = check_shape(sh);
   if (st) return st;
+  if (is_mx4(sh)) return layer_fwd_mx4(sh, io, ws, ws_bytes, stream);
   if (is_fp8(sh)) return layer_fwd_e4m3(sh, io, ws, ws_bytes, stream);
   if (io && io->memory_efficient) return layer_fwd_rowscaled(sh, io, ws, ws_bytes, stream);
   if ((st = check_gemm_dims(sh, sh->T * sh->k, sh->f))) return st;
@@ -898,6 +1007,7 @@ int moe_layer_bwd(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t 
                   void* stream) {
   int st = check_shape(sh);
   if (st) return st;
+  if (is_mx4(sh)) return MOE_ERR_UNSUPPORTED;
   if (is_fp8(sh)) return layer_bwd_e4m3(sh, io, ws, ws_bytes, stream);
   if (io && io->memory_efficient) return layer_bwd_rowscaled(sh, io, ws, ws_bytes, stream);
   if ((st = check_gemm_dims(sh, sh->T * sh->k, sh->f))) return st;
@@ -942,6 +1052,35 @@ int moe_layer_bwd(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t 
 }  // extern "C"
 
 namespace {
+
+// MXFP4 layers: x is quantised once per token and read through the map
+int layer_fwd_mx4(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t ws_bytes,
+                  void* stream) {
+  int st;
+  if ((st = check_mx4_dims(sh))) return st;
+  if (!io || !weights_ok(io->wmx4)) return MOE_ERR_INVALID;
+  if (!io->logits || !io->x || !io->topk_idx || !io->topk_prob || !io->counts || !io->offsets ||
+      !io->row_of || !io->token_of || !io->xq || !io->xs || !io->o || !io->y)
+    return MOE_ERR_INVALID;
+  if (io->memory_efficient) return MOE_ERR_UNSUPPORTED;
+  const size_t pws = permute_ws_bytes(sh->T, sh->E);
+  const size_t gws = mx4_ws_bytes(sh);
+  if (!ws || ws_bytes < pws + gws || !aux_ws_ok(sh, io, ws_bytes)) return MOE_ERR_WORKSPACE;
+  if ((st = layer_route(sh, io, ws, ws_bytes, stream))) return st;
+  if ((st = moe_permute(sh, nullptr, io->topk_idx, nullptr, 1, io->counts, io->offsets, io->row_of,
+                        io->token_of, nullptr, ws, pws, stream)))
+    return st;
+  if ((st = layer_aux_loss(sh, io, ws, ws_bytes, stream))) return st;
+  uint8_t* xs = (uint8_t*)io->xs;
+  if ((st = (sh->dtype == MOE_MXFP4
+                 ? moe_quantize_rows_mx4(io->x, MOE_BF16, sh->T, sh->d, io->xq, xs, stream)
+                 : moe_quantize_rows_mx(io->x, MOE_BF16, sh->T, sh->d, io->xq, xs, stream))))
+    return st;
+  if ((st = moe_grouped_gemm_fwd_mx4(sh, io->offsets, io->token_of, io->xq, xs, io->wmx4, io->o,
+                                     (char*)ws + pws, gws, stream)))
+    return st;
+  return moe_unpermute(sh, io->o, io->row_of, io->topk_prob, nullptr, io->y, stream);
+}
 
 // e4m3 and MXFP8 layers
 int layer_fwd_e4m3(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t ws_bytes,

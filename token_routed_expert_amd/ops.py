@@ -48,7 +48,8 @@ def _check(status, call):
 
 
 def make_shape(T, d, E, k, f, f_shared=0, dtype="bf16") -> N.moe_shape:
-    code = {"f32": N.MOE_F32, "bf16": N.MOE_BF16, "e4m3": N.MOE_E4M3, "mxfp8": N.MOE_MXFP8}[dtype]
+    code = {"f32": N.MOE_F32, "bf16": N.MOE_BF16, "e4m3": N.MOE_E4M3, "mxfp8": N.MOE_MXFP8,
+            "mxfp4": N.MOE_MXFP4, "mxfp4_a8": N.MOE_MXFP4_A8}[dtype]
     return N.moe_shape(int(T), int(d), int(E), int(k), int(f), int(f_shared), code, 0)
 
 
@@ -283,6 +284,61 @@ def moe_grouped_gemm_bwd_mx(sh, offsets, token_of, x, ab, h, dO, w: MXWeights, d
            "moe_grouped_gemm_bwd_mx")
 
 
+_SRC_DTYPE = {torch.bfloat16: N.MOE_BF16, torch.float32: N.MOE_F32}
+
+
+def moe_quantize_rows_mx4(src, codes, scales, stream=None):
+    """1 x 32 MXFP4 blocks along the rows of a bf16 or fp32 matrix: packed codes
+    [rows][cols/2], E8M0 scale bytes [rows][cols/32]."""
+    rows, cols = src.shape
+    _check(N.lib().moe_quantize_rows_mx4(_ptr(src), _SRC_DTYPE[src.dtype], rows, cols,
+                                         _ptr(codes, U8), _ptr(scales, U8), _stream(stream)),
+           "moe_quantize_rows_mx4")
+
+
+def moe_quantize_weights_mx4(W, W_pair, codes, scales, stream=None):
+    """MXFP4 tiles of bf16 or fp32 matrices W [E][R][C]; W_pair (or None): a second
+    matrix whose 16-column groups alternate with W's."""
+    E, R, Cc = W.shape
+    if W_pair is not None and (W_pair.shape != W.shape or W_pair.dtype != W.dtype):
+        raise ValueError("W_pair must have W's shape and dtype")
+    _check(N.lib().moe_quantize_weights_mx4(_ptr(W), _ptr(W_pair), _SRC_DTYPE[W.dtype], E, R, Cc,
+                                            _ptr(codes, U8), _ptr(scales, U8), _stream(stream)),
+           "moe_quantize_weights_mx4")
+
+
+def moe_dequantize_weights_mx4(codes, scales, W, W_pair=None, stream=None):
+    """The bf16 values W [E][R][C] (and W_pair) that MXFP4 tiles stand for."""
+    E, R, Cc = W.shape
+    if W_pair is not None and W_pair.shape != W.shape:
+        raise ValueError("W_pair must have W's shape")
+    _check(N.lib().moe_dequantize_weights_mx4(_ptr(codes, U8), _ptr(scales, U8), E, R, Cc,
+                                              _ptr(W, torch.bfloat16), _ptr(W_pair, torch.bfloat16),
+                                              _stream(stream)), "moe_dequantize_weights_mx4")
+
+
+class MX4Weights:
+    """The moe_mx4_weights struct over torch tensors (kept alive here)."""
+
+    NAMES = ("W13", "W2", "W13s", "W2s")
+
+    def __init__(self, tensors: dict):
+        self.tensors = {n: tensors[n] for n in self.NAMES}
+        self.struct = N.moe_mx4_weights(*[_ptr(self.tensors[n], U8).value for n in self.NAMES])
+
+    def __getitem__(self, name):
+        return self.tensors[name]
+
+
+def moe_grouped_gemm_fwd_mx4(sh, offsets, token_of, xq, xs, w: MX4Weights, o, ws, stream=None):
+    """The experts' forward with MXFP4 weights on quantised rows (row r is row
+    token_of[r] of xq, or row r when token_of is None); o [P][d] bf16."""
+    _check(N.lib().moe_grouped_gemm_fwd_mx4(C.byref(sh), _ptr(offsets, I32), _ptr(token_of, I32),
+                                            _ptr(xq, U8), _ptr(xs, U8), C.byref(w.struct),
+                                            _ptr(o, torch.bfloat16), _ptr(ws), _nbytes(ws),
+                                            _stream(stream)), "moe_grouped_gemm_fwd_mx4")
+
+
 def _io(buffers: dict) -> N.moe_layer_io:
     io = N.moe_layer_io()
     for name in N.IO_FIELDS:
@@ -294,6 +350,9 @@ def _io(buffers: dict) -> N.moe_layer_io:
     wmx = buffers.get("wmx")
     if wmx is not None:
         io.wmx = C.cast(C.pointer(wmx.struct), C.c_void_p).value
+    wmx4 = buffers.get("wmx4")
+    if wmx4 is not None:
+        io.wmx4 = C.cast(C.pointer(wmx4.struct), C.c_void_p).value
     io.aux_alpha = float(buffers.get("aux_alpha", 0.0))
     io.memory_efficient = int(buffers.get("memory_efficient", 0))
     io.fused_permute = int(buffers.get("fused_permute", 0))
