@@ -292,6 +292,11 @@ typedef struct {
      the quantised weights; xq holds the codes of x ([T][d/2], MXFP4_A8 [T][d])
      and xs its scale bytes [T][d/32].  xp, xpq, xps, ab and h are not used */
   const struct moe_mx4_weights* wmx4;
+  /* 8-bit checkpoint (bf16 layers, memory_efficient == 3): as
+     memory_efficient == 2, with [a|b] kept as E4M3 codes ab_q [P][2f] and E8M0
+     bytes ab_s [P][2f/32] between forward and backward; ab is not used */
+  uint8_t* ab_q;
+  uint8_t* ab_s;
 } moe_layer_io;
 
 /*
@@ -560,6 +565,46 @@ int moe_grouped_gemm_bwd_rowscaled(const moe_shape* sh, const int32_t* offsets, 
                                    const float* row_prob, void* dab, void* dXp, void* dW1,
                                    void* dW3, void* dW2, const int32_t* row_of, float* dprob,
                                    void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * 8-bit activation checkpoints
+ * ----------------------------
+ * The pages hold activations in 8 bits to save training memory (German summary,
+ * section 2 B and results; French summary, section 2 E) without a recipe.  What
+ * the experts' backward keeps from the forward besides its inputs is [a|b]
+ * (h is recomputed).  Here it is kept as E4M3 codes with one E8M0 scale byte per
+ * 32 columns of a row (the block rule of "MXFP8 expert GEMMs" with s at least
+ * -126; a block with a NaN or an infinity has scale byte 255 and reads back as
+ * NaN): 33/32 bytes a value in place of 2.  The forward's own results do not
+ * change: h is computed from the unrounded fp32 a and b, o as in
+ * moe_grouped_gemm_fwd_rowscaled, bit for bit.  The backward is that of
+ * moe_grouped_gemm_bwd_rowscaled with recompute_h at the a and b that read back.
+ *
+ * moe_grouped_gemm_fwd_ckpt8 -- row-scaled expert forward (probabilities before
+ * W2) that writes abq uint8 [P][2f] and abs uint8 [P][2f/32] in place of ab.
+ * x: row r is row token_of[r] of x [T][d], or, token_of NULL, row r of the
+ * permuted x [P][d].  h [P][f] is scratch (it need not be kept).
+ */
+int moe_grouped_gemm_fwd_ckpt8(const moe_shape* sh, const int32_t* offsets,
+                               const int32_t* token_of, const void* x, const void* W1,
+                               const void* W3, const void* W2, const float* row_prob,
+                               uint8_t* abq, uint8_t* abs, void* h, void* o, void* stream);
+
+/*
+ * moe_grouped_gemm_bwd_ckpt8 -- its backward from abq, abs and the unscaled
+ * permuted upstream gradient dO [P][d]: h [P][f] is filled with p silu(a) b,
+ * outputs dab [P][2f], dXp, dW1, dW3, dW2 and (not NULL) dprob as
+ * moe_grouped_gemm_bwd_rowscaled (row_of NULL: [P] in row order, else [T][k]).
+ * ws_bytes >= moe_workspace_bytes(sh, MOE_WS_GEMM_BWD_ROWSCALED).  Both calls:
+ * bf16 only (MOE_ERR_UNSUPPORTED else), limits as moe_grouped_gemm_fwd / _bwd
+ * and, with token_of, moe_grouped_gemm_fwd_gather.
+ */
+int moe_grouped_gemm_bwd_ckpt8(const moe_shape* sh, const int32_t* offsets,
+                               const int32_t* token_of, const void* x, const uint8_t* abq,
+                               const uint8_t* abs, const void* dO, const void* W1, const void* W3,
+                               const void* W2, const float* row_prob, void* h, void* dab, void* dXp,
+                               void* dW1, void* dW3, void* dW2, const int32_t* row_of,
+                               float* dprob, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * MXFP8 expert GEMMs

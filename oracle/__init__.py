@@ -22,3 +22,4 @@ from .moe_e4m3 import *  # noqa: F401,F403
 from .router import *  # noqa: F401,F403
 from .mx import *  # noqa: F401,F403
 from .mx4 import *  # noqa: F401,F403
+from .ckpt8 import *  # noqa: F401,F403

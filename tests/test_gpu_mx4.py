@@ -21,7 +21,7 @@ import torch
 
 import oracle
 from moe_workloads import Workload, make_inputs, to_f64
-from oracle.moe import sigmoid, silu
+from oracle.moe import silu
 
 from gpu_common import announce, need_gpu
 

@@ -41,10 +41,12 @@ class moe_layer_io(C.Structure):
     _fields_ = ([(n, C.c_void_p) for n in _IO_FIELDS + _IO_FIELDS_E4M3 + _IO_FIELDS_ROUTER]
                 + [("aux_alpha", C.c_float), ("row_prob", C.c_void_p),
                    ("memory_efficient", C.c_int32), ("wmx", C.c_void_p),
-                   ("fused_permute", C.c_int32), ("wmx4", C.c_void_p)])
+                   ("fused_permute", C.c_int32), ("wmx4", C.c_void_p),
+                   ("ab_q", C.c_void_p), ("ab_s", C.c_void_p)])
 
 
-IO_FIELDS = tuple(_IO_FIELDS + _IO_FIELDS_E4M3[1:] + _IO_FIELDS_ROUTER + ["row_prob"])
+IO_FIELDS = tuple(_IO_FIELDS + _IO_FIELDS_E4M3[1:] + _IO_FIELDS_ROUTER
+                  + ["row_prob", "ab_q", "ab_s"])
 
 
 class moe_mx4_weights(C.Structure):
@@ -101,6 +103,8 @@ _PROTOS = {
     "moe_grouped_gemm_bwd_mx": (C.c_int, [_SH, _P, _P, _P, _P, _P, _P,
                                           C.POINTER(moe_mx_weights), _P, _P, _P, _P, _P, _P,
                                           C.c_size_t, _P]),
+    "moe_grouped_gemm_fwd_ckpt8": (C.c_int, [_SH] + [_P] * 12),
+    "moe_grouped_gemm_bwd_ckpt8": (C.c_int, [_SH] + [_P] * 19 + [C.c_size_t, _P]),
     "moe_quantize_rows_mx4": (C.c_int, [_P, C.c_int32, _I64, _I64, _P, _P, _P]),
     "moe_quantize_weights_mx4": (C.c_int, [_P, _P, C.c_int32, _I64, _I64, _I64, _P, _P, _P]),
     "moe_dequantize_weights_mx4": (C.c_int, [_P, _P, _I64, _I64, _I64, _P, _P, _P]),

@@ -17,7 +17,8 @@ def layer_buffers(T, d, E, k, f, f_shared=0, dtype="bf16", device="cuda", inputs
     router_grad: also the load-balancing loss (coefficient aux_alpha) and the
     router gradient (aux_loss, dprob, dlogits).
     memory_efficient: probabilities applied before W2 (row_prob [P]);
-    2 also recomputes h in the backward.
+    2 also recomputes h in the backward; 3 (bf16) also keeps [a|b] in 8 bits
+    (ab_q, ab_s in place of ab).
     fused_permute: the experts read x through token_of; no xp buffer.
     Returns (shape, buffers, ws_fwd, ws_bwd).
     """
@@ -72,6 +73,9 @@ def layer_buffers(T, d, E, k, f, f_shared=0, dtype="bf16", device="cuda", inputs
     if memory_efficient:
         b.update(row_prob=z(P, dtype=torch.float32), memory_efficient=int(memory_efficient))
         bwd_kind = N.MOE_WS_LAYER_BWD_ROWSCALED
+        if memory_efficient == 3:
+            b.pop("ab")
+            b.update(ab_q=z(P, 2 * f, dtype=torch.uint8), ab_s=z(P, 2 * f // 32, dtype=torch.uint8))
     ws_b = torch.empty(max(256, moe_workspace_bytes(sh, bwd_kind)), dtype=torch.uint8,
                        device=device)
     return sh, b, ws_f, ws_b

@@ -126,7 +126,10 @@ __device__ __forceinline__ bf16x8_t lds_tr_pair(const char* p) {
 // reads the ids of stage kt + 3 at the top of stage kt, where they have
 // landed, and turns them into the lane offsets of that stage's A loads after
 // the stage's barrier, so the read's latency hides under the MFMAs between.
-template <int OP, int NW, bool RS, bool GATHER = false>
+//
+// CK: the row-scaled products that write (fc1 forward) or read (fc2 dgrad) the
+// pre-activations in 8 bits; only the epilogue differs (store_tile).
+template <int OP, int NW, bool RS, bool GATHER = false, bool CK = false>
 __global__ __launch_bounds__(NW * 64, 1) void gemm_bf16_kernel(GemmArgs args, int NT, int MT) {
   constexpr int WAVES_N = NW / 2;
   constexpr int WM = BM / 2, WN = BN / WAVES_N;  // wavefront sub-tile
@@ -630,7 +633,7 @@ __global__ __launch_bounds__(NW * 64, 1) void gemm_bf16_kernel(GemmArgs args, in
     // budget (fc1 dgrad's would spill); measured on the Qwen3 shape: fc1 and
     // fc2 weight gradients 3-4 % faster, fc2 forward 1.6 %
     constexpr bool kLines = FN == 4 && (OP == OP_FC2_FWD || OP == OP_FC2_WGRAD || OP == OP_FC1_WGRAD);
-    store_tile<OP, FM, FN, WM, WN, TR::ragged_m, RS, kLines>(args, acc, ti, TR::ragged_m ? ti.rows : Mfix,
+    store_tile<OP, FM, FN, WM, WN, TR::ragged_m, RS, kLines, CK>(args, acc, ti, TR::ragged_m ? ti.rows : Mfix,
                                                                N, wm, wn, lane, dp_red);
     if (!have_next) break;
     if (cross) {
@@ -705,12 +708,15 @@ int launch(const GemmArgs& a, hipStream_t s) {
   // gathered fc1 operand (fc1 forward and fc1 weight gradient)
   const unsigned g = (unsigned)grid;
   if constexpr (OP == OP_FC1_FWD) {
-    if (a.gather && a.row_prob) gemm_bf16_kernel<OP, NW, true, true><<<g, NW * 64, 0, s>>>(a, NT, MT);
+    if (a.ck_q && a.gather) gemm_bf16_kernel<OP, NW, true, true, true><<<g, NW * 64, 0, s>>>(a, NT, MT);
+    else if (a.ck_q) gemm_bf16_kernel<OP, NW, true, false, true><<<g, NW * 64, 0, s>>>(a, NT, MT);
+    else if (a.gather && a.row_prob) gemm_bf16_kernel<OP, NW, true, true><<<g, NW * 64, 0, s>>>(a, NT, MT);
     else if (a.gather) gemm_bf16_kernel<OP, NW, false, true><<<g, NW * 64, 0, s>>>(a, NT, MT);
     else if (a.row_prob) gemm_bf16_kernel<OP, NW, true><<<g, NW * 64, 0, s>>>(a, NT, MT);
     else gemm_bf16_kernel<OP, NW, false><<<g, NW * 64, 0, s>>>(a, NT, MT);
   } else if constexpr (OP == OP_FC2_DGRAD) {
-    if (a.row_prob) gemm_bf16_kernel<OP, NW, true><<<g, NW * 64, 0, s>>>(a, NT, MT);
+    if (a.ck_q) gemm_bf16_kernel<OP, NW, true, false, true><<<g, NW * 64, 0, s>>>(a, NT, MT);
+    else if (a.row_prob) gemm_bf16_kernel<OP, NW, true><<<g, NW * 64, 0, s>>>(a, NT, MT);
     else gemm_bf16_kernel<OP, NW, false><<<g, NW * 64, 0, s>>>(a, NT, MT);
   } else if constexpr (OP == OP_FC1_WGRAD) {
     if (a.gather) gemm_bf16_kernel<OP, NW, false, true><<<g, NW * 64, 0, s>>>(a, NT, MT);

@@ -5,6 +5,7 @@
 
 #include "common.h"
 #include "internal.h"
+#include "mx4.h"
 #include "schedule.h"
 
 namespace tre {
@@ -132,6 +133,49 @@ __device__ __forceinline__ void pair_f32(f32x4_t& x, f32x4_t& y) {
   }
 }
 
+// Largest v over the four lanes that hold one row (lanes l, l ^ 16, l ^ 32, l ^ 48).
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+  uint32_t x = v, y = v;
+  swap16(x, y);
+  x = max(x, y);
+  const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  return max((uint32_t)r[0], (uint32_t)r[1]);
+}
+
+// The 8-bit checkpoint of one 32-column block of 16 rows: v = the lane's 8
+// consecutive columns (four lanes hold a row's block) -> E4M3 codes at q and,
+// from the lanes `first`, the block's E8M0 byte at sc.  `ok`: the row exists.
+__device__ __forceinline__ void store_ckpt(const f32x4_t& x, const f32x4_t& y, bool ok, bool first,
+                                           uint8_t* q, uint8_t* sc) {
+  float v[8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = x[i];
+    v[4 + i] = y[i];
+    m = max(m, max(mx::mag(x[i]), mx::mag(y[i])));
+  }
+  const uint32_t b = mx::scale_byte<false>(row_max(m));
+  const float inv = mx::inv_scale_of(b == mx::kNanScale ? 127u : b);
+  const uint32_t lo = mx::pack4_fp8(v, inv), hi = mx::pack4_fp8(v + 4, inv);
+  if (!ok) return;
+  *(uint2*)q = make_uint2(lo, hi);
+  if (first) *sc = (uint8_t)b;
+}
+// Eight values back from their codes and scale byte.
+__device__ __forceinline__ void load_ckpt(const uint8_t* q, const uint8_t* sc, float* v) {
+  const uint2 w = *(const uint2*)q;
+  const float s = mx::scale_any(*sc);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int u = (int)(i == 0 ? w.x : w.y);
+    const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8(u, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(u, true);
+    v[4 * i] = a[0] * s;
+    v[4 * i + 1] = a[1] * s;
+    v[4 * i + 2] = b[0] * s;
+    v[4 * i + 3] = b[1] * s;
+  }
+}
 
 // Writes a wavefront's FM x FN accumulator fragments (16x16 each, the
 // wavefront covering rows wm*WM.. and columns wn*WN.. of the block tile) as
@@ -155,7 +199,14 @@ __device__ __forceinline__ void pair_f32(f32x4_t& x, f32x4_t& y) {
 // 128-byte line of a bf16 row): lanes l and l + 8 of each row of 16 lanes
 // trade pair halves (one DPP rotate per dword), so that each store
 // instruction writes whole lines of 8 rows instead of half lines of 16 rows.
-template <int OP, int FM, int FN, int WM, int WN, bool RAGGED, bool RS = false, bool LINES = false>
+//
+// CK (row-scaled fc1 forward and fc2 dgrad): the pre-activations [a|b] are kept
+// in 8 bits (args.ck_q, args.ck_s; a 32-column fragment pair of a row is one
+// scale block, held by four lanes).  The forward rounds them from the fp32
+// accumulators, h stays that of the unrounded a and b; the backward takes a and
+// b as they read back, for the recomputed h too.
+template <int OP, int FM, int FN, int WM, int WN, bool RAGGED, bool RS = false, bool LINES = false,
+          bool CK = false>
 __device__ __forceinline__ void store_tile(const GemmArgs& args, const f32x4_t (&acc)[FM][FN],
                                            const TileInfo& ti, int M, int N, int wm, int wn,
                                            int lane, float* red = nullptr) {
@@ -175,7 +226,31 @@ __device__ __forceinline__ void store_tile(const GemmArgs& args, const f32x4_t (
     const bool row_ok = RAGGED ? (m < ti.rows) : (ti.m0 + m < M);
     float pr = 1.0f, dp = 0.0f;            // RS: the row's probability, <h, dh'> partial
     if constexpr (RS) pr = row_ok ? args.row_prob[ti.row0 + m] : 0.0f;
-    if constexpr (OP == OP_FC1_FWD) {
+    if constexpr (OP == OP_FC1_FWD && CK) {
+      static_for<0, HB / 2>([&](auto JP) __attribute__((always_inline)) {
+        constexpr int j0 = 2 * JP.value;
+        f32x4_t a0 = acc[i][j0], a1 = acc[i][j0 + 1];
+        f32x4_t b0v = acc[i][j0 + HB], b1v = acc[i][j0 + HB + 1];
+        pair_f32(a0, a1);   // a at columns pc + 0..3 (a0), pc + 4..7 (a1)
+        pair_f32(b0v, b1v);
+        f32x4_t h0, h1;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          h0[q] = silu_f32(a0[q]) * b0v[q] * pr;
+          h1[q] = silu_f32(a1[q]) * b1v[q] * pr;
+        }
+        const int blk = ti.n0 / 2 + (wn * HB + j0) * 16;  // first column of the block
+        const size_t row = (size_t)(ti.row0 + m);
+        uint8_t* cq = args.ck_q + row * (2 * (size_t)f) + blk + pc;
+        uint8_t* cs = args.ck_s + row * (size_t)(f / 16) + blk / 32;
+        store_ckpt(a0, a1, row_ok, lane < 16, cq, cs);
+        store_ckpt(b0v, b1v, row_ok, lane < 16, cq + f, cs + f / 32);
+        if (row_ok)
+          *(u32x4_t*)((bf16_t*)args.h_out + row * (size_t)f + blk + pc) =
+              u32x4_t{pack_bf16x2(h0[0], h0[1]), pack_bf16x2(h0[2], h0[3]),
+                      pack_bf16x2(h1[0], h1[1]), pack_bf16x2(h1[2], h1[3])};
+      });
+    } else if constexpr (OP == OP_FC1_FWD) {
       // pairs jp < HB/2 hold W1 columns (a), pair jp + HB/2 the same W3 columns (b)
       static_for<0, HB / 2>([&](auto JP) __attribute__((always_inline)) {
         constexpr int j0 = 2 * JP.value;
@@ -249,15 +324,30 @@ __device__ __forceinline__ void store_tile(const GemmArgs& args, const f32x4_t (
             pair_f32(x, y);  // dh at columns col + 0..3 (x), col + 4..7 (y)
             if (row_ok) {
               const size_t row = (size_t)(ti.row0 + m);
-              const bf16_t* abr = (const bf16_t*)args.ab + row * (2 * (size_t)f);
-              const u32x4_t av = *(const u32x4_t*)(abr + col);
-              const u32x4_t bv = *(const u32x4_t*)(abr + f + col);
+              u32x4_t av, bv;
+              float ac[8], bc[8];
+              if constexpr (CK) {
+                const uint8_t* cq = args.ck_q + row * (2 * (size_t)f) + col;
+                const uint8_t* cs = args.ck_s + row * (size_t)(f / 16) + col0 / 32;
+                load_ckpt(cq, cs, ac);
+                load_ckpt(cq + f, cs + f / 32, bc);
+              } else {
+                const bf16_t* abr = (const bf16_t*)args.ab + row * (2 * (size_t)f);
+                av = *(const u32x4_t*)(abr + col);
+                bv = *(const u32x4_t*)(abr + f + col);
+              }
               float da[8], db[8], hr[8];
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
-                const uint32_t aw = av[q >> 1], bw = bv[q >> 1];
-                const float aq = (q & 1) ? hi_bf16(aw) : lo_bf16(aw);
-                const float bq = (q & 1) ? hi_bf16(bw) : lo_bf16(bw);
+                float aq, bq;
+                if constexpr (CK) {
+                  aq = ac[q];
+                  bq = bc[q];
+                } else {
+                  const uint32_t aw = av[q >> 1], bw = bv[q >> 1];
+                  aq = (q & 1) ? hi_bf16(aw) : lo_bf16(aw);
+                  bq = (q & 1) ? hi_bf16(bw) : lo_bf16(bw);
+                }
                 float c = q < 4 ? x[q] : y[q - 4];
                 const float sg = sigmoid_f32(aq);
                 if constexpr (RS) {

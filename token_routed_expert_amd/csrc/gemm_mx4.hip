@@ -20,7 +20,6 @@
 // to the format fc2 reads, and neither a, b nor an unquantised h leaves the
 // registers.
 #include "gemm_common.h"
-#include "mx4.h"
 
 namespace tre {
 
@@ -36,15 +35,6 @@ __device__ __forceinline__ f32x4_t mma(const i32x4_t& w, const i32x8_t& x, const
                                        int xs) {
   const i32x8_t w8 = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, x, c, 4, A8 ? 0 : 4, WSEL, ws, 0, xs);
-}
-
-// Largest v over the four lanes that hold one row (lanes l, l ^ 16, l ^ 32, l ^ 48).
-__device__ __forceinline__ uint32_t row_max(uint32_t v) {
-  uint32_t x = v, y = v;
-  swap16(x, y);
-  x = max(x, y);
-  const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-  return max((uint32_t)r[0], (uint32_t)r[1]);
 }
 
 // Epilogue of fc1 for one 16-row fragment: acc = [a0 b0 a1 b1] (16 columns of

@@ -114,6 +114,11 @@ struct GemmArgs {
   const int32_t* gather;
   const void* gx;
   int gT;
+  // 8-bit checkpoint of [a|b] (bf16 row-scaled fc1 forward writes it in place of
+  // ab_out, fc2 dgrad reads it in place of ab): E4M3 codes [P][2f] and E8M0
+  // bytes [P][2f/32]
+  uint8_t* ck_q;
+  uint8_t* ck_s;
 };
 
 // gemm_bf16.hip: MFMA kernels, bf16 in/out, fp32 accumulation

@@ -285,11 +285,21 @@ size_t dp_part_bytes(const moe_shape* sh) {
   return align_up((size_t)(sh->T * sh->k) * (size_t)((sh->f + 255) / 256) * sizeof(float), 256);
 }
 int layer_combine_bwd(const moe_shape* sh, const moe_layer_io* io, void* stream);
+// [a|b] between forward and backward: bf16, or the 8-bit checkpoint (q, s)
+struct SavedAb {
+  void* ab;
+  uint8_t *q, *s;
+};
+SavedAb saved_of(const moe_layer_io* io) {
+  return io->memory_efficient == 3 ? SavedAb{nullptr, io->ab_q, io->ab_s}
+                                   : SavedAb{io->ab, nullptr, nullptr};
+}
+bool saved_ok(const SavedAb& v) { return v.ab || (v.q && v.s); }
 int fwd_rowscaled(const moe_shape* sh, const int32_t* offsets, const RowSrc& rows, const void* W1,
-                  const void* W3, const void* W2, const float* row_prob, void* ab, void* h, void* o,
-                  void* stream);
-int bwd_rowscaled(const moe_shape* sh, const int32_t* offsets, const RowSrc& rows, const void* ab,
-                  void* h, int32_t recompute_h, const void* dO, const void* W1, const void* W3,
+                  const void* W3, const void* W2, const float* row_prob, const SavedAb& ab, void* h,
+                  void* o, void* stream);
+int bwd_rowscaled(const moe_shape* sh, const int32_t* offsets, const RowSrc& rows,
+                  const SavedAb& ab, void* h, int32_t recompute_h, const void* dO, const void* W1, const void* W3,
                   const void* W2, const float* row_prob, void* dab, void* dXp, void* dW1,
                   void* dW3, void* dW2, const int32_t* row_of, float* dprob, void* ws,
                   void* stream);
@@ -581,8 +591,8 @@ int moe_grouped_gemm_fwd_rowscaled(const moe_shape* sh, const int32_t* offsets, 
   if ((st = check_gemm_dims(sh, sh->T * sh->k, sh->f))) return st;
   if (sh->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (!offsets || !xp || !W1 || !W3 || !W2 || !row_prob || !ab || !h || !o) return MOE_ERR_INVALID;
-  return fwd_rowscaled(sh, offsets, RowSrc{xp, nullptr, nullptr}, W1, W3, W2, row_prob, ab, h, o,
-                       stream);
+  return fwd_rowscaled(sh, offsets, RowSrc{xp, nullptr, nullptr}, W1, W3, W2, row_prob,
+                       SavedAb{ab, nullptr, nullptr}, h, o, stream);
 }
 
 int moe_grouped_gemm_bwd_rowscaled(const moe_shape* sh, const int32_t* offsets, const void* xp,
@@ -599,8 +609,46 @@ int moe_grouped_gemm_bwd_rowscaled(const moe_shape* sh, const int32_t* offsets, 
       !dW1 || !dW3 || !dW2)
     return MOE_ERR_INVALID;
   if (!ws || ws_bytes < dp_part_bytes(sh)) return MOE_ERR_WORKSPACE;
-  return bwd_rowscaled(sh, offsets, RowSrc{xp, nullptr, nullptr}, ab, h, recompute_h, dO, W1, W3,
-                       W2, row_prob, dab, dXp, dW1, dW3, dW2, row_of, dprob, ws, stream);
+  return bwd_rowscaled(sh, offsets, RowSrc{xp, nullptr, nullptr},
+                       SavedAb{(void*)ab, nullptr, nullptr}, h, recompute_h, dO, W1, W3, W2,
+                       row_prob, dab, dXp, dW1, dW3, dW2, row_of, dprob, ws, stream);
+}
+
+int moe_grouped_gemm_fwd_ckpt8(const moe_shape* sh, const int32_t* offsets,
+                               const int32_t* token_of, const void* x, const void* W1,
+                               const void* W3, const void* W2, const float* row_prob,
+                               uint8_t* abq, uint8_t* abs, void* h, void* o, void* stream) {
+  int st = check_shape(sh);
+  if (st) return st;
+  if ((st = check_gemm_dims(sh, sh->T * sh->k, sh->f))) return st;
+  if (sh->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (token_of && (st = check_gather(sh))) return st;
+  if (!offsets || !x || !W1 || !W3 || !W2 || !row_prob || !abq || !abs || !h || !o)
+    return MOE_ERR_INVALID;
+  return fwd_rowscaled(sh, offsets,
+                       token_of ? RowSrc{nullptr, token_of, x} : RowSrc{x, nullptr, nullptr}, W1, W3,
+                       W2, row_prob, SavedAb{nullptr, abq, abs}, h, o, stream);
+}
+
+int moe_grouped_gemm_bwd_ckpt8(const moe_shape* sh, const int32_t* offsets,
+                               const int32_t* token_of, const void* x, const uint8_t* abq,
+                               const uint8_t* abs, const void* dO, const void* W1, const void* W3,
+                               const void* W2, const float* row_prob, void* h, void* dab, void* dXp,
+                               void* dW1, void* dW3, void* dW2, const int32_t* row_of,
+                               float* dprob, void* ws, size_t ws_bytes, void* stream) {
+  int st = check_shape(sh);
+  if (st) return st;
+  if ((st = check_gemm_dims(sh, sh->T * sh->k, sh->f))) return st;
+  if (sh->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (token_of && (st = check_gather(sh))) return st;
+  if (!offsets || !x || !abq || !abs || !dO || !W1 || !W3 || !W2 || !row_prob || !h || !dab ||
+      !dXp || !dW1 || !dW3 || !dW2)
+    return MOE_ERR_INVALID;
+  if (!ws || ws_bytes < dp_part_bytes(sh)) return MOE_ERR_WORKSPACE;
+  return bwd_rowscaled(sh, offsets,
+                       token_of ? RowSrc{nullptr, token_of, x} : RowSrc{x, nullptr, nullptr},
+                       SavedAb{nullptr, (uint8_t*)abq, (uint8_t*)abs}, h, 1, dO, W1, W3, W2,
+                       row_prob, dab, dXp, dW1, dW3, dW2, row_of, dprob, ws, stream);
 }
 
 }  // extern "C"
@@ -609,24 +657,26 @@ namespace {
 
 // Row-scaled expert forward and backward (bf16; arguments checked by the caller).
 int fwd_rowscaled(const moe_shape* sh, const int32_t* offsets, const RowSrc& rows, const void* W1,
-                  const void* W3, const void* W2, const float* row_prob, void* ab, void* h, void* o,
-                  void* stream) {
+                  const void* W3, const void* W2, const float* row_prob, const SavedAb& ab, void* h,
+                  void* o, void* stream) {
   GemmArgs a = expert_args(sh, offsets);
   set_rows(a, sh, rows);
   a.W1 = W1; a.W3 = W3; a.W2 = W2; a.row_prob = row_prob;
-  a.ab_out = ab; a.h_out = h; a.h = h; a.o_out = o;
+  a.ab_out = ab.ab; a.ck_q = ab.q; a.ck_s = ab.s;
+  a.h_out = h; a.h = h; a.o_out = o;
   return fwd_sequence(sh, a, (hipStream_t)stream);
 }
 
-int bwd_rowscaled(const moe_shape* sh, const int32_t* offsets, const RowSrc& rows, const void* ab,
-                  void* h, int32_t recompute_h, const void* dO, const void* W1, const void* W3,
+int bwd_rowscaled(const moe_shape* sh, const int32_t* offsets, const RowSrc& rows,
+                  const SavedAb& ab, void* h, int32_t recompute_h, const void* dO, const void* W1, const void* W3,
                   const void* W2, const float* row_prob, void* dab, void* dXp, void* dW1,
                   void* dW3, void* dW2, const int32_t* row_of, float* dprob, void* ws,
                   void* stream) {
   int st;
   GemmArgs a = expert_args(sh, offsets);
   set_rows(a, sh, rows);
-  a.ab = ab; a.h = h; a.dO = dO; a.W1 = W1; a.W3 = W3; a.W2 = W2;
+  a.ab = ab.ab; a.ck_q = ab.q; a.ck_s = ab.s;
+  a.h = h; a.dO = dO; a.W1 = W1; a.W3 = W3; a.W2 = W2;
   a.dab_out = dab; a.dXp_out = dXp; a.dW1 = dW1; a.dW3 = dW3; a.dW2 = dW2;
   a.row_prob = row_prob;
   a.dp_part = (float*)ws;
@@ -636,6 +686,7 @@ int bwd_rowscaled(const moe_shape* sh, const int32_t* offsets, const RowSrc& row
   if ((st = gemm_bf16_launch(OP_FC2_DGRAD, a, s))) return st;
   a.row_prob = nullptr;
   a.h_out = nullptr;
+  a.ck_q = nullptr;
   a.dab = a.dab_out;
   if ((st = gemm_bf16_launch(OP_FC1_DGRAD, a, s))) return st;
   if ((st = gemm_bf16_launch(OP_FC2_WGRAD, a, s))) return st;
@@ -1089,6 +1140,7 @@ int layer_fwd_e4m3(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t
   const bool mx = sh->dtype == MOE_MXFP8;
   if ((st = check_gemm_dims(sh, sh->T * sh->k, sh->f))) return st;
   if (!io || !(mx ? weights_ok(io->wmx) : weights_ok(io->wq))) return MOE_ERR_INVALID;
+  if (io->memory_efficient == 3) return MOE_ERR_UNSUPPORTED;  // the 8-bit checkpoint is bf16
   if (!io->logits || !io->x || !io->topk_idx || !io->topk_prob ||
       !io->counts || !io->offsets || !io->row_of || !io->token_of || !io->xq || !io->xs ||
       !io->xpq || !io->xps || !io->ab || !io->h || !io->o || !io->y)
@@ -1123,6 +1175,7 @@ int layer_bwd_e4m3(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t
   const bool mx = sh->dtype == MOE_MXFP8;
   if ((st = check_gemm_dims(sh, sh->T * sh->k, sh->f))) return st;
   if (!io || !(mx ? weights_ok(io->wmx) : weights_ok(io->wq))) return MOE_ERR_INVALID;
+  if (io->memory_efficient == 3) return MOE_ERR_UNSUPPORTED;  // the 8-bit checkpoint is bf16
   if (!io->dY || !io->x || !io->topk_prob || !io->offsets ||
       !io->row_of || !io->token_of || !io->ab || !io->h || !io->dO || !io->dab || !io->dXp ||
       !io->dX || !io->dW1 || !io->dW3 || !io->dW2)
@@ -1204,7 +1257,8 @@ int layer_fwd_rowscaled(const moe_shape* sh, const moe_layer_io* io, void* ws, s
   if (sh->f_shared && (st = check_gemm_dims(sh, sh->T, sh->f_shared))) return st;
   if (!io->logits || !io->x || !io->W1 || !io->W3 || !io->W2 || !io->topk_idx ||
       !io->topk_prob || !io->counts || !io->offsets || !io->row_of || !io->token_of ||
-      (!io->xp && !io->fused_permute) || !io->ab || !io->h || !io->o || !io->y || !io->row_prob)
+      (!io->xp && !io->fused_permute) || !saved_ok(saved_of(io)) || !io->h || !io->o ||
+      !io->y || !io->row_prob)
     return MOE_ERR_INVALID;
   if (io->fused_permute && (st = check_gather(sh))) return st;
   if (sh->f_shared &&
@@ -1220,7 +1274,7 @@ int layer_fwd_rowscaled(const moe_shape* sh, const moe_layer_io* io, void* ws, s
   if ((st = layer_aux_loss(sh, io, ws, ws_bytes, stream))) return st;
   if ((st = moe_row_probs(sh, io->row_of, io->topk_prob, io->row_prob, stream))) return st;
   if ((st = fwd_rowscaled(sh, io->offsets, rows_of(io), io->W1, io->W3, io->W2, io->row_prob,
-                          io->ab, io->h, io->o, stream)))
+                          saved_of(io), io->h, io->o, stream)))
     return st;
   const void* add = nullptr;
   if (sh->f_shared) {
@@ -1244,7 +1298,8 @@ int layer_bwd_rowscaled(const moe_shape* sh, const moe_layer_io* io, void* ws, s
   if ((st = check_gemm_dims(sh, sh->T * sh->k, sh->f))) return st;
   if (sh->f_shared && (st = check_gemm_dims(sh, sh->T, sh->f_shared))) return st;
   if (!io->dY || !io->W1 || !io->W3 || !io->W2 || !io->offsets || !io->row_of ||
-      !io->ab || !io->h || !io->dO || !io->dab || !io->dXp || !io->dX || !io->dW1 || !io->dW3 ||
+      !saved_ok(saved_of(io)) || !io->h || !io->dO || !io->dab || !io->dXp || !io->dX ||
+      !io->dW1 || !io->dW3 ||
       !io->dW2 || !io->row_prob)
     return MOE_ERR_INVALID;
   if (io->fused_permute ? (!io->token_of || !io->x) : !io->xp) return MOE_ERR_INVALID;
@@ -1263,8 +1318,9 @@ int layer_bwd_rowscaled(const moe_shape* sh, const moe_layer_io* io, void* ws, s
                         io->dO, nullptr, 0, stream)))
     return st;
   // dprob[t][j] too when the router gradient is asked for
-  if ((st = bwd_rowscaled(sh, io->offsets, rows_of(io), io->ab, io->h, io->memory_efficient == 2,
-                          io->dO, io->W1, io->W3, io->W2, io->row_prob, io->dab, io->dXp,
+  if ((st = bwd_rowscaled(sh, io->offsets, rows_of(io), saved_of(io), io->h,
+                          io->memory_efficient == 2 || io->memory_efficient == 3, io->dO, io->W1,
+                          io->W3, io->W2, io->row_prob, io->dab, io->dXp,
                           io->dW1, io->dW3, io->dW2, io->row_of,
                           io->dlogits ? io->dprob : nullptr, dp_part, stream)))
     return st;

@@ -386,6 +386,27 @@ def moe_grouped_gemm_bwd_rowscaled(sh, offsets, xp, ab, h, dO, W1, W3, W2, row_p
         "moe_grouped_gemm_bwd_rowscaled")
 
 
+def moe_grouped_gemm_fwd_ckpt8(sh, offsets, token_of, x, W1, W3, W2, row_prob, abq, abs_, h, o,
+                               stream=None):
+    """The row-scaled expert forward that keeps [a|b] in 8 bits (abq [P][2f] E4M3
+    codes, abs_ [P][2f/32] E8M0 bytes); token_of None: x is already permuted."""
+    _check(N.lib().moe_grouped_gemm_fwd_ckpt8(
+        C.byref(sh), _ptr(offsets, I32), _ptr(token_of, I32), _ptr(x), _ptr(W1), _ptr(W3), _ptr(W2),
+        _ptr(row_prob, F32), _ptr(abq, U8), _ptr(abs_, U8), _ptr(h), _ptr(o), _stream(stream)),
+        "moe_grouped_gemm_fwd_ckpt8")
+
+
+def moe_grouped_gemm_bwd_ckpt8(sh, offsets, token_of, x, abq, abs_, dO, W1, W3, W2, row_prob, h, dab,
+                               dXp, dW1, dW3, dW2, row_of, dprob, ws, stream=None):
+    """Backward of moe_grouped_gemm_fwd_ckpt8 for the unscaled permuted dO; h is
+    refilled from the checkpoint; dprob [P] (row_of None) or [T][k], or None."""
+    _check(N.lib().moe_grouped_gemm_bwd_ckpt8(
+        C.byref(sh), _ptr(offsets, I32), _ptr(token_of, I32), _ptr(x), _ptr(abq, U8), _ptr(abs_, U8),
+        _ptr(dO), _ptr(W1), _ptr(W3), _ptr(W2), _ptr(row_prob, F32), _ptr(h), _ptr(dab), _ptr(dXp),
+        _ptr(dW1), _ptr(dW3), _ptr(dW2), _ptr(row_of, I32), _ptr(dprob, F32), _ptr(ws), _nbytes(ws),
+        _stream(stream)), "moe_grouped_gemm_bwd_ckpt8")
+
+
 def moe_aux_loss(logits, k, counts, alpha, loss, ws, stream=None):
     """Load-balancing loss (device scalar `loss`) from logits [T][E] and counts [E]."""
     T, E = logits.shape
