@@ -202,9 +202,246 @@ int launch_rows(const Mx4Args& a, hipStream_t s) {
   return MOE_OK;
 }
 
+// Many rows per expert: tiles of 128 rows x 256 stored columns, four
+// wavefronts side by side (each all 128 rows x 64 columns, one scale group, as
+// 8 x 4 fragments), two blocks to a compute unit, so that one block's prologue,
+// epilogue and barrier waits run under the other's products.  K advances 128 a
+// stage through an LDS ring of NS stages; every byte of a stage arrives by
+// buffer_load ... lds.  LDS layout of a stage:
+//  * A: 128 rows of 64 (E2M1) or 128 (E4M3) bytes, the 16-byte chunk c of row r
+//    stored at chunk c ^ swz(r), swz(r) = (r >> 1) & 3 or & 7: the 16 rows of a
+//    fragment read then spread over all banks;
+//  * B: the wavefronts' 4 fragments each, 1 KB as stored: a lane reads back its
+//    own 16 bytes;
+//  * scales: one word per A row (its four group bytes; 1 KB, the second half
+//    unused), one per lane and column group for B.
+// A stage's slot is free once every wavefront has its last fragments in
+// registers: with the reads of stage kt done, a wait for stage kt + 1's loads
+// and one barrier, the loads of stage kt + NS go to that slot, spread over the
+// products that follow.
+template <int FC, bool A8>
+__global__ __launch_bounds__(256, 2) void gemm_mx4_tile_kernel(Mx4Args args, int NT) {
+  constexpr int BM = 128, BN = 256, FM = BM / 16;
+  constexpr int NS = A8 ? 2 : 3;
+  constexpr int ARB = A8 ? 128 : 64;            // bytes of an A row and stage
+  constexpr int A_BYTES = BM * ARB, B_BYTES = 16 * 1024, AS_BYTES = 1024, BS_BYTES = 1024;
+  constexpr int STAGE = A_BYTES + B_BYTES + AS_BYTES + BS_BYTES;
+  constexpr int A_PER_WAVE = A_BYTES / 4096;    // 1 KB DMA instructions
+  constexpr int LOADS = A_PER_WAVE + 4 + 2;     // a wavefront's loads of a stage
+  __shared__ __attribute__((aligned(1024))) char lds[NS * STAGE];
+  __shared__ int sched[8];
+  TileInfo ti;
+  if (!decode_ragged_m<BM, 4>(args.offsets, args.E, NT, sched, ti)) return;
+  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+  const int w = uniform((int)threadIdx.x >> 6);
+  const int e = uniform(ti.e), row0 = uniform(ti.row0), rows = uniform(ti.rows);
+  const int n0 = uniform(ti.n0) * BN;
+  const int K = FC == 1 ? args.d : args.f, N = FC == 1 ? 2 * args.f : args.d;
+  const int KT = K >> 7;
+  const uint32_t a_ld = (uint32_t)(A8 ? K : K >> 1), as_ld = (uint32_t)(K >> 5);
+
+  // ---- sources: rows past the expert's end and columns past N read as zero
+  const bool gather = FC == 1 && args.token_of != nullptr;
+  const size_t a_rows = gather ? (size_t)args.T : (size_t)rows, a_first = gather ? 0 : (size_t)row0;
+  const rsrc_t a_src = make_rsrc(args.a + a_first * a_ld, (uint32_t)(a_rows * a_ld));
+  const rsrc_t as_src = make_rsrc(args.as + a_first * as_ld, (uint32_t)(a_rows * as_ld));
+  const uint32_t b_size = (uint32_t)(N >> 4) * (uint32_t)KT * 1024u;
+  const rsrc_t b_src = make_rsrc(args.w + (size_t)e * b_size, b_size);
+  const rsrc_t bs_src = make_rsrc(args.ws + (size_t)e * (b_size / 16), b_size / 16);
+  constexpr uint32_t kPast = 0x80000000u;       // past every range
+  auto row_of = [&](int m) __attribute__((always_inline)) -> uint32_t {  // source row of tile row m
+    return gather ? (uint32_t)args.token_of[row0 + min(m, rows - 1)] : (uint32_t)m;
+  };
+  uint32_t a_off[A_PER_WAVE];
+#pragma unroll
+  for (int q = 0; q < A_PER_WAVE; ++q) {
+    const int t = w * A_PER_WAVE + q;           // instruction t: 1 KB of A rows
+    const int m = A8 ? 8 * t + (lane >> 3) : 16 * t + (lane >> 2);
+    const int c = A8 ? (lane & 7) ^ ((m >> 1) & 7) : (lane & 3) ^ ((m >> 1) & 3);
+    a_off[q] = m < rows ? row_of(m) * a_ld + (uint32_t)c * 16u : kPast;
+  }
+  // A scales: wavefronts 0 and 1 (64 rows each); 2 and 3 issue a load of nothing
+  const uint32_t as_off = w < 2 && 64 * w + lane < rows ? row_of(64 * w + lane) * as_ld : kPast;
+  const uint32_t b_off = ((uint32_t)(n0 >> 4) + 4u * w) * (uint32_t)KT * 1024u + (uint32_t)lane * 16u;
+  const uint32_t bs_off = ((uint32_t)(n0 >> 6) + (uint32_t)w) * (uint32_t)KT * 256u + (uint32_t)lane * 4u;
+
+  const uint32_t lds_base = (uint32_t)uniform((int)(uint32_t)(size_t)LDS_PTR(lds));
+  // load q of stage s (past the last stage: nothing is read, zeros land)
+  auto issue = [&](int s, int slot, auto Q) __attribute__((always_inline)) {
+    constexpr int q = decltype(Q)::value;
+    const uint32_t base = lds_base + (uint32_t)(slot * STAGE);
+    const bool live = s < KT;
+    if constexpr (q < A_PER_WAVE) {
+      rsrc_t src = a_src;
+      src[2] = live ? src[2] : 0;
+      dma16(uniform_rsrc(src), a_off[q] + (uint32_t)(s * ARB), base + (uint32_t)((w * A_PER_WAVE + q) * 1024));
+    } else if constexpr (q < A_PER_WAVE + 4) {
+      constexpr int j = q - A_PER_WAVE;
+      rsrc_t src = b_src;
+      src[2] = live ? src[2] : 0;
+      dma16(uniform_rsrc(src), b_off + (uint32_t)(j * KT + s) * 1024u,
+            base + (uint32_t)(A_BYTES + (4 * w + j) * 1024));
+    } else if constexpr (q == A_PER_WAVE + 4) {
+      rsrc_t src = as_src;
+      src[2] = live ? src[2] : 0;
+      dma4(uniform_rsrc(src), as_off + (uint32_t)(s * 4),
+           base + (uint32_t)(A_BYTES + B_BYTES + w * 256));
+    } else {
+      rsrc_t src = bs_src;
+      src[2] = live ? src[2] : 0;
+      dma4(uniform_rsrc(src), bs_off + (uint32_t)s * 256u,
+           base + (uint32_t)(A_BYTES + B_BYTES + AS_BYTES + w * 256));
+    }
+  };
+
+  // ---- fragments
+  const uint32_t sw = (uint32_t)(r >> 1) & (A8 ? 7u : 3u);
+  const uint32_t a_lo = (uint32_t)r * ARB + (((uint32_t)g ^ sw) << 4);
+  const uint32_t a_hi = (uint32_t)r * ARB + (((uint32_t)(4 + g) ^ sw) << 4);
+  auto ld16 = [&](const char* p) __attribute__((always_inline)) -> i32x4_t {
+    return *(const __attribute__((address_space(3))) i32x4_t*)p;
+  };
+  auto read_a = [&](const char* st, int i) __attribute__((always_inline)) -> i32x8_t {
+    const i32x4_t lo = ld16(st + a_lo + i * 16 * ARB);
+    if constexpr (A8) return __builtin_shufflevector(lo, ld16(st + a_hi + i * 16 * ARB), 0, 1, 2, 3, 4, 5, 6, 7);
+    else return __builtin_shufflevector(lo, i32x4_t{0, 0, 0, 0}, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  auto read_as = [&](const char* st, int i) __attribute__((always_inline)) -> int {
+    return *(const __attribute__((address_space(3))) uint8_t*)(st + A_BYTES + B_BYTES + (16 * i + r) * 4 + g);
+  };
+  auto read_b = [&](const char* st, int j) __attribute__((always_inline)) -> i32x4_t {
+    return ld16(st + A_BYTES + (4 * w + j) * 1024 + lane * 16);
+  };
+  auto read_bs = [&](const char* st) __attribute__((always_inline)) -> int {
+    return *(const __attribute__((address_space(3))) int*)(st + A_BYTES + B_BYTES + AS_BYTES + w * 256 + lane * 4);
+  };
+
+  f32x4_t acc[FM][4];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  static_for<0, NS>([&](auto S) __attribute__((always_inline)) {
+    static_for<0, LOADS>([&](auto Q) __attribute__((always_inline)) { issue(S.value, S.value, Q); });
+  });
+  wait_vmcnt<LOADS * (NS - 1)>();
+  block_barrier();
+
+  i32x8_t xf[4];        // A fragments in flight: i & 3
+  int sx[4];
+  i32x4_t wf[2][4];     // B fragments of the stages of either parity
+  int sw_[2];
+  int slot = 0;
+  {
+    const char* st = lds;
+    static_for<0, 4>([&](auto J) __attribute__((always_inline)) { wf[0][J.value] = read_b(st, J.value); });
+    sw_[0] = read_bs(st);
+    static_for<0, 2>([&](auto I) __attribute__((always_inline)) {
+      xf[I.value] = read_a(st, I.value);
+      sx[I.value] = read_as(st, I.value);
+    });
+  }
+  // the loads of a stage are issued in PARTS pieces, one ahead of each step's
+  // products: after the barrier in steps 6 and 7, the rest in steps 0.. of the
+  // next stage
+  const int nfr = min(FM, (rows + 15) >> 4);    // fragments with rows
+  constexpr int BAR = 5;                        // the barrier follows step BAR
+  constexpr int TAIL = FM - 1 - BAR;            // steps of a stage after it
+  // NS = 2: all loads right after the barrier (they are waited for at the next)
+  constexpr int SPREAD = NS == 2 ? TAIL : FM;   // steps that issue loads
+  auto stage = [&](int kt, auto PAR, auto SKIP) __attribute__((always_inline)) {
+    constexpr int p = decltype(PAR)::value;
+    constexpr bool skip = decltype(SKIP)::value;
+    const int nslot = slot + 1 == NS ? 0 : slot + 1;
+    const int pslot = slot == 0 ? NS - 1 : slot - 1;
+    const char* st = lds + slot * STAGE;
+    const char* nst = lds + nslot * STAGE;
+    static_for<0, FM>([&](auto I) __attribute__((always_inline)) {
+      constexpr int i = I.value;
+      __builtin_amdgcn_sched_barrier(0);
+      // step c of the SPREAD steps that issue stage kt + NS (after the barrier)
+      // or the rest of stage kt - 1 + NS (before it)
+      constexpr int c = i > BAR ? i - BAR - 1 : i + TAIL;
+      if constexpr (c < SPREAD) {
+        constexpr int q0 = c * LOADS / SPREAD, q1 = (c + 1) * LOADS / SPREAD;
+        static_for<q0, q1>([&](auto Q) __attribute__((always_inline)) {
+          if constexpr (i > BAR) issue(kt + NS, slot, Q);
+          else if (kt > 0) issue(kt - 1 + NS, pslot, Q);
+        });
+      }
+      if constexpr (i + 2 < FM) {
+        if (!skip || i + 2 < nfr) {
+          xf[(i + 2) & 3] = read_a(st, i + 2);
+          sx[(i + 2) & 3] = read_as(st, i + 2);
+        }
+      } else {
+        xf[(i + 2) & 3] = read_a(nst, i + 2 - FM);
+        sx[(i + 2) & 3] = read_as(nst, i + 2 - FM);
+      }
+      if constexpr (i == BAR + 1) {
+        static_for<0, 4>([&](auto J) __attribute__((always_inline)) { wf[1 - p][J.value] = read_b(nst, J.value); });
+        sw_[1 - p] = read_bs(nst);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (!skip || i < nfr) {
+        static_for<0, 4>([&](auto J) __attribute__((always_inline)) {
+          acc[i][J.value] = mma<A8, J.value>(wf[p][J.value], xf[i & 3], acc[i][J.value], sw_[p], sx[i & 3]);
+        });
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (i == BAR) {
+        __builtin_amdgcn_s_waitcnt(0xc07f);     // lgkmcnt(0): this stage's reads are in registers
+        wait_vmcnt<LOADS * (NS - 2)>();         // stage kt + 1 has landed for this wavefront
+        block_barrier();
+      }
+    });
+    slot = nslot;
+  };
+  auto run = [&](auto SKIP) __attribute__((always_inline)) {
+    int kt = 0;
+    for (; kt + 1 < KT; kt += 2) {
+      stage(kt, IntC<0>{}, SKIP);
+      stage(kt + 1, IntC<1>{}, SKIP);
+    }
+    if (kt < KT) stage(kt, IntC<0>{}, SKIP);
+  };
+  if (nfr == FM) run(IntC<0>{});
+  else run(IntC<1>{});
+  wait_vmcnt<0>();  // no LDS write may be in flight when the block ends
+
+  const int col = n0 + 64 * w;
+  if (col >= N) return;
+  static_for<0, FM>([&](auto I) __attribute__((always_inline)) {
+    constexpr int i = I.value;
+    const int m = 16 * i + r;
+    const size_t row = (size_t)(row0 + m);
+    if constexpr (FC == 1) store_h<A8>(acc[i], m < rows, row, col >> 1, args.f, lane, args.hq, args.hs);
+    else store_o(acc[i], m < rows, row, col, args.d, lane, (bf16_t*)args.o);
+  });
+}
+
+template <int FC, bool A8>
+int launch_tiles(const Mx4Args& a, hipStream_t s) {
+  const int64_t NT = ((FC == 1 ? 2 * (int64_t)a.f : (int64_t)a.d) + 255) / 256;
+  // at most sum_e ceil(m_e / 128) row tiles; a block past the device-side count ends at once
+  const int64_t grid = ((int64_t)a.P / 128 + a.E) * NT;
+  if (grid > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  gemm_mx4_tile_kernel<FC, A8><<<(unsigned)grid, 256, 0, s>>>(a, (int)NT);
+  TRE_LAUNCH_CHECK();
+  return MOE_OK;
+}
+
+// Which kernel: the rows kernel reads a column group's weights once per 16 rows
+// of an expert, the tile kernel once per 128.
+bool few_rows(const Mx4Args& a) { return (int64_t)a.P <= 32 * (int64_t)a.E; }
+
 }  // namespace
 
 int gemm_mx4_launch(int fc, bool a8, const Mx4Args& a, hipStream_t s) {
+  if (!few_rows(a)) {
+    if (fc == 1) return a8 ? launch_tiles<1, true>(a, s) : launch_tiles<1, false>(a, s);
+    return a8 ? launch_tiles<2, true>(a, s) : launch_tiles<2, false>(a, s);
+  }
   if (fc == 1) return a8 ? launch_rows<1, true>(a, s) : launch_rows<1, false>(a, s);
   return a8 ? launch_rows<2, true>(a, s) : launch_rows<2, false>(a, s);
 }
