@@ -81,6 +81,23 @@ __device__ __forceinline__ void dma4(rsrc_t r, uint32_t voff, uint32_t m0) {
                : "memory");
 }
 
+// The same with a uniform part `soff` of the offset in a scalar register.
+// (Callers keep both the lane part alone and the sum inside the resource, or
+// the lane part alone outside: the load then does the same whether the range
+// check counts the scalar part or not.)
+__device__ __forceinline__ void dma16(rsrc_t r, uint32_t voff, uint32_t soff, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds"
+               :
+               : "v"(voff), "s"(r), "s"(m0), "s"(soff)
+               : "memory");
+}
+__device__ __forceinline__ void dma4(rsrc_t r, uint32_t voff, uint32_t soff, uint32_t m0) {
+  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dword %0, %1, %3 offen lds"
+               :
+               : "v"(voff), "s"(r), "s"(m0), "s"(soff)
+               : "memory");
+}
+
 // Workgroup barrier without the memory fence of __syncthreads (which would
 // wait for every outstanding load); the empty asm statements keep the
 // compiler from moving memory accesses across it.

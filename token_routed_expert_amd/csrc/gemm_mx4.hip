@@ -29,11 +29,27 @@ using namespace gemm;
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
+// A row's 128 values of one K step in registers: E2M1 or E4M3.
+template <bool A8>
+struct Frag {
+  typedef i32x4_t type;
+};
+template <>
+struct Frag<true> {
+  typedef i32x8_t type;
+};
+
+// The registers an E2M1 operand does not use (the instruction reads four).
+__device__ __forceinline__ i32x8_t widen(const i32x4_t& v) {
+  return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
+}
+__device__ __forceinline__ i32x8_t widen(const i32x8_t& v) { return v; }
+
 // D += W X for one 16 x 16 x 128 block: w fp4, x fp4 or fp8; WSEL: byte of ws.
 template <bool A8, int WSEL>
-__device__ __forceinline__ f32x4_t mma(const i32x4_t& w, const i32x8_t& x, const f32x4_t& c, int ws,
-                                       int xs) {
-  const i32x8_t w8 = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
+__device__ __forceinline__ f32x4_t mma(const i32x4_t& w, const typename Frag<A8>::type& xf, const f32x4_t& c,
+                                       int ws, int xs) {
+  const i32x8_t w8 = widen(w), x = widen(xf);
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, x, c, 4, A8 ? 0 : 4, WSEL, ws, 0, xs);
 }
 
@@ -41,8 +57,12 @@ __device__ __forceinline__ f32x4_t mma(const i32x4_t& w, const i32x8_t& x, const
 // f each; lane l: row l & 15, columns 4 (l >> 4)..+3) -> h of the 32 columns
 // as one block per row, its codes to hq and its scale byte to hs.  `row`: the
 // row's index in the permuted buffers; col: the block's first column.
+//
+// The quantised h lies in panels of 128 columns, [f/128][P] rows of 64 (E2M1)
+// or 128 (E4M3) code bytes and of one scale word: what fc2 reads of 128 rows in
+// one K step is then one piece of memory.
 template <bool A8>
-__device__ __forceinline__ void store_h(const f32x4_t (&acc)[4], bool ok, size_t row, int col, int f,
+__device__ __forceinline__ void store_h(const f32x4_t (&acc)[4], bool ok, size_t row, int col, size_t P,
                                         int lane, uint8_t* hq, uint8_t* hs) {
   f32x4_t h0, h1;
 #pragma unroll
@@ -64,13 +84,15 @@ __device__ __forceinline__ void store_h(const f32x4_t (&acc)[4], bool ok, size_t
   m = row_max(m);
   const uint32_t b = mx::scale_byte<!A8>(m);
   if (!ok) return;
+  const size_t at = (size_t)(col >> 7) * P + row;
+  const int c = (col & 127) + pc;
   if constexpr (A8) {
     const float inv = mx::inv_scale_of(b == mx::kNanScale ? 127u : b);
-    *(uint2*)(hq + row * (size_t)f + col + pc) = make_uint2(mx::pack4_fp8(v, inv), mx::pack4_fp8(v + 4, inv));
+    *(uint2*)(hq + at * 128 + c) = make_uint2(mx::pack4_fp8(v, inv), mx::pack4_fp8(v + 4, inv));
   } else {
-    *(uint32_t*)(hq + row * (size_t)(f / 2) + (col + pc) / 2) = mx::pack8_fp4(v, b);
+    *(uint32_t*)(hq + at * 64 + c / 2) = mx::pack8_fp4(v, b);
   }
-  if (lane < 16) hs[row * (size_t)(f / 32) + col / 32] = (uint8_t)b;
+  if (lane < 16) hs[at * 4 + (col & 127) / 32] = (uint8_t)b;
 }
 
 // Epilogue of fc2 for one 16-row fragment: 64 columns from col on as bf16.
@@ -127,7 +149,11 @@ __global__ __launch_bounds__(256) void gemm_mx4_rows_kernel(Mx4Args args) {
   rows = uniform(rows);
   const uint8_t* wt = args.w + ((size_t)e * (N >> 4) + (size_t)nb * 4) * KT * 1024 + lane * 16;
   const uint8_t* wst = args.ws + ((size_t)e * NB + nb) * KT * 256 + lane * 4;
-  const size_t a_ld = A8 ? (size_t)K : (size_t)(K >> 1), as_ld = (size_t)(K >> 5);
+  // A row: fc1 row-major, fc2 in panels; a K step is a_step / as_step bytes on
+  constexpr int ARB = A8 ? 128 : 64;
+  const size_t a_ld = FC == 1 ? (size_t)KT * ARB : ARB, as_ld = FC == 1 ? (size_t)KT * 4 : 4;
+  const uint32_t a_step = FC == 1 ? ARB : (uint32_t)args.P * ARB;  // (the whole of A: below 2^31 bytes)
+  const uint32_t as_step = FC == 1 ? 4 : (uint32_t)args.P * 4;
   const size_t wstride = (size_t)KT * 1024;  // from one 16-column group to the next
   for (int m0 = 0; m0 < rows; m0 += 16) {
     // rows past the last are read as the last one and not stored
@@ -140,7 +166,7 @@ __global__ __launch_bounds__(256) void gemm_mx4_rows_kernel(Mx4Args args) {
     for (int j = 0; j < 4; ++j) acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     for (int k0 = w; k0 < KT; k0 += 4 * U) {
       i32x4_t wf[U][4];
-      i32x8_t xf[U];
+      typename Frag<A8>::type xf[U];
       int sw[U], sx[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -149,14 +175,13 @@ __global__ __launch_bounds__(256) void gemm_mx4_rows_kernel(Mx4Args args) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) wf[u][j] = *(const i32x4_t*)(wt + j * wstride + (size_t)kt * 1024);
           sw[u] = *(const int*)(wst + (size_t)kt * 256);
-          sx[u] = ast[kt * 4];
+          sx[u] = ast[(uint32_t)kt * as_step];
           if constexpr (A8) {
-            const i32x4_t lo = *(const i32x4_t*)(at + (size_t)kt * 128);
-            const i32x4_t hi = *(const i32x4_t*)(at + (size_t)kt * 128 + 64);
+            const i32x4_t lo = *(const i32x4_t*)(at + (uint32_t)kt * a_step);
+            const i32x4_t hi = *(const i32x4_t*)(at + (uint32_t)kt * a_step + 64);
             xf[u] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
           } else {
-            const i32x4_t lo = *(const i32x4_t*)(at + (size_t)kt * 64);
-            xf[u] = __builtin_shufflevector(lo, i32x4_t{0, 0, 0, 0}, 0, 1, 2, 3, 4, 5, 6, 7);
+            xf[u] = *(const i32x4_t*)(at + (uint32_t)kt * a_step);
           }
         }
       }
@@ -187,7 +212,7 @@ __global__ __launch_bounds__(256) void gemm_mx4_rows_kernel(Mx4Args args) {
     }
     const bool ok = m0 + r < rows;
     const size_t row = (size_t)(row0 + m0 + r);
-    if constexpr (FC == 1) store_h<A8>(acc, ok, row, nb * 32, args.f, lane, args.hq, args.hs);
+    if constexpr (FC == 1) store_h<A8>(acc, ok, row, nb * 32, (size_t)args.P, lane, args.hq, args.hs);
     else store_o(acc, ok, row, nb * 64, args.d, lane, (bf16_t*)args.o);
   }
 }
@@ -206,29 +231,48 @@ int launch_rows(const Mx4Args& a, hipStream_t s) {
 // wavefronts side by side (each all 128 rows x 64 columns, one scale group, as
 // 8 x 4 fragments), two blocks to a compute unit, so that one block's prologue,
 // epilogue and barrier waits run under the other's products.  K advances 128 a
-// stage through an LDS ring of NS stages; every byte of a stage arrives by
-// buffer_load ... lds.  LDS layout of a stage:
-//  * A: 128 rows of 64 (E2M1) or 128 (E4M3) bytes, the 16-byte chunk c of row r
-//    stored at chunk c ^ swz(r), swz(r) = (r >> 1) & 3 or & 7: the 16 rows of a
-//    fragment read then spread over all banks;
+// stage through two LDS slots; every byte of a stage arrives by buffer_load ...
+// lds.  What bounds the kernel beside the matrix cores is the number of cache
+// lines that a compute unit can have on the way from L2 (a build whose loads all
+// hit L1 took 407 us where this tiling's first form took 557, Qwen3 shape, fc1
+// with E2M1 rows; one more slot of look-ahead changed nothing), so every load
+// takes whole 128-byte lines where the layout allows it:
 //  * B: the wavefronts' 4 fragments each, 1 KB as stored: a lane reads back its
 //    own 16 bytes;
-//  * scales: one word per A row (its four group bytes; 1 KB, the second half
-//    unused), one per lane and column group for B.
-// A stage's slot is free once every wavefront has its last fragments in
-// registers: with the reads of stage kt done, a wait for stage kt + 1's loads
-// and one barrier, the loads of stage kt + NS go to that slot, spread over the
-// products that follow.
+//  * A: 128 rows of 128 bytes, the 16-byte chunk c of row r stored at chunk
+//    c ^ ((r >> 1) & 7), which spreads the 16 rows of a fragment read over all
+//    banks.  That is one stage of E4M3 rows.  E2M1 rows have 64 bytes a stage:
+//    fc1, whose rows lie anywhere (token_of), loads two stages together (PAIR);
+//    fc2's lie in panels, row next to row, and take 128 rows of 64 bytes a
+//    stage, chunk c at c ^ ((r >> 1) & 3);
+//  * scales: one word per lane and column group for B, one per row (its four
+//    group bytes) for fc2's A.  fc1's A scales are row-major in memory, where a
+//    word per row and stage would be as many lines as the codes themselves:
+//    they come 16 bytes a row, for four stages together, into one of two
+//    buffers (the first two stages of four load the next four's).
+// A slot is free once every wavefront has its last fragments in registers: with
+// the reads of stage kt done, a wait for stage kt + 1's loads and one barrier,
+// the loads of stage kt + 2 that the block shares go there.  A wavefront's own
+// B fragments need no barrier: they are loaded as soon as the registers hold
+// the stage's, so they have almost two stages to arrive.
+// An empty use of four accumulators.
+__device__ __forceinline__ void stay(f32x4_t (&a)[4]) {
+  asm volatile("" : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]), "+v"(a[3]));
+}
+
 template <int FC, bool A8>
 __global__ __launch_bounds__(256, 2) void gemm_mx4_tile_kernel(Mx4Args args, int NT) {
   constexpr int BM = 128, BN = 256, FM = BM / 16;
-  constexpr int NS = A8 ? 2 : 3;
-  constexpr int ARB = A8 ? 128 : 64;            // bytes of an A row and stage
-  constexpr int A_BYTES = BM * ARB, B_BYTES = 16 * 1024, AS_BYTES = 1024, BS_BYTES = 1024;
-  constexpr int STAGE = A_BYTES + B_BYTES + AS_BYTES + BS_BYTES;
-  constexpr int A_PER_WAVE = A_BYTES / 4096;    // 1 KB DMA instructions
-  constexpr int LOADS = A_PER_WAVE + 4 + 2;     // a wavefront's loads of a stage
-  __shared__ __attribute__((aligned(1024))) char lds[NS * STAGE];
+  constexpr bool PAIR = FC == 1 && !A8;         // A loads of two stages
+  constexpr int KB = A8 ? 128 : 64;             // bytes of an A row and stage
+  constexpr int ARB = PAIR ? 128 : KB;          // bytes of an A row in LDS
+  constexpr int A_BYTES = BM * ARB, B_BYTES = 16 * 1024, BS_BYTES = 1024;
+  constexpr int AS_BYTES = FC == 1 ? 0 : BM * 4;        // fc2: A scales in the stage
+  constexpr int AS4_BYTES = FC == 1 ? BM * 16 : 0;      // fc1: of four stages
+  constexpr int STAGE = B_BYTES + AS_BYTES + BS_BYTES;
+  constexpr int B_AT = 2 * A_BYTES, AS4_AT = B_AT + 2 * STAGE;
+  constexpr int NA = A_BYTES / 4096;            // a wavefront's 1 KB loads of an A slot
+  __shared__ __attribute__((aligned(1024))) char lds[AS4_AT + 2 * AS4_BYTES];
   __shared__ int sched[8];
   TileInfo ti;
   if (!decode_ragged_m<BM, 4>(args.offsets, args.E, NT, sched, ti)) return;
@@ -238,82 +282,133 @@ __global__ __launch_bounds__(256, 2) void gemm_mx4_tile_kernel(Mx4Args args, int
   const int n0 = uniform(ti.n0) * BN;
   const int K = FC == 1 ? args.d : args.f, N = FC == 1 ? 2 * args.f : args.d;
   const int KT = K >> 7;
-  const uint32_t a_ld = (uint32_t)(A8 ? K : K >> 1), as_ld = (uint32_t)(K >> 5);
 
-  // ---- sources: rows past the expert's end and columns past N read as zero
+  // ---- sources: rows past the expert's end and columns past N read as zero.
+  // A row: fc1 row-major, a slot is ARB bytes on; fc2 in panels
   const bool gather = FC == 1 && args.token_of != nullptr;
-  const size_t a_rows = gather ? (size_t)args.T : (size_t)rows, a_first = gather ? 0 : (size_t)row0;
-  const rsrc_t a_src = make_rsrc(args.a + a_first * a_ld, (uint32_t)(a_rows * a_ld));
-  const rsrc_t as_src = make_rsrc(args.as + a_first * as_ld, (uint32_t)(a_rows * as_ld));
-  const uint32_t b_size = (uint32_t)(N >> 4) * (uint32_t)KT * 1024u;
-  const rsrc_t b_src = make_rsrc(args.w + (size_t)e * b_size, b_size);
-  const rsrc_t bs_src = make_rsrc(args.ws + (size_t)e * (b_size / 16), b_size / 16);
+  const uint32_t a_rows = (uint32_t)(gather ? args.T : args.P);
+  const uint32_t a_ld = FC == 1 ? (uint32_t)KT * KB : KB, as_ld = FC == 1 ? (uint32_t)KT * 4u : 4u;
+  const uint32_t a_step = FC == 1 ? ARB : (uint32_t)args.P * KB, as_step = (uint32_t)args.P * 4u;
+  const rsrc_t a_src = make_rsrc(args.a, a_rows * (uint32_t)KT * KB);
+  const rsrc_t as_src = make_rsrc(args.as, a_rows * (uint32_t)KT * 4u);
+  const int col = n0 + 64 * w;                  // this wavefront's 64 columns
+  const uint32_t b_size = col < N ? 4096u * (uint32_t)KT : 0u;
+  const int colc = min(col, N - 64);
+  const rsrc_t b_src = make_rsrc(args.w + ((size_t)e * (N >> 4) + (size_t)(colc >> 4)) * KT * 1024, b_size);
+  const rsrc_t bs_src = make_rsrc(args.ws + ((size_t)e * (N >> 6) + (size_t)(colc >> 6)) * KT * 256, b_size / 16);
   constexpr uint32_t kPast = 0x80000000u;       // past every range
   auto row_of = [&](int m) __attribute__((always_inline)) -> uint32_t {  // source row of tile row m
-    return gather ? (uint32_t)args.token_of[row0 + min(m, rows - 1)] : (uint32_t)m;
+    const int pr = row0 + min(m, rows - 1);
+    return gather ? (uint32_t)args.token_of[pr] : (uint32_t)pr;
   };
-  uint32_t a_off[A_PER_WAVE];
+  uint32_t a_off[NA];
 #pragma unroll
-  for (int q = 0; q < A_PER_WAVE; ++q) {
-    const int t = w * A_PER_WAVE + q;           // instruction t: 1 KB of A rows
-    const int m = A8 ? 8 * t + (lane >> 3) : 16 * t + (lane >> 2);
-    const int c = A8 ? (lane & 7) ^ ((m >> 1) & 7) : (lane & 3) ^ ((m >> 1) & 3);
+  for (int q = 0; q < NA; ++q) {
+    const int t = w * NA + q;                   // load t: 1 KB of A rows
+    const int m = ARB == 128 ? 8 * t + (lane >> 3) : 16 * t + (lane >> 2);
+    const int c = ARB == 128 ? (lane & 7) ^ ((m >> 1) & 7) : (lane & 3) ^ ((m >> 1) & 3);
     a_off[q] = m < rows ? row_of(m) * a_ld + (uint32_t)c * 16u : kPast;
   }
-  // A scales: wavefronts 0 and 1 (64 rows each); 2 and 3 issue a load of nothing
-  const uint32_t as_off = w < 2 && 64 * w + lane < rows ? row_of(64 * w + lane) * as_ld : kPast;
-  const uint32_t b_off = ((uint32_t)(n0 >> 4) + 4u * w) * (uint32_t)KT * 1024u + (uint32_t)lane * 16u;
-  const uint32_t bs_off = ((uint32_t)(n0 >> 6) + (uint32_t)w) * (uint32_t)KT * 256u + (uint32_t)lane * 4u;
-
+  // A scales.  fc1: the wavefront's 16 rows of either half of the tile, a lane
+  // one of a row's four words; fc2: wavefronts 0 and 1, 64 rows each
+  uint32_t as_off[FC == 1 ? 2 : 1];
+#pragma unroll
+  for (int q = 0; q < (FC == 1 ? 2 : 1); ++q) {
+    const int m = FC == 1 ? 64 * q + 16 * w + (lane >> 2) : 64 * (w & 1) + lane;
+    as_off[q] = m < rows ? row_of(m) * as_ld + (FC == 1 ? (uint32_t)(lane & 3) * 4u : 0u) : kPast;
+  }
+  const uint32_t lane16 = (uint32_t)lane * 16u, lane4 = (uint32_t)lane * 4u;
   const uint32_t lds_base = (uint32_t)uniform((int)(uint32_t)(size_t)LDS_PTR(lds));
-  // load q of stage s (past the last stage: nothing is read, zeros land)
-  auto issue = [&](int s, int slot, auto Q) __attribute__((always_inline)) {
-    constexpr int q = decltype(Q)::value;
-    const uint32_t base = lds_base + (uint32_t)(slot * STAGE);
+
+  // Loads of stage s (slot s & 1); past the last stage nothing is read and
+  // zeros land.
+  auto src = [&](rsrc_t v, bool live) __attribute__((always_inline)) {
+    v[2] = live ? v[2] : 0;
+    return uniform_rsrc(v);
+  };
+  auto issue_bs = [&](int s, int slot) __attribute__((always_inline)) {
     const bool live = s < KT;
-    if constexpr (q < A_PER_WAVE) {
-      rsrc_t src = a_src;
-      src[2] = live ? src[2] : 0;
-      dma16(uniform_rsrc(src), a_off[q] + (uint32_t)(s * ARB), base + (uint32_t)((w * A_PER_WAVE + q) * 1024));
-    } else if constexpr (q < A_PER_WAVE + 4) {
-      constexpr int j = q - A_PER_WAVE;
-      rsrc_t src = b_src;
-      src[2] = live ? src[2] : 0;
-      dma16(uniform_rsrc(src), b_off + (uint32_t)(j * KT + s) * 1024u,
-            base + (uint32_t)(A_BYTES + (4 * w + j) * 1024));
-    } else if constexpr (q == A_PER_WAVE + 4) {
-      rsrc_t src = as_src;
-      src[2] = live ? src[2] : 0;
-      dma4(uniform_rsrc(src), as_off + (uint32_t)(s * 4),
-           base + (uint32_t)(A_BYTES + B_BYTES + w * 256));
+    dma4(src(bs_src, live), lane4, (uint32_t)(live ? s : 0) * 256u,
+         lds_base + (uint32_t)(B_AT + slot * STAGE + B_BYTES + AS_BYTES + w * 256));
+  };
+  auto issue_b = [&](int s, int slot, int j) __attribute__((always_inline)) {
+    const bool live = s < KT;
+    dma16(src(b_src, live), lane16, (uint32_t)(j * KT + (live ? s : 0)) * 1024u,
+          lds_base + (uint32_t)(B_AT + slot * STAGE + (4 * w + j) * 1024));
+  };
+  // load q of A slot content u: stage u, or (PAIR) stages 2 u and 2 u + 1.  The
+  // pair of an odd last stage reaches past its row: the rows' own part of the
+  // offset carries u, so that the range check sees the sum.
+  auto issue_a = [&](int u, int slot, int q) __attribute__((always_inline)) {
+    const bool live = (PAIR ? 2 * u : u) < KT;
+    const uint32_t dst = lds_base + (uint32_t)(slot * A_BYTES + (w * NA + q) * 1024);
+    if constexpr (PAIR) dma16(src(a_src, live), a_off[q] + (uint32_t)u * a_step, dst);
+    else dma16(src(a_src, live), a_off[q], (uint32_t)(live ? u : 0) * a_step, dst);
+  };
+  // fc1: half `half` of the A scales of stages 4 grp .. 4 grp + 3 (words past a
+  // row's end are not used)
+  auto issue_as4 = [&](int grp, int half) __attribute__((always_inline)) {
+    dma4(as_src, (half ? as_off[FC == 1 ? 1 : 0] : as_off[0]) + (uint32_t)grp * 16u,
+         lds_base + (uint32_t)(AS4_AT + (grp & 1) * AS4_BYTES + (64 * half + 16 * w) * 16));
+  };
+  // A scales loaded during stage kt: fc1, half of the next four stages' in the
+  // first two of four; fc2, stage kt + 2's.  Who has none to load repeats its B
+  // scales, so that all wavefronts issue as many loads.
+  // (Without a branch: one would split the stage, and the compiler then sinks
+  // the products in front of it past the barrier, with all their operands live.)
+  auto issue_as = [&](int kt, int slot) __attribute__((always_inline)) {
+    const bool live = kt + 2 < KT;
+    const int sc = live ? kt + 2 : 0;
+    const uint32_t bs_dst = lds_base + (uint32_t)(B_AT + slot * STAGE + B_BYTES + AS_BYTES + w * 256);
+    const bool as = FC == 1 ? (kt & 3) < 2 : w < 2;
+    rsrc_t v = pick(as, as_src, bs_src);
+    uint32_t dst, off;
+    if constexpr (FC == 1) {
+      const int grp = (kt >> 2) + 1, half = kt & 1;
+      v[2] = as || live ? v[2] : 0;
+      off = as ? (half ? as_off[FC == 1 ? 1 : 0] : as_off[0]) + (uint32_t)grp * 16u : lane4 + (uint32_t)sc * 256u;
+      dst = as ? lds_base + (uint32_t)(AS4_AT + (grp & 1) * AS4_BYTES + (64 * half + 16 * w) * 16) : bs_dst;
     } else {
-      rsrc_t src = bs_src;
-      src[2] = live ? src[2] : 0;
-      dma4(uniform_rsrc(src), bs_off + (uint32_t)s * 256u,
-           base + (uint32_t)(A_BYTES + B_BYTES + AS_BYTES + w * 256));
+      v[2] = live ? v[2] : 0;
+      off = as ? as_off[0] + (uint32_t)sc * as_step : lane4 + (uint32_t)sc * 256u;
+      dst = as ? lds_base + (uint32_t)(B_AT + slot * STAGE + B_BYTES + w * 256) : bs_dst;
     }
+    dma4(uniform_rsrc(v), off, (uint32_t)uniform((int)dst));
   };
 
-  // ---- fragments
-  const uint32_t sw = (uint32_t)(r >> 1) & (A8 ? 7u : 3u);
+  // ---- fragments of stage s
+  const uint32_t sw = (uint32_t)(r >> 1) & (ARB == 128 ? 7u : 3u);
   const uint32_t a_lo = (uint32_t)r * ARB + (((uint32_t)g ^ sw) << 4);
   const uint32_t a_hi = (uint32_t)r * ARB + (((uint32_t)(4 + g) ^ sw) << 4);
   auto ld16 = [&](const char* p) __attribute__((always_inline)) -> i32x4_t {
     return *(const __attribute__((address_space(3))) i32x4_t*)p;
   };
-  auto read_a = [&](const char* st, int i) __attribute__((always_inline)) -> i32x8_t {
-    const i32x4_t lo = ld16(st + a_lo + i * 16 * ARB);
-    if constexpr (A8) return __builtin_shufflevector(lo, ld16(st + a_hi + i * 16 * ARB), 0, 1, 2, 3, 4, 5, 6, 7);
-    else return __builtin_shufflevector(lo, i32x4_t{0, 0, 0, 0}, 0, 1, 2, 3, 4, 5, 6, 7);
+  // par = s & 1 (a constant); s itself for what is kept longer than two stages
+  auto read_a = [&](int s, auto PAR, int i) __attribute__((always_inline)) -> typename Frag<A8>::type {
+    constexpr int par = decltype(PAR)::value;
+    if constexpr (A8) {
+      const char* st = lds + par * A_BYTES + i * 16 * ARB;
+      return __builtin_shufflevector(ld16(st + a_lo), ld16(st + a_hi), 0, 1, 2, 3, 4, 5, 6, 7);
+    } else if constexpr (PAIR) {
+      return ld16(lds + ((s >> 1) & 1) * A_BYTES + i * 16 * ARB + (par ? a_hi : a_lo));
+    } else {
+      return ld16(lds + par * A_BYTES + i * 16 * ARB + a_lo);
+    }
   };
-  auto read_as = [&](const char* st, int i) __attribute__((always_inline)) -> int {
-    return *(const __attribute__((address_space(3))) uint8_t*)(st + A_BYTES + B_BYTES + (16 * i + r) * 4 + g);
+  auto read_as = [&](int s, auto PAR, int i) __attribute__((always_inline)) -> int {
+    constexpr int par = decltype(PAR)::value;
+    const char* p = FC == 1 ? lds + AS4_AT + ((s >> 2) & 1) * AS4_BYTES + (16 * i + r) * 16 + (s & 3) * 4 + g
+                            : lds + B_AT + par * STAGE + B_BYTES + (16 * i + r) * 4 + g;
+    return *(const __attribute__((address_space(3))) uint8_t*)p;
   };
-  auto read_b = [&](const char* st, int j) __attribute__((always_inline)) -> i32x4_t {
-    return ld16(st + A_BYTES + (4 * w + j) * 1024 + lane * 16);
+  auto read_b = [&](auto PAR, int j) __attribute__((always_inline)) -> i32x4_t {
+    constexpr int par = decltype(PAR)::value;
+    return ld16(lds + B_AT + par * STAGE + (4 * w + j) * 1024 + lane * 16);
   };
-  auto read_bs = [&](const char* st) __attribute__((always_inline)) -> int {
-    return *(const __attribute__((address_space(3))) int*)(st + A_BYTES + B_BYTES + AS_BYTES + w * 256 + lane * 4);
+  auto read_bs = [&](auto PAR) __attribute__((always_inline)) -> int {
+    constexpr int par = decltype(PAR)::value;
+    return *(const __attribute__((address_space(3))) int*)(lds + B_AT + par * STAGE + B_BYTES + AS_BYTES +
+                                                          w * 256 + lane * 4);
   };
 
   f32x4_t acc[FM][4];
@@ -321,81 +416,93 @@ __global__ __launch_bounds__(256, 2) void gemm_mx4_tile_kernel(Mx4Args args, int
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  static_for<0, NS>([&](auto S) __attribute__((always_inline)) {
-    static_for<0, LOADS>([&](auto Q) __attribute__((always_inline)) { issue(S.value, S.value, Q); });
+  // both slots, in the order in which the stages issue them
+  if constexpr (FC == 1) {
+    issue_as4(0, 0);
+    issue_as4(0, 1);
+  }
+  static_for<0, 2>([&](auto S) __attribute__((always_inline)) {
+    static_for<0, 4>([&](auto J) __attribute__((always_inline)) { issue_b(S.value, S.value, J.value); });
+    issue_bs(S.value, S.value);
+    if constexpr (FC == 2) issue_as(S.value - 2, S.value);
+    static_for<0, NA>([&](auto Q) __attribute__((always_inline)) { issue_a(S.value, S.value, Q.value); });
   });
-  wait_vmcnt<LOADS * (NS - 1)>();
+  constexpr int OWN = 5;                        // a stage's loads before the barrier
+  wait_vmcnt<OWN + NA + (FC == 2 ? 1 : 0)>();
   block_barrier();
 
-  i32x8_t xf[4];        // A fragments in flight: i & 3
+  typename Frag<A8>::type xf[4];                // A fragments in flight: i & 3
   int sx[4];
-  i32x4_t wf[2][4];     // B fragments of the stages of either parity
-  int sw_[2];
-  int slot = 0;
-  {
-    const char* st = lds;
-    static_for<0, 4>([&](auto J) __attribute__((always_inline)) { wf[0][J.value] = read_b(st, J.value); });
-    sw_[0] = read_bs(st);
-    static_for<0, 2>([&](auto I) __attribute__((always_inline)) {
-      xf[I.value] = read_a(st, I.value);
-      sx[I.value] = read_as(st, I.value);
-    });
-  }
-  // the loads of a stage are issued in PARTS pieces, one ahead of each step's
-  // products: after the barrier in steps 6 and 7, the rest in steps 0.. of the
-  // next stage
+  // a B fragment is replaced by the next stage's after its last product
+  i32x4_t wf[4];
+  int wsc;
+  static_for<0, 4>([&](auto J) __attribute__((always_inline)) { wf[J.value] = read_b(IntC<0>{}, J.value); });
+  wsc = read_bs(IntC<0>{});
+  static_for<0, 2>([&](auto I) __attribute__((always_inline)) {
+    xf[I.value] = read_a(0, IntC<0>{}, I.value);
+    sx[I.value] = read_as(0, IntC<0>{}, I.value);
+  });
   const int nfr = min(FM, (rows + 15) >> 4);    // fragments with rows
   constexpr int BAR = 5;                        // the barrier follows step BAR
-  constexpr int TAIL = FM - 1 - BAR;            // steps of a stage after it
-  // NS = 2: all loads right after the barrier (they are waited for at the next)
-  constexpr int SPREAD = NS == 2 ? TAIL : FM;   // steps that issue loads
   auto stage = [&](int kt, auto PAR, auto SKIP) __attribute__((always_inline)) {
     constexpr int p = decltype(PAR)::value;
     constexpr bool skip = decltype(SKIP)::value;
-    const int nslot = slot + 1 == NS ? 0 : slot + 1;
-    const int pslot = slot == 0 ? NS - 1 : slot - 1;
-    const char* st = lds + slot * STAGE;
-    const char* nst = lds + nslot * STAGE;
+    constexpr IntC<1 - p> NEXT{};
     static_for<0, FM>([&](auto I) __attribute__((always_inline)) {
       constexpr int i = I.value;
       __builtin_amdgcn_sched_barrier(0);
-      // step c of the SPREAD steps that issue stage kt + NS (after the barrier)
-      // or the rest of stage kt - 1 + NS (before it)
-      constexpr int c = i > BAR ? i - BAR - 1 : i + TAIL;
-      if constexpr (c < SPREAD) {
-        constexpr int q0 = c * LOADS / SPREAD, q1 = (c + 1) * LOADS / SPREAD;
-        static_for<q0, q1>([&](auto Q) __attribute__((always_inline)) {
-          if constexpr (i > BAR) issue(kt + NS, slot, Q);
-          else if (kt > 0) issue(kt - 1 + NS, pslot, Q);
-        });
+      if constexpr (i >= 1 && i < BAR) issue_b(kt + 2, p, i - 1);
+      if constexpr (i == BAR) issue_bs(kt + 2, p);
+      if constexpr (i > BAR) {
+        // shared loads: the A scales, then A (PAIR: the pair after next, in the
+        // second stage of a pair)
+        if constexpr (i == BAR + 1) issue_as(kt, p);
+        if constexpr (!PAIR || p == 1) {
+          constexpr int q0 = (i - BAR - 1) * NA / 2, q1 = (i - BAR) * NA / 2;
+          static_for<q0, q1>([&](auto Q) __attribute__((always_inline)) {
+            issue_a(PAIR ? (kt >> 1) + 2 : kt + 2, PAIR ? (kt >> 1) & 1 : p, Q.value);
+          });
+        }
       }
       if constexpr (i + 2 < FM) {
         if (!skip || i + 2 < nfr) {
-          xf[(i + 2) & 3] = read_a(st, i + 2);
-          sx[(i + 2) & 3] = read_as(st, i + 2);
+          xf[(i + 2) & 3] = read_a(kt, PAR, i + 2);
+          sx[(i + 2) & 3] = read_as(kt, PAR, i + 2);
         }
       } else {
-        xf[(i + 2) & 3] = read_a(nst, i + 2 - FM);
-        sx[(i + 2) & 3] = read_as(nst, i + 2 - FM);
-      }
-      if constexpr (i == BAR + 1) {
-        static_for<0, 4>([&](auto J) __attribute__((always_inline)) { wf[1 - p][J.value] = read_b(nst, J.value); });
-        sw_[1 - p] = read_bs(nst);
+        xf[(i + 2) & 3] = read_a(kt + 1, NEXT, i + 2 - FM);
+        sx[(i + 2) & 3] = read_as(kt + 1, NEXT, i + 2 - FM);
       }
       __builtin_amdgcn_sched_barrier(0);
       if (!skip || i < nfr) {
         static_for<0, 4>([&](auto J) __attribute__((always_inline)) {
-          acc[i][J.value] = mma<A8, J.value>(wf[p][J.value], xf[i & 3], acc[i][J.value], sw_[p], sx[i & 3]);
+          acc[i][J.value] = mma<A8, J.value>(wf[J.value], xf[i & 3], acc[i][J.value], wsc, sx[i & 3]);
+          if constexpr (i == FM - 1 && !skip) {
+            __builtin_amdgcn_sched_barrier(0);
+            wf[J.value] = read_b(NEXT, J.value);
+          }
         });
+      }
+      // The products stay in their step: without a use here the compiler sinks
+      // them to the end of the stage, past the barrier, with every fragment live.
+      stay(acc[i]);
+      if constexpr (i == FM - 1) {
+        if constexpr (skip)
+          static_for<0, 4>([&](auto J) __attribute__((always_inline)) { wf[J.value] = read_b(NEXT, J.value); });
+        wsc = read_bs(NEXT);
       }
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (i == BAR) {
         __builtin_amdgcn_s_waitcnt(0xc07f);     // lgkmcnt(0): this stage's reads are in registers
-        wait_vmcnt<LOADS * (NS - 2)>();         // stage kt + 1 has landed for this wavefront
+        // stage kt + 1 has landed for this wavefront: newer than its B loads are
+        // the shared loads issued in stage kt - 1 and this stage's B loads; its A
+        // loads (not PAIR, or the next pair's when p is 1) are the last of those
+        if constexpr (PAIR && p == 0) wait_vmcnt<OWN + 1 + NA>();
+        else if constexpr (PAIR) wait_vmcnt<OWN + 1>();
+        else wait_vmcnt<OWN>();
         block_barrier();
       }
     });
-    slot = nslot;
   };
   auto run = [&](auto SKIP) __attribute__((always_inline)) {
     int kt = 0;
@@ -409,13 +516,12 @@ __global__ __launch_bounds__(256, 2) void gemm_mx4_tile_kernel(Mx4Args args, int
   else run(IntC<1>{});
   wait_vmcnt<0>();  // no LDS write may be in flight when the block ends
 
-  const int col = n0 + 64 * w;
   if (col >= N) return;
   static_for<0, FM>([&](auto I) __attribute__((always_inline)) {
     constexpr int i = I.value;
     const int m = 16 * i + r;
     const size_t row = (size_t)(row0 + m);
-    if constexpr (FC == 1) store_h<A8>(acc[i], m < rows, row, col >> 1, args.f, lane, args.hq, args.hs);
+    if constexpr (FC == 1) store_h<A8>(acc[i], m < rows, row, col >> 1, (size_t)args.P, lane, args.hq, args.hs);
     else store_o(acc[i], m < rows, row, col, args.d, lane, (bf16_t*)args.o);
   });
 }
