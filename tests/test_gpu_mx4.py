@@ -198,6 +198,9 @@ COUNTS = {
     "hot": [700, 3, 0, 1],
     "wide": [0, 5] * 100,
     "tail": [513],
+    # few rows on average: one expert holds many, and the passes of 16 and 32 rows end inside them
+    "few_edges": [16, 17, 0, 31, 32, 33, 48, 64, 65] + [0] * 30,
+    "few_hot": [0] * 40 + [300, 1],
 }
 
 

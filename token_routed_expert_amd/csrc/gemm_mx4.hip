@@ -107,16 +107,19 @@ __device__ __forceinline__ void store_o(const f32x4_t (&acc)[4], bool ok, size_t
 }
 
 // Few rows per expert: the product is bound by reading the weights.  A block
-// of four wavefronts takes 64 stored columns of one expert (one scale group)
-// and all its rows, 16 at a time; the wavefronts split K (wavefront w takes
-// the 128-K steps w, w + 4, ...), read the weight fragments from memory into
+// of NW wavefronts takes 64 stored columns of one expert (one scale group) and
+// all its rows, 16 or 32 at a time; the wavefronts split K (wavefront w takes
+// the 128-K steps w, w + NW, ...), read the weight fragments from memory into
 // registers as they are stored, and their partial sums meet in LDS, added in
 // wavefront order.  Blocks take the experts that have rows, in order, so a
-// call with few rows launches few blocks.
+// call with few rows launches few blocks.  The weights are read with
+// non-temporal loads (each is used once a pass; 128 experts, d 4096, f 1536, 23
+// tokens of 8 experts, E2M1 rows: fc1 107 -> 100 us, fc2 58 -> 55 us, 6.4 TB/s).  Eight wavefronts, or eight K steps
+// in flight, are slower by 5-40 %.
+constexpr int NW = 4;  // wavefronts of a block, which split K
 template <int FC, bool A8>
-__global__ __launch_bounds__(256) void gemm_mx4_rows_kernel(Mx4Args args) {
-  constexpr int U = 4;  // K steps whose loads are in flight together
-  __shared__ f32x4_t part[4][4][64];
+__global__ __launch_bounds__(NW * 64) void gemm_mx4_rows_kernel(Mx4Args args) {
+  __shared__ f32x4_t part[2][NW][4][64];
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int w = uniform((int)threadIdx.x >> 6);
   const int K = FC == 1 ? args.d : args.f, N = FC == 1 ? 2 * args.f : args.d;
@@ -155,65 +158,87 @@ __global__ __launch_bounds__(256) void gemm_mx4_rows_kernel(Mx4Args args) {
   const uint32_t a_step = FC == 1 ? ARB : (uint32_t)args.P * ARB;  // (the whole of A: below 2^31 bytes)
   const uint32_t as_step = FC == 1 ? 4 : (uint32_t)args.P * 4;
   const size_t wstride = (size_t)KT * 1024;  // from one 16-column group to the next
-  for (int m0 = 0; m0 < rows; m0 += 16) {
-    // rows past the last are read as the last one and not stored
-    const int pr = row0 + min(m0 + r, rows - 1);
-    const size_t ar = FC == 1 && args.token_of ? (size_t)args.token_of[pr] : (size_t)pr;
-    const uint8_t* at = args.a + ar * a_ld + g * 16;
-    const uint8_t* ast = args.as + ar * as_ld + g;
-    f32x4_t acc[4];
+  // rows m0 .. m0 + 16 MT - 1, U K steps' loads of a wavefront in flight together
+  auto pass = [&](int m0, auto MTC, auto UC) __attribute__((always_inline)) {
+    constexpr int MT = decltype(MTC)::value, U = decltype(UC)::value;
+    const uint8_t *at[MT], *ast[MT];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int k0 = w; k0 < KT; k0 += 4 * U) {
+    for (int t = 0; t < MT; ++t) {
+      // rows past the last are read as the last one and not stored
+      const int pr = row0 + min(m0 + 16 * t + r, rows - 1);
+      const size_t ar = FC == 1 && args.token_of ? (size_t)args.token_of[pr] : (size_t)pr;
+      at[t] = args.a + ar * a_ld + g * 16;
+      ast[t] = args.as + ar * as_ld + g;
+    }
+    f32x4_t acc[MT][4];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[t][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int k0 = w; k0 < KT; k0 += NW * U) {
       i32x4_t wf[U][4];
-      typename Frag<A8>::type xf[U];
-      int sw[U], sx[U];
+      typename Frag<A8>::type xf[U][MT];
+      int sw[U], sx[U][MT];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int kt = k0 + 4 * u;
+        const int kt = k0 + NW * u;
         if (kt < KT) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) wf[u][j] = *(const i32x4_t*)(wt + j * wstride + (size_t)kt * 1024);
+          for (int j = 0; j < 4; ++j)
+            wf[u][j] = __builtin_nontemporal_load((const i32x4_t*)(wt + j * wstride + (size_t)kt * 1024));
           sw[u] = *(const int*)(wst + (size_t)kt * 256);
-          sx[u] = ast[(uint32_t)kt * as_step];
-          if constexpr (A8) {
-            const i32x4_t lo = *(const i32x4_t*)(at + (uint32_t)kt * a_step);
-            const i32x4_t hi = *(const i32x4_t*)(at + (uint32_t)kt * a_step + 64);
-            xf[u] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-          } else {
-            xf[u] = *(const i32x4_t*)(at + (uint32_t)kt * a_step);
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            const uint8_t* a = at[t] + (uint32_t)kt * a_step;
+            sx[u][t] = ast[t][(uint32_t)kt * as_step];
+            if constexpr (A8) {
+              const i32x4_t lo = *(const i32x4_t*)a, hi = *(const i32x4_t*)(a + 64);
+              xf[u][t] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            } else {
+              xf[u][t] = *(const i32x4_t*)a;
+            }
           }
         }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (k0 + 4 * u < KT) {
-          static_for<0, 4>([&](auto J) __attribute__((always_inline)) {
-            acc[J.value] = mma<A8, J.value>(wf[u][J.value], xf[u], acc[J.value], sw[u], sx[u]);
-          });
+        if (k0 + NW * u < KT) {
+#pragma unroll
+          for (int t = 0; t < MT; ++t)
+            static_for<0, 4>([&](auto J) __attribute__((always_inline)) {
+              acc[t][J.value] = mma<A8, J.value>(wf[u][J.value], xf[u][t], acc[t][J.value], sw[u], sx[u][t]);
+            });
         }
       }
     }
     __syncthreads();  // the previous rows' partial sums have been read
 #pragma unroll
-    for (int j = 0; j < 4; ++j) part[w][j][lane] = acc[j];
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) part[t][w][j][lane] = acc[t][j];
     __syncthreads();
-    if (w != 0) continue;
+    if (w >= MT) return;  // wavefront t stores rows 16 t ..
+    f32x4_t sum[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      f32x4_t s = part[0][j][lane];
+      f32x4_t s = part[w][0][j][lane];
 #pragma unroll
-      for (int i = 1; i < 4; ++i) {
-        const f32x4_t p = part[i][j][lane];
+      for (int i = 1; i < NW; ++i) {
+        const f32x4_t p = part[w][i][j][lane];
 #pragma unroll
         for (int q = 0; q < 4; ++q) s[q] += p[q];
       }
-      acc[j] = s;
+      sum[j] = s;
     }
-    const bool ok = m0 + r < rows;
-    const size_t row = (size_t)(row0 + m0 + r);
-    if constexpr (FC == 1) store_h<A8>(acc, ok, row, nb * 32, (size_t)args.P, lane, args.hq, args.hs);
-    else store_o(acc, ok, row, nb * 64, args.d, lane, (bf16_t*)args.o);
+    const int m = m0 + 16 * w + r;
+    const size_t row = (size_t)(row0 + m);
+    if constexpr (FC == 1) store_h<A8>(sum, m < rows, row, nb * 32, (size_t)args.P, lane, args.hq, args.hs);
+    else store_o(sum, m < rows, row, nb * 64, args.d, lane, (bf16_t*)args.o);
+  };
+  if (rows <= 16) {
+    pass(0, IntC<1>{}, IntC<4>{});
+  } else {
+    for (int m0 = 0; m0 < rows; m0 += 32) pass(m0, IntC<2>{}, IntC<2>{});
   }
 }
 
@@ -222,7 +247,7 @@ int launch_rows(const Mx4Args& a, hipStream_t s) {
   const int64_t NB = (FC == 1 ? 2 * (int64_t)a.f : (int64_t)a.d) / 64;
   const int64_t grid = NB * (a.P < a.E ? a.P : a.E);
   if (grid > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
-  gemm_mx4_rows_kernel<FC, A8><<<(unsigned)grid, 256, 0, s>>>(a);
+  gemm_mx4_rows_kernel<FC, A8><<<(unsigned)grid, NW * 64, 0, s>>>(a);
   TRE_LAUNCH_CHECK();
   return MOE_OK;
 }
@@ -537,9 +562,14 @@ int launch_tiles(const Mx4Args& a, hipStream_t s) {
   return MOE_OK;
 }
 
-// Which kernel: the rows kernel reads a column group's weights once per 16 rows
-// of an expert, the tile kernel once per 128.
-bool few_rows(const Mx4Args& a) { return (int64_t)a.P <= 32 * (int64_t)a.E; }
+// Which kernel: the rows kernel reads a column group's weights once per 16 or 32
+// rows of an expert and wins while they are read once or hardly more: at 16
+// rows an expert on average it took 217 us (E2M1 rows) and 253 us (E4M3) where
+// the tile kernel took 235 and 242 us (128 experts, d 4096, f 1536), and 125 and
+// 138 us against 168 and 178 us (8 experts, f 14336); at 24 and 32 rows the tile
+// kernel wins (243 and 250 against 245 and 294 us; 172 and 183 against 211 and
+// 243 us).
+bool few_rows(const Mx4Args& a) { return (int64_t)a.P <= 16 * (int64_t)a.E; }
 
 }  // namespace
 
