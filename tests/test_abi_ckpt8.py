@@ -73,3 +73,16 @@ def test_layer_mode(call):
     for dtype in ("e4m3", "mxfp8", "f32"):
         s8 = make_shape(**{**SHAPE, "dtype": dtype})
         assert fn(C.byref(s8), C.byref(io), P, 16, None) == UNS
+
+
+def test_misaligned_pointers():
+    sh = make_shape(**SHAPE)
+    odd = C.c_void_p(24)
+    for i in (2, 3, 4, 5, 7, 9, 10):
+        a = [P, P] + [P] * 9 + [None]
+        a[i] = odd
+        assert N.lib().moe_grouped_gemm_fwd_ckpt8(C.byref(sh), *a) == UNS, i
+    for i in (2, 3, 5, 6, 7, 8, 10, 11, 12, 13, 14, 15):
+        a = [P, P] + [P] * 14 + [None, None]
+        a[i] = odd
+        assert N.lib().moe_grouped_gemm_bwd_ckpt8(C.byref(sh), *a, P, 1 << 40, None) == UNS, i

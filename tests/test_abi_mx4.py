@@ -115,3 +115,44 @@ def test_layer_refuses_before_enqueuing():
         setattr(io, n, 16)
     io.aux_loss = 16
     assert lib.moe_layer_fwd(C.byref(sh), C.byref(io), P, need, None) == WS
+
+
+ODD = C.c_void_p(24)  # 8-byte aligned only
+
+
+def test_misaligned_pointers():
+    lib = N.lib()
+    for a in ((ODD, P), (P, ODD)):
+        assert lib.moe_quantize_rows_mx4(a[0], N.MOE_BF16, 4, 64, a[1], P, None) == UNS
+        assert lib.moe_quantize_weights_mx4(a[0], None, N.MOE_F32, 1, 128, 128, a[1], P, None) == UNS
+        assert lib.moe_dequantize_weights_mx4(a[0], P, 1, 128, 128, a[1], None, None) == UNS
+    assert lib.moe_quantize_weights_mx4(P, ODD, N.MOE_F32, 1, 128, 128, P, P, None) == UNS
+    sh = make_shape(**OK_SHAPE)
+    for i in (2, 4, 5):                                   # xq, o, ws
+        a = [P, None, P, P, P, P]
+        a[i] = ODD
+        assert lib.moe_grouped_gemm_fwd_mx4(C.byref(sh), a[0], a[1], a[2], a[3], C.byref(weights()), a[4],
+                                            a[5], 1 << 40, None) == UNS, i
+    half = C.c_void_p(18)
+    assert lib.moe_grouped_gemm_fwd_mx4(C.byref(sh), P, None, P, half, C.byref(weights()), P, P, 1 << 40,
+                                        None) == UNS
+
+
+def test_python_refuses_what_the_kernels_cannot_take():
+    """Host tensors, wrong types, short buffers and foreign layouts stop before the library."""
+    import torch
+
+    import token_routed_expert_amd as tre
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    q, s = torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(4, 2, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="device"):
+        tre.moe_quantize_rows_mx4(x, q, s)
+    with pytest.raises(TypeError):
+        tre.moe_quantize_rows_mx4(x.half(), q, s)
+    with pytest.raises(ValueError, match="contiguous"):
+        tre.moe_quantize_rows_mx4(x.t(), q, s)
+    W = torch.zeros(1, 128, 128)
+    with pytest.raises(ValueError, match="shape"):
+        tre.moe_quantize_weights_mx4(W, W[:, :, :64], q, s)
+    with pytest.raises(ValueError, match="shape"):
+        tre.moe_dequantize_weights_mx4(q, s, W.bfloat16(), W[:, :64].bfloat16())

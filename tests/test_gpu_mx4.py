@@ -112,7 +112,7 @@ def product_case(counts, d, f, a8, seed, gather, T=None):
     E, P = len(counts), int(sum(counts))
     T = P if T is None else T
     X = torch.from_numpy(rng.standard_normal((T if gather else P, d)).astype(np.float32)).bfloat16()
-    tok = rng.integers(0, T, P).astype(np.int32) if gather else None
+    tok = rng.integers(0, T, T).astype(np.int32) if gather else None   # (entries past the last expert: unused)
     W1, W3 = (rng.standard_normal((E, d, f)).astype(np.float32) * d ** -0.5 for _ in range(2))
     W2 = rng.standard_normal((E, f, d)).astype(np.float32) * f ** -0.5
     return X, tok, W1, W3, W2, offsets_of(counts)
@@ -219,7 +219,7 @@ def test_product(name, gather, a8):
 @pytest.mark.parametrize("a8", [False, True], ids=["a4", "a8"])
 @pytest.mark.parametrize("d,f", [(128, 128), (128, 1152), (1152, 128), (896, 384)])
 def test_product_widths(d, f, a8):
-    case = product_case([40, 0, 1, 90], d, f, a8, d + f, True, T=77)
+    case = product_case([40, 0, 1, 90], d, f, a8, d + f, True)
     check(case, a8, 4, 1, 131, f)
 
 
@@ -346,3 +346,32 @@ def test_a_call_on_another_stream():
     s.synchronize()
     rq, rs = oracle.quant_mx4_rows(src.double().cpu().numpy())
     assert np.array_equal(u8(codes), rq) and np.array_equal(u8(sb), rs)
+
+
+def test_python_refuses_short_and_misaligned_tensors():
+    import token_routed_expert_amd as tre
+    x = torch.zeros(8, 64, dtype=torch.bfloat16, device="cuda")
+    q, s = torch.zeros(8 * 32, dtype=torch.uint8, device="cuda"), torch.zeros(16, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="elements"):
+        tre.moe_quantize_rows_mx4(x, q[:-1], s)
+    with pytest.raises(ValueError, match="elements"):
+        tre.moe_quantize_rows_mx4(x, q, s[:-1])
+    with pytest.raises(ValueError, match="aligned"):
+        tre.moe_quantize_rows_mx4(x.flatten()[4:4 + 7 * 64].view(7, 64), q, s)
+    with pytest.raises(ValueError, match="device"):
+        tre.moe_quantize_rows_mx4(x, q.cpu(), s)
+    case = product_case([3], 128, 128, False, 1, False)
+    o, w = run_product(case, False, 1, 1, 3, 128)
+    sh = tre.make_shape(3, 128, 1, 1, 128, dtype="mxfp4")
+    off = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    xq, xs = torch.zeros(3, 64, dtype=torch.uint8, device="cuda"), torch.zeros(3, 4, dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(4096, dtype=torch.uint8, device="cuda")
+    tre.moe_grouped_gemm_fwd_mx4(sh, off, None, xq, xs, w, o, ws)
+    for bad in (dict(xq=xq[:2]), dict(xs=xs[:2]), dict(o=o[:2]), dict(off=off[:1]), dict(off=off.long())):
+        a = {**dict(off=off, xq=xq, xs=xs, o=o), **bad}
+        with pytest.raises((ValueError, TypeError)):
+            tre.moe_grouped_gemm_fwd_mx4(sh, a["off"], None, a["xq"], a["xs"], w, a["o"], ws)
+    with pytest.raises(tre.MoeError):
+        tre.moe_grouped_gemm_fwd_mx4(sh, off, None, xq, xs, w, o, None)
+    torch.cuda.synchronize()
+    assert not o.float().abs().max()          # zero rows give zeros

@@ -12,6 +12,12 @@ namespace {
 
 constexpr int64_t kMaxE = 256;
 
+// Whether every pointer is a multiple of n bytes (null ones are).
+template <typename... T>
+bool aligned(size_t n, const T*... p) {
+  return ((((uintptr_t)p) | ...) & (n - 1)) == 0;
+}
+
 __global__ void fill_offsets_kernel(int32_t* off, int32_t T) {
   if (threadIdx.x == 0) { off[0] = 0; off[1] = T; }
 }
@@ -625,6 +631,9 @@ int moe_grouped_gemm_fwd_ckpt8(const moe_shape* sh, const int32_t* offsets,
   if (token_of && (st = check_gather(sh))) return st;
   if (!offsets || !x || !W1 || !W3 || !W2 || !row_prob || !abq || !abs || !h || !o)
     return MOE_ERR_INVALID;
+  if (!aligned(16, (const char*)x, (const char*)W1, (const char*)W3, (const char*)W2,
+               (const char*)abq, (const char*)h, (const char*)o))
+    return MOE_ERR_UNSUPPORTED;
   return fwd_rowscaled(sh, offsets,
                        token_of ? RowSrc{nullptr, token_of, x} : RowSrc{x, nullptr, nullptr}, W1, W3,
                        W2, row_prob, SavedAb{nullptr, abq, abs}, h, o, stream);
@@ -644,6 +653,10 @@ int moe_grouped_gemm_bwd_ckpt8(const moe_shape* sh, const int32_t* offsets,
   if (!offsets || !x || !abq || !abs || !dO || !W1 || !W3 || !W2 || !row_prob || !h || !dab ||
       !dXp || !dW1 || !dW3 || !dW2)
     return MOE_ERR_INVALID;
+  if (!aligned(16, (const char*)x, (const char*)abq, (const char*)dO, (const char*)W1,
+               (const char*)W3, (const char*)W2, (const char*)h, (const char*)dab,
+               (const char*)dXp, (const char*)dW1, (const char*)dW3, (const char*)dW2))
+    return MOE_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < dp_part_bytes(sh)) return MOE_ERR_WORKSPACE;
   return bwd_rowscaled(sh, offsets,
                        token_of ? RowSrc{nullptr, token_of, x} : RowSrc{x, nullptr, nullptr},
@@ -950,6 +963,7 @@ int moe_quantize_rows_mx4(const void* src, int32_t src_dtype, int64_t rows, int6
   if (cols % 32 != 0 || rows >= ((int64_t)1 << 40) || cols >= (1 << 30) ||
       (cols > 0 && rows > ((int64_t)1 << 36) / (cols / 32)))
     return MOE_ERR_UNSUPPORTED;
+  if (!aligned(16, (const char*)src, codes)) return MOE_ERR_UNSUPPORTED;
   return quant_rows_mx4_launch(src, src_dtype == MOE_F32, rows, cols, codes, scales,
                                (hipStream_t)stream);
 }
@@ -971,6 +985,7 @@ int moe_quantize_weights_mx4(const void* W, const void* W_pair, int32_t src_dtyp
   int st = check_mx4_matrix(E, R, C, W_pair != nullptr);
   if (st) return st;
   if (src_dtype != MOE_BF16 && src_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  if (!aligned(16, (const char*)W, (const char*)W_pair, codes)) return MOE_ERR_UNSUPPORTED;
   return quant_weights_mx4_launch(W, W_pair, src_dtype == MOE_F32, E, R, C, codes, scales,
                                   (hipStream_t)stream);
 }
@@ -980,6 +995,7 @@ int moe_dequantize_weights_mx4(const uint8_t* codes, const uint8_t* scales, int6
   if (!W || !codes || !scales) return MOE_ERR_INVALID;
   int st = check_mx4_matrix(E, R, C, W_pair != nullptr);
   if (st) return st;
+  if (!aligned(16, codes, (const char*)W, (const char*)W_pair)) return MOE_ERR_UNSUPPORTED;
   return dequant_weights_mx4_launch(codes, scales, E, R, C, W, W_pair, (hipStream_t)stream);
 }
 
@@ -990,6 +1006,10 @@ int moe_grouped_gemm_fwd_mx4(const moe_shape* sh, const int32_t* offsets, const 
   if (st) return st;
   if ((st = check_mx4_dims(sh))) return st;
   if (!offsets || !xq || !xs || !weights_ok(w) || !o) return MOE_ERR_INVALID;
+  if (!aligned(16, xq, w->W13, w->W2, (const char*)o, (const char*)ws) ||
+      !aligned(4, (const char*)offsets, (const char*)token_of, (const char*)xs, (const char*)w->W13s,
+               (const char*)w->W2s))
+    return MOE_ERR_UNSUPPORTED;
   size_t need;
   const Mx4Ws W = carve_mx4(sh, ws, &need);
   if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE;

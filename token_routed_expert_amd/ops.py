@@ -38,8 +38,41 @@ def _ptr(t, dtype=None):
 
 def _stream(stream=None):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # torch.cuda.current_stream().cuda_stream without building a Stream object
+        # (2.5 us of a 7 us call)
+        return C.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
     return C.c_void_p(stream.cuda_stream)
+
+
+class _Bufs:
+    """Checked pointers of one call: every tensor contiguous, of the given type, on
+    the current device, aligned as the kernels access it and at least as large as
+    they assume (a kernel handed less reads or writes past it)."""
+
+    __slots__ = ("call", "dev")
+
+    def __init__(self, call):
+        self.call = call
+        self.dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+
+    def __call__(self, name, t, dtype, numel, align=16):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{self.call}: {name}: expected a torch.Tensor, got {type(t)}")
+        if t.dtype != dtype:
+            raise TypeError(f"{self.call}: {name}: expected a {dtype} tensor, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{self.call}: {name} must be contiguous")
+        if t.numel() < numel:
+            raise ValueError(f"{self.call}: {name} has {t.numel()} elements, {numel} are needed")
+        if t.get_device() != self.dev or self.dev < 0:
+            raise ValueError(f"{self.call}: {name} is not on the current device")
+        p = t.data_ptr()
+        if p % align:
+            raise ValueError(f"{self.call}: {name} is not aligned to {align} bytes")
+        return p
+
+    def opt(self, name, t, dtype, numel, align=16):
+        return None if t is None else self(name, t, dtype, numel, align)
 
 
 def _check(status, call):
@@ -285,36 +318,55 @@ def moe_grouped_gemm_bwd_mx(sh, offsets, token_of, x, ab, h, dO, w: MXWeights, d
 
 
 _SRC_DTYPE = {torch.bfloat16: N.MOE_BF16, torch.float32: N.MOE_F32}
+BF16 = torch.bfloat16
+
+
+def _src_dtype(call, t):
+    code = _SRC_DTYPE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{call}: expected a bfloat16 or float32 source, got {t.dtype}")
+    return code
 
 
 def moe_quantize_rows_mx4(src, codes, scales, stream=None):
     """1 x 32 MXFP4 blocks along the rows of a bf16 or fp32 matrix: packed codes
     [rows][cols/2], E8M0 scale bytes [rows][cols/32]."""
+    call = "moe_quantize_rows_mx4"
     rows, cols = src.shape
-    _check(N.lib().moe_quantize_rows_mx4(_ptr(src), _SRC_DTYPE[src.dtype], rows, cols,
-                                         _ptr(codes, U8), _ptr(scales, U8), _stream(stream)),
-           "moe_quantize_rows_mx4")
+    code, b, n = _src_dtype(call, src), _Bufs(call), rows * cols
+    _check(N.lib().moe_quantize_rows_mx4(b("src", src, src.dtype, n), code, rows, cols,
+                                         b("codes", codes, U8, n // 2),
+                                         b("scales", scales, U8, n // 32, 1), _stream(stream)), call)
 
 
 def moe_quantize_weights_mx4(W, W_pair, codes, scales, stream=None):
     """MXFP4 tiles of bf16 or fp32 matrices W [E][R][C]; W_pair (or None): a second
     matrix whose 16-column groups alternate with W's."""
+    call = "moe_quantize_weights_mx4"
     E, R, Cc = W.shape
-    if W_pair is not None and (W_pair.shape != W.shape or W_pair.dtype != W.dtype):
-        raise ValueError("W_pair must have W's shape and dtype")
-    _check(N.lib().moe_quantize_weights_mx4(_ptr(W), _ptr(W_pair), _SRC_DTYPE[W.dtype], E, R, Cc,
-                                            _ptr(codes, U8), _ptr(scales, U8), _stream(stream)),
-           "moe_quantize_weights_mx4")
+    if W_pair is not None and W_pair.shape != W.shape:
+        raise ValueError("W_pair must have W's shape")
+    code, b, one = _src_dtype(call, W), _Bufs(call), E * R * Cc
+    n = one if W_pair is None else 2 * one
+    _check(N.lib().moe_quantize_weights_mx4(b("W", W, W.dtype, one),
+                                            b.opt("W_pair", W_pair, W.dtype, one), code, E, R, Cc,
+                                            b("codes", codes, U8, n // 2),
+                                            b("scales", scales, U8, n // 32, 1), _stream(stream)),
+           call)
 
 
 def moe_dequantize_weights_mx4(codes, scales, W, W_pair=None, stream=None):
     """The bf16 values W [E][R][C] (and W_pair) that MXFP4 tiles stand for."""
+    call = "moe_dequantize_weights_mx4"
     E, R, Cc = W.shape
     if W_pair is not None and W_pair.shape != W.shape:
         raise ValueError("W_pair must have W's shape")
-    _check(N.lib().moe_dequantize_weights_mx4(_ptr(codes, U8), _ptr(scales, U8), E, R, Cc,
-                                              _ptr(W, torch.bfloat16), _ptr(W_pair, torch.bfloat16),
-                                              _stream(stream)), "moe_dequantize_weights_mx4")
+    b, one = _Bufs(call), E * R * Cc
+    n = one if W_pair is None else 2 * one
+    _check(N.lib().moe_dequantize_weights_mx4(b("codes", codes, U8, n // 2),
+                                              b("scales", scales, U8, n // 32, 1), E, R, Cc,
+                                              b("W", W, BF16, one), b.opt("W_pair", W_pair, BF16, one),
+                                              _stream(stream)), call)
 
 
 class MX4Weights:
@@ -333,10 +385,18 @@ class MX4Weights:
 def moe_grouped_gemm_fwd_mx4(sh, offsets, token_of, xq, xs, w: MX4Weights, o, ws, stream=None):
     """The experts' forward with MXFP4 weights on quantised rows (row r is row
     token_of[r] of xq, or row r when token_of is None); o [P][d] bf16."""
-    _check(N.lib().moe_grouped_gemm_fwd_mx4(C.byref(sh), _ptr(offsets, I32), _ptr(token_of, I32),
-                                            _ptr(xq, U8), _ptr(xs, U8), C.byref(w.struct),
-                                            _ptr(o, torch.bfloat16), _ptr(ws), _nbytes(ws),
-                                            _stream(stream)), "moe_grouped_gemm_fwd_mx4")
+    call = "moe_grouped_gemm_fwd_mx4"
+    b = _Bufs(call)
+    T, d, E, f, P = sh.T, sh.d, sh.E, sh.f, sh.T * sh.k
+    rows = P if token_of is None else T
+    mat = E * d * f
+    b("W13", w["W13"], U8, mat), b("W2", w["W2"], U8, mat // 2)
+    b("W13s", w["W13s"], U8, mat // 16), b("W2s", w["W2s"], U8, mat // 32)
+    _check(N.lib().moe_grouped_gemm_fwd_mx4(
+        C.byref(sh), b("offsets", offsets, I32, E + 1, 4), b.opt("token_of", token_of, I32, P, 4),
+        b("xq", xq, U8, rows * d // (2 if sh.dtype == N.MOE_MXFP4 else 1)),
+        b("xs", xs, U8, rows * d // 32), C.byref(w.struct), b("o", o, BF16, P * d),
+        None if ws is None else b("ws", ws, ws.dtype, 0), _nbytes(ws), _stream(stream)), call)
 
 
 def _io(buffers: dict) -> N.moe_layer_io:
@@ -386,25 +446,39 @@ def moe_grouped_gemm_bwd_rowscaled(sh, offsets, xp, ab, h, dO, W1, W3, W2, row_p
         "moe_grouped_gemm_bwd_rowscaled")
 
 
+def _ckpt_inputs(b, sh, offsets, token_of, x, W1, W3, W2, row_prob):
+    E, mat, P = sh.E, sh.E * sh.d * sh.f, sh.T * sh.k
+    return (b("offsets", offsets, I32, E + 1, 4), b.opt("token_of", token_of, I32, P, 4),
+            b("x", x, BF16, (P if token_of is None else sh.T) * sh.d), b("W1", W1, BF16, mat),
+            b("W3", W3, BF16, mat), b("W2", W2, BF16, mat), b("row_prob", row_prob, F32, P, 4))
+
+
 def moe_grouped_gemm_fwd_ckpt8(sh, offsets, token_of, x, W1, W3, W2, row_prob, abq, abs_, h, o,
                                stream=None):
     """The row-scaled expert forward that keeps [a|b] in 8 bits (abq [P][2f] E4M3
     codes, abs_ [P][2f/32] E8M0 bytes); token_of None: x is already permuted."""
+    call = "moe_grouped_gemm_fwd_ckpt8"
+    b, P = _Bufs(call), sh.T * sh.k
     _check(N.lib().moe_grouped_gemm_fwd_ckpt8(
-        C.byref(sh), _ptr(offsets, I32), _ptr(token_of, I32), _ptr(x), _ptr(W1), _ptr(W3), _ptr(W2),
-        _ptr(row_prob, F32), _ptr(abq, U8), _ptr(abs_, U8), _ptr(h), _ptr(o), _stream(stream)),
-        "moe_grouped_gemm_fwd_ckpt8")
+        C.byref(sh), *_ckpt_inputs(b, sh, offsets, token_of, x, W1, W3, W2, row_prob),
+        b("abq", abq, U8, P * 2 * sh.f), b("abs", abs_, U8, P * sh.f // 16, 1),
+        b("h", h, BF16, P * sh.f), b("o", o, BF16, P * sh.d), _stream(stream)), call)
 
 
 def moe_grouped_gemm_bwd_ckpt8(sh, offsets, token_of, x, abq, abs_, dO, W1, W3, W2, row_prob, h, dab,
                                dXp, dW1, dW3, dW2, row_of, dprob, ws, stream=None):
     """Backward of moe_grouped_gemm_fwd_ckpt8 for the unscaled permuted dO; h is
     refilled from the checkpoint; dprob [P] (row_of None) or [T][k], or None."""
+    call = "moe_grouped_gemm_bwd_ckpt8"
+    b, P, mat = _Bufs(call), sh.T * sh.k, sh.E * sh.d * sh.f
+    off, tok, xp, w1, w3, w2, prob = _ckpt_inputs(b, sh, offsets, token_of, x, W1, W3, W2, row_prob)
     _check(N.lib().moe_grouped_gemm_bwd_ckpt8(
-        C.byref(sh), _ptr(offsets, I32), _ptr(token_of, I32), _ptr(x), _ptr(abq, U8), _ptr(abs_, U8),
-        _ptr(dO), _ptr(W1), _ptr(W3), _ptr(W2), _ptr(row_prob, F32), _ptr(h), _ptr(dab), _ptr(dXp),
-        _ptr(dW1), _ptr(dW3), _ptr(dW2), _ptr(row_of, I32), _ptr(dprob, F32), _ptr(ws), _nbytes(ws),
-        _stream(stream)), "moe_grouped_gemm_bwd_ckpt8")
+        C.byref(sh), off, tok, xp, b("abq", abq, U8, P * 2 * sh.f),
+        b("abs", abs_, U8, P * sh.f // 16, 1), b("dO", dO, BF16, P * sh.d), w1, w3, w2, prob,
+        b("h", h, BF16, P * sh.f), b("dab", dab, BF16, P * 2 * sh.f), b("dXp", dXp, BF16, P * sh.d),
+        b("dW1", dW1, BF16, mat), b("dW3", dW3, BF16, mat), b("dW2", dW2, BF16, mat),
+        b.opt("row_of", row_of, I32, P, 4), b.opt("dprob", dprob, F32, P, 4),
+        None if ws is None else b("ws", ws, ws.dtype, 0), _nbytes(ws), _stream(stream)), call)
 
 
 def moe_aux_loss(logits, k, counts, alpha, loss, ws, stream=None):
