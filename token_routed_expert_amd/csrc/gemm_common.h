@@ -180,9 +180,8 @@ __device__ __forceinline__ void store_ckpt(const f32x4_t& x, const f32x4_t& y, b
   if (first) *sc = (uint8_t)b;
 }
 // Eight values back from their codes and scale byte.
-__device__ __forceinline__ void load_ckpt(const uint8_t* q, const uint8_t* sc, float* v) {
-  const uint2 w = *(const uint2*)q;
-  const float s = mx::scale_any(*sc);
+__device__ __forceinline__ void load_ckpt(const uint2& w, uint32_t sc, float* v) {
+  const float s = mx::scale_any(sc);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int u = (int)(i == 0 ? w.x : w.y);
@@ -237,12 +236,47 @@ __device__ __forceinline__ void store_tile(const GemmArgs& args, const f32x4_t (
   // row receives 64 contiguous bytes per instruction.
   const int lm = lane & 15;
   const int pc = ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
+  // What the epilogue reads is loaded ahead of the stores before it: the compiler
+  // keeps every load behind them (they may alias), a memory latency each time.
+  // The rows' probabilities at once; the checkpoint's codes (16 + 2 bytes a lane
+  // and fragment pair) AHEAD fragments early.
+  float prs[RS ? FM : 1];
+  if constexpr (RS) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int m = wm * WM + i * 16 + lm;
+      prs[i] = m < ti.rows ? args.row_prob[ti.row0 + m] : 0.0f;
+    }
+  }
+  constexpr bool READ_CK = CK && OP == OP_FC2_DGRAD;
+  constexpr int AHEAD = 3, RING = READ_CK ? AHEAD + 1 : 1;
+  uint2 cka[RING][FN / 2], ckb[RING][FN / 2];
+  uint32_t cks[RING][FN / 2];  // the two scale bytes
+  auto ckpt_ahead = [&](auto I) __attribute__((always_inline)) {
+    constexpr int i = decltype(I)::value;
+    if constexpr (READ_CK && i < FM) {
+      const int m = wm * WM + i * 16 + lm;
+      static_for<0, FN / 2>([&](auto JP) __attribute__((always_inline)) {
+        const int col0 = ti.n0 + wn * WN + 2 * JP.value * 16;
+        if (m < ti.rows && col0 < N) {
+          const size_t row = (size_t)(ti.row0 + m);
+          const uint8_t* cq = args.ck_q + row * (2 * (size_t)f) + col0 + pc;
+          const uint8_t* cs = args.ck_s + row * (size_t)(f / 16) + col0 / 32;
+          cka[i % RING][JP.value] = *(const uint2*)cq;
+          ckb[i % RING][JP.value] = *(const uint2*)(cq + f);
+          cks[i % RING][JP.value] = (uint32_t)cs[0] | (uint32_t)cs[f / 32] << 8;
+        }
+      });
+    }
+  };
+  static_for<0, READ_CK ? AHEAD : 0>([&](auto I) __attribute__((always_inline)) { ckpt_ahead(I); });
   static_for<0, FM>([&](auto I) __attribute__((always_inline)) {
     constexpr int i = I.value;
+    ckpt_ahead(IntC<i + AHEAD>{});
     const int m = wm * WM + i * 16 + lm;  // row within the tile
     const bool row_ok = RAGGED ? (m < ti.rows) : (ti.m0 + m < M);
     float pr = 1.0f, dp = 0.0f;            // RS: the row's probability, <h, dh'> partial
-    if constexpr (RS) pr = row_ok ? args.row_prob[ti.row0 + m] : 0.0f;
+    if constexpr (RS) pr = prs[i];
     if constexpr (OP == OP_FC1_FWD && CK) {
       static_for<0, HB / 2>([&](auto JP) __attribute__((always_inline)) {
         constexpr int j0 = 2 * JP.value;
@@ -344,10 +378,9 @@ __device__ __forceinline__ void store_tile(const GemmArgs& args, const f32x4_t (
               u32x4_t av, bv;
               float ac[8], bc[8];
               if constexpr (CK) {
-                const uint8_t* cq = args.ck_q + row * (2 * (size_t)f) + col;
-                const uint8_t* cs = args.ck_s + row * (size_t)(f / 16) + col0 / 32;
-                load_ckpt(cq, cs, ac);
-                load_ckpt(cq + f, cs + f / 32, bc);
+                const uint32_t sc = cks[i % RING][JP.value];
+                load_ckpt(cka[i % RING][JP.value], sc & 0xffu, ac);
+                load_ckpt(ckb[i % RING][JP.value], sc >> 8, bc);
               } else {
                 const bf16_t* abr = (const bf16_t*)args.ab + row * (2 * (size_t)f);
                 av = *(const u32x4_t*)(abr + col);
