@@ -575,10 +575,11 @@ int moe_grouped_gemm_bwd_rowscaled(const moe_shape* sh, const int32_t* offsets, 
  * (h is recomputed).  Here it is kept as E4M3 codes with one E8M0 scale byte per
  * 32 columns of a row (the block rule of "MXFP8 expert GEMMs" with s at least
  * -126; a block with a NaN or an infinity has scale byte 255 and reads back as
- * NaN): 33/32 bytes a value in place of 2.  The forward's own results do not
- * change: h is computed from the unrounded fp32 a and b, o as in
- * moe_grouped_gemm_fwd_rowscaled, bit for bit.  The backward is that of
- * moe_grouped_gemm_bwd_rowscaled with recompute_h at the a and b that read back.
+ * NaN): 33/32 bytes a value in place of 2.  The forward's own results are those
+ * of moe_grouped_gemm_fwd_rowscaled: h comes from the unrounded fp32 a and b.
+ * The backward is that of moe_grouped_gemm_bwd_rowscaled with recompute_h at
+ * the a and b that read back.  (Both up to the order of the fp32 sums: small
+ * calls take kernels that split the contraction.)
  *
  * moe_grouped_gemm_fwd_ckpt8 -- row-scaled expert forward (probabilities before
  * W2) that writes abq uint8 [P][2f] and abs uint8 [P][2f/32] in place of ab.

@@ -150,6 +150,13 @@ __device__ __forceinline__ void pair_f32(f32x4_t& x, f32x4_t& y) {
   }
 }
 
+// An empty use of four accumulators: the products stay where they are written
+// (the compiler may otherwise sink them past a barrier, with every operand of
+// theirs live until then).
+__device__ __forceinline__ void stay(f32x4_t (&a)[4]) {
+  asm volatile("" : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]), "+v"(a[3]));
+}
+
 // Largest v over the four lanes that hold one row (lanes l, l ^ 16, l ^ 32, l ^ 48).
 __device__ __forceinline__ uint32_t row_max(uint32_t v) {
   uint32_t x = v, y = v;
@@ -221,8 +228,11 @@ __device__ __forceinline__ void load_ckpt(const uint2& w, uint32_t sc, float* v)
 // scale block, held by four lanes).  The forward rounds them from the fp32
 // accumulators, h stays that of the unrounded a and b; the backward takes a and
 // b as they read back, for the recomputed h too.
+//
+// BN: columns of a block's tile (the probability partials are one per row and
+// tile column).
 template <int OP, int FM, int FN, int WM, int WN, bool RAGGED, bool RS = false, bool LINES = false,
-          bool CK = false>
+          bool CK = false, int BN = 256>
 __device__ __forceinline__ void store_tile(const GemmArgs& args, const f32x4_t (&acc)[FM][FN],
                                            const TileInfo& ti, int M, int N, int wm, int wn,
                                            int lane, float* red = nullptr) {
@@ -450,7 +460,7 @@ __device__ __forceinline__ void store_tile(const GemmArgs& args, const f32x4_t (
     }
   });
   if constexpr (RS && OP == OP_FC2_DGRAD) {
-    constexpr int WAVES_N = 256 / WN;
+    constexpr int WAVES_N = BN / WN;
     // the partials were written with plain LDS stores, and other wavefronts
     // read them: they must have completed before the (fence-free) barrier
     __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
@@ -460,7 +470,7 @@ __device__ __forceinline__ void store_tile(const GemmArgs& args, const f32x4_t (
       float s = 0.0f;
 #pragma unroll
       for (int w = 0; w < WAVES_N; ++w) s += red[w * 256 + t];
-      args.dp_part[(size_t)(ti.row0 + t) * (size_t)((f + 255) / 256) + ti.n0 / 256] = s;
+      args.dp_part[(size_t)(ti.row0 + t) * (size_t)((f + BN - 1) / BN) + ti.n0 / BN] = s;
     }
   }
 }

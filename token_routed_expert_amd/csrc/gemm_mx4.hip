@@ -280,11 +280,6 @@ int launch_rows(const Mx4Args& a, hipStream_t s) {
 // the loads of stage kt + 2 that the block shares go there.  A wavefront's own
 // B fragments need no barrier: they are loaded as soon as the registers hold
 // the stage's, so they have almost two stages to arrive.
-// An empty use of four accumulators.
-__device__ __forceinline__ void stay(f32x4_t (&a)[4]) {
-  asm volatile("" : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]), "+v"(a[3]));
-}
-
 template <int FC, bool A8>
 __global__ __launch_bounds__(256, 2) void gemm_mx4_tile_kernel(Mx4Args args, int NT) {
   constexpr int BM = 128, BN = 256, FM = BM / 16;

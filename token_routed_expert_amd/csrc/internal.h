@@ -123,6 +123,10 @@ struct GemmArgs {
 
 // gemm_bf16.hip: MFMA kernels, bf16 in/out, fp32 accumulation
 int gemm_bf16_launch(GemmOp op, const GemmArgs& a, hipStream_t s);
+// gemm_bf16_rows.hip: the ragged-M products with the 8-bit checkpoint (fc1
+// forward and fc2 dgrad row-scaled) for few rows per expert; probability
+// partials [P][ceil(f/128)]
+int gemm_bf16_rows_launch(GemmOp op, const GemmArgs& a, hipStream_t s);
 // gemm_f32.hip: fp32 kernels
 int gemm_f32_launch(GemmOp op, const GemmArgs& a, hipStream_t s);
 // gemm_fp8.hip: e4m3 x e4m3 MFMA with fp32 block scales, bf16 outputs

@@ -290,6 +290,22 @@ int layer_bwd_rowscaled(const moe_shape* sh, const moe_layer_io* io, void* ws, s
 size_t dp_part_bytes(const moe_shape* sh) {
   return align_up((size_t)(sh->T * sh->k) * (size_t)((sh->f + 255) / 256) * sizeof(float), 256);
 }
+// Which kernels take the ragged-M products of the 8-bit checkpoint: those for few
+// rows, up to 48 rows an expert on average or while their tiles (of 64 rows,
+// 128 columns: the most a call has are fc1 forward's) give each of 256 compute
+// units at most five.  Forward and backward together, few-row kernels against
+// the 256 x 256 ones, us: 32 rows an expert, d 4096, f 1536, 128 experts 3076
+// against 3185, at 64 rows 3646 against 3515; 192 rows, d 2048, f 1408, 64
+// experts 1536 against 1130; few tiles: 256 rows, d 512, f 384, 16 experts 87
+// against 131; 256 rows, d 384, f 3840, 4 experts 158 against 309; 128 rows,
+// d 1152, f 1408, 24 experts (1584 tiles) 329 against 321.  (The few-row fc2
+// dgrad writes a probability partial per 128 columns, twice what the workspace
+// holds: they lie in dW2, which is written last, so they must fit there.)
+bool few_rows(const moe_shape* sh) {
+  const int64_t P = sh->T * sh->k;
+  if (P * (sh->f / 128) * 4 > sh->E * sh->f * sh->d * 2) return false;
+  return P <= 48 * sh->E || ((P + 63) / 64 + sh->E) * (sh->f / 64) <= 5 * 256;
+}
 int layer_combine_bwd(const moe_shape* sh, const moe_layer_io* io, void* stream);
 // [a|b] between forward and backward: bf16, or the 8-bit checkpoint (q, s)
 struct SavedAb {
@@ -677,6 +693,10 @@ int fwd_rowscaled(const moe_shape* sh, const int32_t* offsets, const RowSrc& row
   a.W1 = W1; a.W3 = W3; a.W2 = W2; a.row_prob = row_prob;
   a.ab_out = ab.ab; a.ck_q = ab.q; a.ck_s = ab.s;
   a.h_out = h; a.h = h; a.o_out = o;
+  if (ab.q && few_rows(sh)) {
+    const int st = gemm_bf16_rows_launch(OP_FC1_FWD, a, (hipStream_t)stream);
+    return st ? st : gemm_bf16_rows_launch(OP_FC2_FWD, a, (hipStream_t)stream);
+  }
   return fwd_sequence(sh, a, (hipStream_t)stream);
 }
 
@@ -692,21 +712,25 @@ int bwd_rowscaled(const moe_shape* sh, const int32_t* offsets, const RowSrc& row
   a.h = h; a.dO = dO; a.W1 = W1; a.W3 = W3; a.W2 = W2;
   a.dab_out = dab; a.dXp_out = dXp; a.dW1 = dW1; a.dW3 = dW3; a.dW2 = dW2;
   a.row_prob = row_prob;
-  a.dp_part = (float*)ws;
+  const bool few = ab.q && few_rows(sh);
+  a.dp_part = (float*)(few ? dW2 : ws);
   a.h_out = recompute_h ? h : nullptr;  // fc2 dgrad's epilogue refills h for fc2 wgrad
   hipStream_t s = (hipStream_t)stream;
   // fc2 dgrad alone is row-scaled; the other products take the plain path
-  if ((st = gemm_bf16_launch(OP_FC2_DGRAD, a, s))) return st;
+  auto dgrad = [&](GemmOp op) { return few ? gemm_bf16_rows_launch(op, a, s) : gemm_bf16_launch(op, a, s); };
+  if ((st = dgrad(OP_FC2_DGRAD))) return st;
+  auto sum_dprob = [&](int64_t cols) {  // partials of `cols` columns each
+    return dp_rows_launch(a.dp_part, (int)((sh->f + cols - 1) / cols), row_of, (int)(sh->T * sh->k), dprob, s);
+  };
+  if (few && dprob && (st = sum_dprob(128))) return st;
   a.row_prob = nullptr;
   a.h_out = nullptr;
   a.ck_q = nullptr;
   a.dab = a.dab_out;
-  if ((st = gemm_bf16_launch(OP_FC1_DGRAD, a, s))) return st;
+  if ((st = dgrad(OP_FC1_DGRAD))) return st;
   if ((st = gemm_bf16_launch(OP_FC2_WGRAD, a, s))) return st;
   if ((st = gemm_bf16_launch(OP_FC1_WGRAD, a, s))) return st;
-  if (!dprob) return MOE_OK;
-  return dp_rows_launch((const float*)ws, (int)((sh->f + 255) / 256), row_of,
-                        (int)(sh->T * sh->k), dprob, s);
+  return dprob && !few ? sum_dprob(256) : MOE_OK;
 }
 
 }  // namespace
