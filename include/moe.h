@@ -595,7 +595,9 @@ int moe_grouped_gemm_fwd_ckpt8(const moe_shape* sh, const int32_t* offsets,
  * moe_grouped_gemm_bwd_ckpt8 -- its backward from abq, abs and the unscaled
  * permuted upstream gradient dO [P][d]: h [P][f] is filled with p silu(a) b,
  * outputs dab [P][2f], dXp, dW1, dW3, dW2 and (not NULL) dprob as
- * moe_grouped_gemm_bwd_rowscaled (row_of NULL: [P] in row order, else [T][k]).
+ * moe_grouped_gemm_bwd_rowscaled (row_of NULL: [P] in row order, entries from
+ * offsets[E] on unspecified, else [T][k]).  dW2 may hold partial sums of dprob
+ * until it is written.
  * ws_bytes >= moe_workspace_bytes(sh, MOE_WS_GEMM_BWD_ROWSCALED).  Both calls:
  * bf16 only (MOE_ERR_UNSUPPORTED else), limits as moe_grouped_gemm_fwd / _bwd
  * and, with token_of, moe_grouped_gemm_fwd_gather.
@@ -750,7 +752,7 @@ int moe_dequantize_weights_mx4(const uint8_t* codes, const uint8_t* scales, int6
  * and NaN blocks as above) and o [P][d] is bf16.  xq, xs are rows as
  * moe_quantize_rows_mx4 (MOE_MXFP4) or moe_quantize_rows_mx (MOE_MXFP4_A8)
  * writes them: row r is row token_of[r] of [T] rows, or, token_of NULL, row r
- * of [P] permuted rows.  Rows of o from offsets[E] on are not written.
+ * of [P] permuted rows; an entry outside [0, T) reads a row of zeros.  Rows of o from offsets[E] on are not written.
  * ws_bytes >= moe_workspace_bytes(sh, MOE_WS_GEMM_FWD).  Errors: MOE_ERR_INVALID
  * for another dtype; MOE_ERR_UNSUPPORTED for d or f not a multiple of 128,
  * P * max(d, f) >= 2^31 - 4096 or d * f >= 2^31.

@@ -75,6 +75,19 @@ def test_layer_mode(call):
         assert fn(C.byref(s8), C.byref(io), P, 16, None) == UNS
 
 
+@pytest.mark.parametrize("call,names", [("moe_layer_fwd", ("x", "xp", "W1", "ab_q", "h", "o")),
+                                        ("moe_layer_bwd", ("xp", "ab_q", "dO", "dab", "dXp", "dW2"))])
+def test_layer_refuses_misaligned_buffers_before_enqueuing(call, names):
+    sh = make_shape(**SHAPE)
+    for odd in names:
+        io = N.moe_layer_io()
+        for n in N.IO_FIELDS:
+            if n not in ("ab", "aux_loss", "dlogits"):
+                setattr(io, n, 24 if n == odd else 16)
+        io.memory_efficient = 3
+        assert getattr(N.lib(), call)(C.byref(sh), C.byref(io), P, 1 << 40, None) == UNS, odd
+
+
 def test_misaligned_pointers():
     sh = make_shape(**SHAPE)
     odd = C.c_void_p(24)
@@ -86,3 +99,8 @@ def test_misaligned_pointers():
         a = [P, P] + [P] * 14 + [None, None]
         a[i] = odd
         assert N.lib().moe_grouped_gemm_bwd_ckpt8(C.byref(sh), *a, P, 1 << 40, None) == UNS, i
+    half = C.c_void_p(18)
+    for i in (0, 1, 6):
+        a = [P, P] + [P] * 9 + [None]
+        a[i] = half
+        assert N.lib().moe_grouped_gemm_fwd_ckpt8(C.byref(sh), *a) == UNS, i

@@ -117,6 +117,35 @@ def test_layer_refuses_before_enqueuing():
     assert lib.moe_layer_fwd(C.byref(sh), C.byref(io), P, need, None) == WS
 
 
+def test_layer_refuses_misaligned_buffers_before_enqueuing():
+    lib = N.lib()
+    sh = make_shape(**OK_SHAPE)
+    need = moe_workspace_bytes(sh, N.MOE_WS_LAYER_FWD)
+    names = ("logits", "x", "topk_idx", "topk_prob", "counts", "offsets", "row_of", "token_of", "xq",
+             "xs", "o", "y")
+    for odd, value in (("x", 24), ("xq", 24), ("o", 24), ("y", 24), ("xs", 18), ("W13", 24), ("W2s", 18)):
+        w = weights()
+        io = N.moe_layer_io()
+        for n in names:
+            setattr(io, n, 16)
+        setattr(io if odd in names else w, odd, value)
+        io.wmx4 = C.cast(C.pointer(w), C.c_void_p).value
+        assert lib.moe_layer_fwd(C.byref(sh), C.byref(io), P, need, None) == UNS, odd
+
+
+def test_python_refuses_a_stream_of_another_device():
+    from token_routed_expert_amd.ops import _Bufs
+
+    class Stream:
+        device_index, cuda_stream = 7, 64
+
+    b = _Bufs("call")
+    with pytest.raises(ValueError, match="stream is not on the current device"):
+        b.stream(Stream)
+    b.dev = 7
+    assert b.stream(Stream).value == 64
+
+
 ODD = C.c_void_p(24)  # 8-byte aligned only
 
 

@@ -233,6 +233,24 @@ def test_rows_past_the_last_expert_stay(a8):
     check(case, a8, 2, 2, 4, 256)
 
 
+@pytest.mark.parametrize("rows", [21, 300])
+@pytest.mark.parametrize("a8", [False, True], ids=["a4", "a8"])
+def test_a_token_that_there_is_not_reads_zeros(a8, rows):
+    """Entries of token_of outside [0, T): rows of zeros, their neighbours untouched."""
+    counts = [rows] if rows > 32 else [rows, 0, 0, 2]
+    E, T = len(counts), sum(counts)
+    case = product_case(counts, 384, 256, a8, rows, True)
+    o, w = run_product(case, a8, E, 1, T, 256)
+    tok = case[1].copy()
+    bad = {0: -1, 3: T, rows // 2: 2 ** 31 - 1, rows - 1: -2 ** 31}
+    for at, v in bad.items():
+        tok[at] = v
+    got, _ = run_product((case[0], tok) + case[2:], a8, E, 1, T, 256)
+    got, want = to_f64(got), to_f64(o)
+    want[list(bad)] = 0
+    assert np.array_equal(got, want)
+
+
 @pytest.mark.parametrize("rows", [5, 300])
 @pytest.mark.parametrize("a8", [False, True], ids=["a4", "a8"])
 def test_a_nan_stays_in_its_row(a8, rows):

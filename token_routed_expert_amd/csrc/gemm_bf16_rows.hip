@@ -84,7 +84,9 @@ __global__ __launch_bounds__(512, 1) void gemm_bf16_rows_kernel(GemmArgs args, i
     const int m = 4 * (w * NA + q) + (lane >> 4);
     const int c = (lane & 15) ^ (m & 15);
     const int src_row = gather ? args.gather[ti.row0 + min(m, ti.rows - 1)] : m;
-    a_off[q] = m < ti.rows ? (uint32_t)src_row * a_ld + (uint32_t)c * 16u : kPast;
+    // (a token that there is not reads as a row of zeros)
+    const bool ok = m < ti.rows && (!gather || (uint32_t)src_row < (uint32_t)args.gT);
+    a_off[q] = ok ? (uint32_t)src_row * a_ld + (uint32_t)c * 16u : kPast;
   }
 #pragma unroll
   for (int q = 0; q < NB; ++q) {

@@ -106,16 +106,18 @@ __device__ __forceinline__ void store_o(const f32x4_t (&acc)[4], bool ok, size_t
   *(u32x4_t*)(p + 32) = v1;
 }
 
-// Few rows per expert: the product is bound by reading the weights.  A block
-// of NW wavefronts takes 64 stored columns of one expert (one scale group) and
-// all its rows, 16 or 32 at a time; the wavefronts split K (wavefront w takes
-// the 128-K steps w, w + NW, ...), read the weight fragments from memory into
-// registers as they are stored, and their partial sums meet in LDS, added in
-// wavefront order.  Blocks take the experts that have rows, in order, so a
-// call with few rows launches few blocks.  The weights are read with
-// non-temporal loads (each is used once a pass; 128 experts, d 4096, f 1536, 23
-// tokens of 8 experts, E2M1 rows: fc1 107 -> 100 us, fc2 58 -> 55 us, 6.4 TB/s).  Eight wavefronts, or eight K steps
-// in flight, are slower by 5-40 %.
+// Few rows: the product is bound by reading the weights, or by latency where
+// there are few of them.  A block of NW wavefronts takes 64 stored columns of one
+// expert (one scale group) and up to 32 of its rows; the wavefronts split K
+// (wavefront w takes the 128-K steps w, w + NW, ...), read the weight fragments
+// from memory into registers as they are stored, and their partial sums meet in
+// LDS, added in wavefront order.  Blocks take the pieces of 32 rows that the
+// experts have, in order, so a call with few rows launches few blocks, and a
+// call whose rows all went to one expert spreads them (2048 rows on one of 128
+// experts, d 4096, f 1536, E2M1 rows: 117 us; one block per column group that
+// walked them all took 599 us).  The weights are read with non-temporal loads
+// (23 tokens of 8 of those experts: fc1 107 -> 100 us, fc2 58 -> 55 us,
+// 6.4 TB/s).  Eight wavefronts, or eight K steps in flight, are slower by 5-40 %.
 constexpr int NW = 4;  // wavefronts of a block, which split K
 template <int FC, bool A8>
 __global__ __launch_bounds__(NW * 64) void gemm_mx4_rows_kernel(Mx4Args args) {
@@ -125,25 +127,30 @@ __global__ __launch_bounds__(NW * 64) void gemm_mx4_rows_kernel(Mx4Args args) {
   const int K = FC == 1 ? args.d : args.f, N = FC == 1 ? 2 * args.f : args.d;
   const int KT = K >> 7, NB = N >> 6;
   const int nb = (int)blockIdx.x % NB;
-  // the expert: the (blockIdx / NB)-th one that has rows
+  // the piece: the (blockIdx / NB)-th of the experts' pieces of 32 rows, in order
   int e = -1, row0 = 0, rows = 0;
   {
     int want = (int)blockIdx.x / NB;
     for (int base = 0; base < args.E; base += 64) {
       const int x = base + lane;
       const int o0 = x < args.E ? args.offsets[x] : 0, o1 = x < args.E ? args.offsets[x + 1] : 0;
-      const uint64_t has = __ballot(o1 > o0);
-      const int n = __popcll(has);
-      if (want < n) {
-        uint64_t m = has;
-        for (int i = 0; i < want; ++i) m &= m - 1;
-        const int at = __builtin_ctzll(m);
+      const int n = (o1 - o0 + 31) >> 5;
+      int end = n;  // pieces of this expert and of those before it
+#pragma unroll
+      for (int i = 1; i < 64; i *= 2) {
+        const int v = __shfl_up(end, i, 64);
+        end += lane >= i ? v : 0;
+      }
+      const uint64_t past = __ballot(end > want);
+      if (past) {
+        const int at = __builtin_ctzll(past);
+        const int first = 32 * (want - __shfl(end - n, at, 64));
         e = base + at;
-        row0 = __shfl(o0, at, 64);
-        rows = __shfl(o1, at, 64) - row0;
+        row0 = __shfl(o0, at, 64) + first;
+        rows = min(__shfl(o1, at, 64) - row0, 32);
         break;
       }
-      want -= n;
+      want -= __shfl(end, 63, 64);
     }
   }
   e = uniform(e);
@@ -158,15 +165,23 @@ __global__ __launch_bounds__(NW * 64) void gemm_mx4_rows_kernel(Mx4Args args) {
   const uint32_t a_step = FC == 1 ? ARB : (uint32_t)args.P * ARB;  // (the whole of A: below 2^31 bytes)
   const uint32_t as_step = FC == 1 ? 4 : (uint32_t)args.P * 4;
   const size_t wstride = (size_t)KT * 1024;  // from one 16-column group to the next
-  // rows m0 .. m0 + 16 MT - 1, U K steps' loads of a wavefront in flight together
-  auto pass = [&](int m0, auto MTC, auto UC) __attribute__((always_inline)) {
+  // the rows as MT fragments of 16, U K steps' loads of a wavefront in flight together
+  auto run = [&](auto MTC, auto UC) __attribute__((always_inline)) {
     constexpr int MT = decltype(MTC)::value, U = decltype(UC)::value;
     const uint8_t *at[MT], *ast[MT];
+    bool known[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      // rows past the last are read as the last one and not stored
-      const int pr = row0 + min(m0 + 16 * t + r, rows - 1);
-      const size_t ar = FC == 1 && args.token_of ? (size_t)args.token_of[pr] : (size_t)pr;
+      // rows past the last are read as the last one and not stored; a token that
+      // there is not counts as a row of zeros
+      const int pr = row0 + min(16 * t + r, rows - 1);
+      size_t ar = (size_t)pr;
+      known[t] = true;
+      if (FC == 1 && args.token_of) {
+        const uint32_t token = (uint32_t)args.token_of[pr];
+        known[t] = token < (uint32_t)args.T;
+        ar = known[t] ? token : 0;
+      }
       at[t] = args.a + ar * a_ld + g * 16;
       ast[t] = args.as + ar * as_ld + g;
     }
@@ -211,11 +226,10 @@ __global__ __launch_bounds__(NW * 64) void gemm_mx4_rows_kernel(Mx4Args args) {
         }
       }
     }
-    __syncthreads();  // the previous rows' partial sums have been read
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) part[t][w][j][lane] = acc[t][j];
+      for (int j = 0; j < 4; ++j) part[t][w][j][lane] = known[t] ? acc[t][j] : f32x4_t{0.f, 0.f, 0.f, 0.f};
     __syncthreads();
     if (w >= MT) return;  // wavefront t stores rows 16 t ..
     f32x4_t sum[4];
@@ -230,22 +244,20 @@ __global__ __launch_bounds__(NW * 64) void gemm_mx4_rows_kernel(Mx4Args args) {
       }
       sum[j] = s;
     }
-    const int m = m0 + 16 * w + r;
+    const int m = 16 * w + r;
     const size_t row = (size_t)(row0 + m);
     if constexpr (FC == 1) store_h<A8>(sum, m < rows, row, nb * 32, (size_t)args.P, lane, args.hq, args.hs);
     else store_o(sum, m < rows, row, nb * 64, args.d, lane, (bf16_t*)args.o);
   };
-  if (rows <= 16) {
-    pass(0, IntC<1>{}, IntC<4>{});
-  } else {
-    for (int m0 = 0; m0 < rows; m0 += 32) pass(m0, IntC<2>{}, IntC<2>{});
-  }
+  if (rows <= 16) run(IntC<1>{}, IntC<4>{});
+  else run(IntC<2>{}, IntC<2>{});
 }
 
 template <int FC, bool A8>
 int launch_rows(const Mx4Args& a, hipStream_t s) {
   const int64_t NB = (FC == 1 ? 2 * (int64_t)a.f : (int64_t)a.d) / 64;
-  const int64_t grid = NB * (a.P < a.E ? a.P : a.E);
+  // at most sum_e ceil(m_e / 32) pieces, P with fewer rows than experts
+  const int64_t grid = NB * (a.P / 32 + (a.P < a.E ? a.P : a.E));
   if (grid > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
   gemm_mx4_rows_kernel<FC, A8><<<(unsigned)grid, NW * 64, 0, s>>>(a);
   TRE_LAUNCH_CHECK();
@@ -317,9 +329,12 @@ __global__ __launch_bounds__(256, 2) void gemm_mx4_tile_kernel(Mx4Args args, int
   const rsrc_t b_src = make_rsrc(args.w + ((size_t)e * (N >> 4) + (size_t)(colc >> 4)) * KT * 1024, b_size);
   const rsrc_t bs_src = make_rsrc(args.ws + ((size_t)e * (N >> 6) + (size_t)(colc >> 6)) * KT * 256, b_size / 16);
   constexpr uint32_t kPast = 0x80000000u;       // past every range
-  auto row_of = [&](int m) __attribute__((always_inline)) -> uint32_t {  // source row of tile row m
+  // offset of tile row m's source row; none for rows past the last and for a
+  // token that there is not
+  auto row_at = [&](int m, uint32_t ld, uint32_t at) __attribute__((always_inline)) -> uint32_t {
     const int pr = row0 + min(m, rows - 1);
-    return gather ? (uint32_t)args.token_of[pr] : (uint32_t)pr;
+    const uint32_t row = gather ? (uint32_t)args.token_of[pr] : (uint32_t)pr;
+    return m < rows && row < a_rows ? row * ld + at : kPast;
   };
   uint32_t a_off[NA];
 #pragma unroll
@@ -327,7 +342,7 @@ __global__ __launch_bounds__(256, 2) void gemm_mx4_tile_kernel(Mx4Args args, int
     const int t = w * NA + q;                   // load t: 1 KB of A rows
     const int m = ARB == 128 ? 8 * t + (lane >> 3) : 16 * t + (lane >> 2);
     const int c = ARB == 128 ? (lane & 7) ^ ((m >> 1) & 7) : (lane & 3) ^ ((m >> 1) & 3);
-    a_off[q] = m < rows ? row_of(m) * a_ld + (uint32_t)c * 16u : kPast;
+    a_off[q] = row_at(m, a_ld, (uint32_t)c * 16u);
   }
   // A scales.  fc1: the wavefront's 16 rows of either half of the tile, a lane
   // one of a row's four words; fc2: wavefronts 0 and 1, 64 rows each
@@ -335,7 +350,7 @@ __global__ __launch_bounds__(256, 2) void gemm_mx4_tile_kernel(Mx4Args args, int
 #pragma unroll
   for (int q = 0; q < (FC == 1 ? 2 : 1); ++q) {
     const int m = FC == 1 ? 64 * q + 16 * w + (lane >> 2) : 64 * (w & 1) + lane;
-    as_off[q] = m < rows ? row_of(m) * as_ld + (FC == 1 ? (uint32_t)(lane & 3) * 4u : 0u) : kPast;
+    as_off[q] = row_at(m, as_ld, FC == 1 ? (uint32_t)(lane & 3) * 4u : 0u);
   }
   const uint32_t lane16 = (uint32_t)lane * 16u, lane4 = (uint32_t)lane * 4u;
   const uint32_t lds_base = (uint32_t)uniform((int)(uint32_t)(size_t)LDS_PTR(lds));

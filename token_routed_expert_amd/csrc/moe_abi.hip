@@ -317,6 +317,15 @@ SavedAb saved_of(const moe_layer_io* io) {
                                    : SavedAb{io->ab, nullptr, nullptr};
 }
 bool saved_ok(const SavedAb& v) { return v.ab || (v.q && v.s); }
+// Alignment of a checkpointed layer's buffers, before its first launch.
+int check_ckpt(const moe_layer_io* io) {
+  if (io->memory_efficient != 3) return MOE_OK;
+  const void* const p[] = {io->x,  io->xp, io->W1, io->W3,  io->W2,  io->h,   io->o,  io->dO,
+                           io->dab, io->dXp, io->dW1, io->dW3, io->dW2, io->ab_q};
+  for (const void* q : p)
+    if (!aligned(16, (const char*)q)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
 int fwd_rowscaled(const moe_shape* sh, const int32_t* offsets, const RowSrc& rows, const void* W1,
                   const void* W3, const void* W2, const float* row_prob, const SavedAb& ab, void* h,
                   void* o, void* stream);
@@ -648,7 +657,8 @@ int moe_grouped_gemm_fwd_ckpt8(const moe_shape* sh, const int32_t* offsets,
   if (!offsets || !x || !W1 || !W3 || !W2 || !row_prob || !abq || !abs || !h || !o)
     return MOE_ERR_INVALID;
   if (!aligned(16, (const char*)x, (const char*)W1, (const char*)W3, (const char*)W2,
-               (const char*)abq, (const char*)h, (const char*)o))
+               (const char*)abq, (const char*)h, (const char*)o) ||
+      !aligned(4, offsets, token_of, (const int32_t*)row_prob))
     return MOE_ERR_UNSUPPORTED;
   return fwd_rowscaled(sh, offsets,
                        token_of ? RowSrc{nullptr, token_of, x} : RowSrc{x, nullptr, nullptr}, W1, W3,
@@ -671,7 +681,9 @@ int moe_grouped_gemm_bwd_ckpt8(const moe_shape* sh, const int32_t* offsets,
     return MOE_ERR_INVALID;
   if (!aligned(16, (const char*)x, (const char*)abq, (const char*)dO, (const char*)W1,
                (const char*)W3, (const char*)W2, (const char*)h, (const char*)dab,
-               (const char*)dXp, (const char*)dW1, (const char*)dW3, (const char*)dW2))
+               (const char*)dXp, (const char*)dW1, (const char*)dW3, (const char*)dW2,
+               (const char*)ws) ||
+      !aligned(4, offsets, token_of, row_of, (const int32_t*)row_prob, (const int32_t*)dprob))
     return MOE_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < dp_part_bytes(sh)) return MOE_ERR_WORKSPACE;
   return bwd_rowscaled(sh, offsets,
@@ -1158,6 +1170,10 @@ int layer_fwd_mx4(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t 
       !io->row_of || !io->token_of || !io->xq || !io->xs || !io->o || !io->y)
     return MOE_ERR_INVALID;
   if (io->memory_efficient) return MOE_ERR_UNSUPPORTED;
+  if (!aligned(16, (const char*)io->x, io->xq, io->wmx4->W13, io->wmx4->W2, (const char*)io->o,
+               (const char*)io->y, (const char*)ws) ||
+      !aligned(4, (const char*)io->xs, io->wmx4->W13s, io->wmx4->W2s))
+    return MOE_ERR_UNSUPPORTED;
   const size_t pws = permute_ws_bytes(sh->T, sh->E);
   const size_t gws = mx4_ws_bytes(sh);
   if (!ws || ws_bytes < pws + gws || !aux_ws_ok(sh, io, ws_bytes)) return MOE_ERR_WORKSPACE;
@@ -1305,6 +1321,7 @@ int layer_fwd_rowscaled(const moe_shape* sh, const moe_layer_io* io, void* ws, s
       !io->y || !io->row_prob)
     return MOE_ERR_INVALID;
   if (io->fused_permute && (st = check_gather(sh))) return st;
+  if ((st = check_ckpt(io))) return st;
   if (sh->f_shared &&
       (!io->Ws1 || !io->Ws3 || !io->Ws2 || !io->s_ab || !io->s_h || !io->ys))
     return MOE_ERR_INVALID;
@@ -1348,6 +1365,7 @@ int layer_bwd_rowscaled(const moe_shape* sh, const moe_layer_io* io, void* ws, s
     return MOE_ERR_INVALID;
   if (io->fused_permute ? (!io->token_of || !io->x) : !io->xp) return MOE_ERR_INVALID;
   if (io->fused_permute && (st = check_gather(sh))) return st;
+  if ((st = check_ckpt(io))) return st;
   if (sh->f_shared && (!io->x || !io->Ws1 || !io->Ws3 || !io->Ws2 || !io->s_ab || !io->s_h ||
                        !io->s_dab || !io->dXs || !io->dWs1 || !io->dWs3 || !io->dWs2))
     return MOE_ERR_INVALID;

@@ -74,6 +74,11 @@ class _Bufs:
     def opt(self, name, t, dtype, numel, align=16):
         return None if t is None else self(name, t, dtype, numel, align)
 
+    def stream(self, stream):
+        if stream is not None and stream.device_index != self.dev:
+            raise ValueError(f"{self.call}: the stream is not on the current device")
+        return _stream(stream)
+
 
 def _check(status, call):
     if status != N.MOE_OK:
@@ -336,7 +341,7 @@ def moe_quantize_rows_mx4(src, codes, scales, stream=None):
     code, b, n = _src_dtype(call, src), _Bufs(call), rows * cols
     _check(N.lib().moe_quantize_rows_mx4(b("src", src, src.dtype, n), code, rows, cols,
                                          b("codes", codes, U8, n // 2),
-                                         b("scales", scales, U8, n // 32, 1), _stream(stream)), call)
+                                         b("scales", scales, U8, n // 32, 1), b.stream(stream)), call)
 
 
 def moe_quantize_weights_mx4(W, W_pair, codes, scales, stream=None):
@@ -351,7 +356,7 @@ def moe_quantize_weights_mx4(W, W_pair, codes, scales, stream=None):
     _check(N.lib().moe_quantize_weights_mx4(b("W", W, W.dtype, one),
                                             b.opt("W_pair", W_pair, W.dtype, one), code, E, R, Cc,
                                             b("codes", codes, U8, n // 2),
-                                            b("scales", scales, U8, n // 32, 1), _stream(stream)),
+                                            b("scales", scales, U8, n // 32, 1), b.stream(stream)),
            call)
 
 
@@ -366,7 +371,7 @@ def moe_dequantize_weights_mx4(codes, scales, W, W_pair=None, stream=None):
     _check(N.lib().moe_dequantize_weights_mx4(b("codes", codes, U8, n // 2),
                                               b("scales", scales, U8, n // 32, 1), E, R, Cc,
                                               b("W", W, BF16, one), b.opt("W_pair", W_pair, BF16, one),
-                                              _stream(stream)), call)
+                                              b.stream(stream)), call)
 
 
 class MX4Weights:
@@ -395,8 +400,8 @@ def moe_grouped_gemm_fwd_mx4(sh, offsets, token_of, xq, xs, w: MX4Weights, o, ws
     _check(N.lib().moe_grouped_gemm_fwd_mx4(
         C.byref(sh), b("offsets", offsets, I32, E + 1, 4), b.opt("token_of", token_of, I32, P, 4),
         b("xq", xq, U8, rows * d // (2 if sh.dtype == N.MOE_MXFP4 else 1)),
-        b("xs", xs, U8, rows * d // 32), C.byref(w.struct), b("o", o, BF16, P * d),
-        None if ws is None else b("ws", ws, ws.dtype, 0), _nbytes(ws), _stream(stream)), call)
+        b("xs", xs, U8, rows * d // 32, 4), C.byref(w.struct), b("o", o, BF16, P * d),
+        None if ws is None else b("ws", ws, ws.dtype, 0), _nbytes(ws), b.stream(stream)), call)
 
 
 def _io(buffers: dict) -> N.moe_layer_io:
@@ -462,7 +467,7 @@ def moe_grouped_gemm_fwd_ckpt8(sh, offsets, token_of, x, W1, W3, W2, row_prob, a
     _check(N.lib().moe_grouped_gemm_fwd_ckpt8(
         C.byref(sh), *_ckpt_inputs(b, sh, offsets, token_of, x, W1, W3, W2, row_prob),
         b("abq", abq, U8, P * 2 * sh.f), b("abs", abs_, U8, P * sh.f // 16, 1),
-        b("h", h, BF16, P * sh.f), b("o", o, BF16, P * sh.d), _stream(stream)), call)
+        b("h", h, BF16, P * sh.f), b("o", o, BF16, P * sh.d), b.stream(stream)), call)
 
 
 def moe_grouped_gemm_bwd_ckpt8(sh, offsets, token_of, x, abq, abs_, dO, W1, W3, W2, row_prob, h, dab,
@@ -478,7 +483,7 @@ def moe_grouped_gemm_bwd_ckpt8(sh, offsets, token_of, x, abq, abs_, dO, W1, W3, 
         b("h", h, BF16, P * sh.f), b("dab", dab, BF16, P * 2 * sh.f), b("dXp", dXp, BF16, P * sh.d),
         b("dW1", dW1, BF16, mat), b("dW3", dW3, BF16, mat), b("dW2", dW2, BF16, mat),
         b.opt("row_of", row_of, I32, P, 4), b.opt("dprob", dprob, F32, P, 4),
-        None if ws is None else b("ws", ws, ws.dtype, 0), _nbytes(ws), _stream(stream)), call)
+        None if ws is None else b("ws", ws, ws.dtype, 0), _nbytes(ws), b.stream(stream)), call)
 
 
 def moe_aux_loss(logits, k, counts, alpha, loss, ws, stream=None):
