@@ -20,8 +20,16 @@
 // that prefix.  One persistent block per compute unit walks the tile numbers
 // with a stride of the grid; numbers past the device-side count end it.
 // Block ids are remapped so that the blocks one XCD runs at a time (ids with
-// the same value mod 8) take consecutive tiles: they share A rows and expert
-// weights in that XCD's L2.  Weight-gradient products have a fixed grid of
+// the same value mod 8) take consecutive tiles (8 for the data gradients, 32
+// else): they share A rows and expert weights in that XCD's L2.  All XCDs move
+// through the tile list together, where an eighth of the list for each left the
+// XCDs with the large experts to finish alone and set the others on matrices
+// whole experts apart.  An eighth each against this, us, weight gradients fc1
+// and fc2 and data gradients fc2 and fc1: 8 experts, d 4096, f 14336, 8192 rows
+// 2065 924 1162 2208 against 1786 921 1068 1958 (forward 2064 and 1065 against
+// 1770 and 1024); 64 experts, d 2048, f 1408, 12306 rows of which one expert has
+// 1912: 391 210 211 245 against 322 190 211 246; 128 experts, d 4096, f 1536,
+// 65536 rows even: 1901 950 1052 1626 against 1944 958 1044 1631.  Weight-gradient products have a fixed grid of
 // E x (M/BM) x (N/BN) tiles; K is the expert's row count, 0 for an empty
 // expert, which then writes zeros.
 //
@@ -195,7 +203,7 @@ __global__ __launch_bounds__(NW * 64, 1) void gemm_bf16_kernel(GemmArgs args, in
   else total = args.E * MT * NT;
   total = uniform(total);
   auto decode = [&](int slot, TileInfo& ti) __attribute__((always_inline)) {
-    const int logical = xcd_remap(slot, total);
+    const int logical = xcd_remap_rounds<TR::b_kcontig ? 8 : 32>(slot, total);
     if constexpr (TR::ragged_m) {
       ragged_tile(offs, mt_incl, args.E, NT, BM, logical, ti);
       ti.n0 *= BN;

@@ -20,6 +20,16 @@ __device__ __forceinline__ int xcd_remap(int i, int n) {
   return x * q + min(x, r) + j;
 }
 
+// The same in rounds of 8 C tiles: an XCD takes C consecutive ones of each
+// round, so that tiles of unequal work spread over the XCDs; what is left after
+// the last whole round is divided as above.
+template <int C>
+__device__ __forceinline__ int xcd_remap_rounds(int i, int n) {
+  const int whole = n / (8 * C) * (8 * C);
+  if (i >= whole) return whole + xcd_remap(i - whole, n - whole);
+  return i / (8 * C) * (8 * C) + (i & 7) * C + (i >> 3) % C;
+}
+
 struct TileInfo {
   int e;     // expert
   int row0;  // first permuted row of the tile (ragged M) or of the expert (wgrad)
