@@ -233,6 +233,37 @@ def test_rows_past_the_last_expert_stay(a8):
     check(case, a8, 2, 2, 4, 256)
 
 
+@pytest.mark.parametrize("per_expert", [8, 100])
+@pytest.mark.parametrize("a8", [False, True], ids=["a4", "a8"])
+def test_repeated_calls_give_the_same_bits(a8, per_expert):
+    """Many tiles with few K steps, over and over: a load that is read before it has
+    landed (its slot then holds what an earlier call left) shows as another result."""
+    import token_routed_expert_amd as tre
+    E, k, d, f = 96, 8, 384, 1152
+    T = E * per_expert // k
+    g = torch.Generator(device="cuda").manual_seed(5)
+    dev = dict(dtype=torch.uint8, device="cuda")
+    sh = tre.make_shape(T, d, E, k, f, dtype="mxfp4_a8" if a8 else "mxfp4")
+    rnd = lambda lo, hi, *n: torch.randint(lo, hi, n, generator=g, **dev)
+    # (scales that differ from block to block, around 2^-4)
+    w = tre.MX4Weights({"W13": rnd(0, 256, E, d * f), "W2": rnd(0, 256, E, d * f // 2),
+                        "W13s": rnd(121, 126, E, d * f // 16), "W2s": rnd(121, 126, E, d * f // 32)})
+    off = torch.arange(0, E + 1, dtype=torch.int32, device="cuda") * per_expert
+    ws = torch.empty(tre.moe_workspace_bytes(sh, tre.MOE_WS_GEMM_FWD), **dev)
+    xs = rnd(121, 126, T, d // 32)
+    tok = torch.randint(0, T, (T * k,), generator=g, device="cuda", dtype=torch.int32)
+    xq = [rnd(0, 120 if a8 else 256, T, d if a8 else d // 2) for _ in range(2)]
+    o = torch.empty(T * k, d, dtype=torch.bfloat16, device="cuda")
+    first = [None, None]
+    for i in range(400):
+        tre.moe_grouped_gemm_fwd_mx4(sh, off, tok, xq[i & 1], xs, w, o, ws)
+        if i < 2:
+            first[i] = o.clone()
+            assert torch.isfinite(o).all()
+        else:
+            assert torch.equal(o, first[i & 1]), f"call {i}"
+
+
 @pytest.mark.parametrize("rows", [21, 300])
 @pytest.mark.parametrize("a8", [False, True], ids=["a4", "a8"])
 def test_a_token_that_there_is_not_reads_zeros(a8, rows):

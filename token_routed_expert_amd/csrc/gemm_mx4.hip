@@ -307,7 +307,7 @@ __global__ __launch_bounds__(256, 2) void gemm_mx4_tile_kernel(Mx4Args args, int
   __shared__ __attribute__((aligned(1024))) char lds[AS4_AT + 2 * AS4_BYTES];
   __shared__ int sched[8];
   TileInfo ti;
-  if (!decode_ragged_m<BM, 4>(args.offsets, args.E, NT, sched, ti)) return;
+  if (!decode_ragged_m<BM, 4, 32>(args.offsets, args.E, NT, sched, ti)) return;
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int w = uniform((int)threadIdx.x >> 6);
   const int e = uniform(ti.e), row0 = uniform(ti.row0), rows = uniform(ti.rows);
@@ -451,7 +451,9 @@ __global__ __launch_bounds__(256, 2) void gemm_mx4_tile_kernel(Mx4Args args, int
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  // both slots, in the order in which the stages issue them
+  // both slots, in the order and number in which the stages issue them (PAIR: the
+  // B scales of stage 1 twice, in the place of the load that a stage issues after
+  // them: the waits count it)
   if constexpr (FC == 1) {
     issue_as4(0, 0);
     issue_as4(0, 1);
@@ -460,10 +462,11 @@ __global__ __launch_bounds__(256, 2) void gemm_mx4_tile_kernel(Mx4Args args, int
     static_for<0, 4>([&](auto J) __attribute__((always_inline)) { issue_b(S.value, S.value, J.value); });
     issue_bs(S.value, S.value);
     if constexpr (FC == 2) issue_as(S.value - 2, S.value);
+    if constexpr (PAIR && S.value == 1) issue_bs(S.value, S.value);
     static_for<0, NA>([&](auto Q) __attribute__((always_inline)) { issue_a(S.value, S.value, Q.value); });
   });
   constexpr int OWN = 5;                        // a stage's loads before the barrier
-  wait_vmcnt<OWN + NA + (FC == 2 ? 1 : 0)>();
+  wait_vmcnt<OWN + NA + (FC == 2 || PAIR ? 1 : 0)>();
   block_barrier();
 
   typename Frag<A8>::type xf[4];                // A fragments in flight: i & 3

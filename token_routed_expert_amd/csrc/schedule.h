@@ -40,10 +40,11 @@ struct TileInfo {
 
 // Ragged-M decode for a block of NWAVES wavefronts and E <= 64 * NWAVES
 // experts: expert e owns ceil(m_e / BM) M-tiles; tiles are numbered
-// expert-major.  `scratch` is >= NWAVES + 4 ints of shared memory.
+// expert-major; an XCD takes an eighth of them, or, C > 0, C at a time.
+// `scratch` is >= NWAVES + 4 ints of shared memory.
 // Returns false (uniformly for the block) when the block id is past the
 // device-side tile count.
-template <int BM, int NWAVES = 4>
+template <int BM, int NWAVES = 4, int C = 0>
 __device__ __forceinline__ bool decode_ragged_m(const int32_t* __restrict__ offsets, int E, int NT,
                                                 int* scratch, TileInfo& ti) {
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
@@ -69,7 +70,9 @@ __device__ __forceinline__ bool decode_ragged_m(const int32_t* __restrict__ offs
   }
   const int total = total_m * NT;
   if ((int)blockIdx.x >= total) return false;
-  const int logical = xcd_remap(blockIdx.x, total);
+  int logical;
+  if constexpr (C > 0) logical = xcd_remap_rounds<C>(blockIdx.x, total);
+  else logical = xcd_remap(blockIdx.x, total);
   // expert e owns logical tiles [excl * NT, (excl + c) * NT), N-tile-major
   // with the M-tile fastest: tiles that share an expert's weight strip run
   // side by side, and a split across dispatch rounds re-reads the (smaller)
