@@ -291,20 +291,33 @@ size_t dp_part_bytes(const moe_shape* sh) {
   return align_up((size_t)(sh->T * sh->k) * (size_t)((sh->f + 255) / 256) * sizeof(float), 256);
 }
 // Which kernels take the ragged-M products of the 8-bit checkpoint: those for few
-// rows, up to 48 rows an expert on average or while their tiles (of 64 rows,
-// 128 columns: the most a call has are fc1 forward's) give each of 256 compute
-// units at most five.  Forward and backward together, few-row kernels against
-// the 256 x 256 ones, us: 32 rows an expert, d 4096, f 1536, 128 experts 3076
-// against 3185, at 64 rows 3646 against 3515; 192 rows, d 2048, f 1408, 64
-// experts 1536 against 1130; few tiles: 256 rows, d 512, f 384, 16 experts 87
-// against 131; 256 rows, d 384, f 3840, 4 experts 158 against 309; 128 rows,
-// d 1152, f 1408, 24 experts (1584 tiles) 329 against 321.  (The few-row fc2
-// dgrad writes a probability partial per 128 columns, twice what the workspace
-// holds: they lie in dW2, which is written last, so they must fit there.)
+// rows (tiles of 64 x 128) up to 32 rows an expert on average, where both read
+// the weights for most of their time, and beyond that while their tiles, in
+// rounds of one to each of 256 compute units (at least one, however few the
+// tiles) and weighted with the steps of a tile's contraction, are at most 2.75
+// times those of the 256 x 256 kernels, whose step takes about that much longer.
+// Forward and backward together, few-row kernels against the others, us: 128
+// experts, d 4096, f 1536: 32 rows an expert 3060 against 3213, 64 rows 3593
+// against 3405; 8 experts, d 4096, f 14336: 45 rows 1881 against 2238, 175 rows
+// 3287 against 2707; 16 experts, d 512, f 384: 500 rows 129 against 143, 875 rows
+// 180 against 161; 4 experts, d 384, f 3840: 600 rows 225 against 334, 2400 rows
+// 712 against 593; 24 experts, d 1152, f 1408: 125 rows 308 against 321, 183 rows
+// 365 against 343.
+// (The few-row fc2 dgrad writes a probability partial per 128 columns, twice what
+// the workspace holds: they lie in dW2, which is written last, so they must fit
+// there.)
 bool few_rows(const moe_shape* sh) {
-  const int64_t P = sh->T * sh->k;
-  if (P * (sh->f / 128) * 4 > sh->E * sh->f * sh->d * 2) return false;
-  return P <= 48 * sh->E || ((P + 63) / 64 + sh->E) * (sh->f / 64) <= 5 * 256;
+  const int64_t P = sh->T * sh->k, d = sh->d, f = sh->f;
+  if (P * (f / 128) * 4 > sh->E * f * d * 2) return false;
+  if (P <= 32 * sh->E) return true;
+  auto steps = [&](double bm, int64_t bn) {  // an expert's last row tile is half full on average
+    const double row_tiles = (double)P / bm + 0.5 * (double)std::min(P, sh->E);
+    double sum = 0;
+    const int64_t nk[4][2] = {{2 * f, d}, {d, f}, {f, d}, {d, 2 * f}};
+    for (const auto& p : nk) sum += std::max(1.0, row_tiles * (double)((p[0] + bn - 1) / bn) / 256.0) * (double)p[1];
+    return sum;
+  };
+  return steps(64, 128) <= 2.75 * steps(256, 256);
 }
 int layer_combine_bwd(const moe_shape* sh, const moe_layer_io* io, void* stream);
 // [a|b] between forward and backward: bf16, or the 8-bit checkpoint (q, s)
