@@ -252,6 +252,17 @@ def test_backward_is_the_rowscaled_one_on_the_kept_values():
     assert torch.equal(dpa, dp) and torch.equal(dpb, dp)
 
 
+@pytest.mark.parametrize("counts,d,f", [([70] * 16, 384, 640), ([300, 0, 24700], 128, 640)], ids=["few", "many"])
+def test_repeated_calls_give_the_same_bits(counts, d, f):
+    c = Case(counts, d, f, seed=11)
+    q, s = checkpoint(c, 4)
+    ref, (out, dp, _) = forward(c, True), backward(c, q, s, True)
+    for _ in range(20):
+        assert all(torch.equal(a, b) for a, b in zip(ref, forward(c, True)))
+        again, dq, _ = backward(c, q, s, True)
+        assert torch.equal(dp, dq) and all(torch.equal(out[n], again[n]) for n in out)
+
+
 def test_dprob_order_and_absence():
     c = Case([40, 9], 128, 128, seed=1)
     q, s = checkpoint(c, 2)

