@@ -20,18 +20,23 @@
 // that prefix.  One persistent block per compute unit walks the tile numbers
 // with a stride of the grid; numbers past the device-side count end it.
 // Block ids are remapped so that the blocks one XCD runs at a time (ids with
-// the same value mod 8) take consecutive tiles (8 for the data gradients, 32
-// else): they share A rows and expert weights in that XCD's L2.  All XCDs move
-// through the tile list together, where an eighth of the list for each left the
-// XCDs with the large experts to finish alone and set the others on matrices
-// whole experts apart.  An eighth each against this, us, weight gradients fc1
-// and fc2 and data gradients fc2 and fc1: 8 experts, d 4096, f 14336, 8192 rows
-// 2065 924 1162 2208 against 1786 921 1068 1958 (forward 2064 and 1065 against
-// 1770 and 1024); 64 experts, d 2048, f 1408, 12306 rows of which one expert has
-// 1912: 391 210 211 245 against 322 190 211 246; 128 experts, d 4096, f 1536,
-// 65536 rows even: 1901 950 1052 1626 against 1944 958 1044 1631.  Weight-gradient products have a fixed grid of
-// E x (M/BM) x (N/BN) tiles; K is the expert's row count, 0 for an empty
-// expert, which then writes zeros.
+// the same value mod 8) take consecutive tiles: they share A rows and expert
+// weights in that XCD's L2.  Either each XCD has an eighth of the tile list, or,
+// with up to 16 experts, all XCDs move through the list together, 8 (data
+// gradients) or 32 tiles each at a time: an eighth would set them on matrices
+// whole experts apart.  8 experts, d 4096, f 14336, 8192 rows, an eighth against
+// together, us: forward 1950 and 1027 against 1712 and 1006, fc2 and fc1 data
+// gradients 1086 and 2154 against 1041 and 2015, weight gradients 917 and 2042
+// against 940 and 1735; 256 experts, d 7168, f 2048, 131072 rows: fc1 forward 7712
+// against 8260, its data gradient 7995 against 8425; one expert, 16384 rows: fc1
+// forward 828 against 890, its data gradient 817 against 715.  The weight
+// gradients, whose tiles take as long as their expert has rows, also go together
+// when an eighth of the experts has 5/4 of an eighth of the rows: 64 experts, d
+// 2048, f 1408, 12306 rows of which one expert has 1912: 210 and 391 against 190
+// and 322; 128 even experts, d 4096, f 1536, 65536 rows: 977 and 1885 against 1000
+// and 1925.
+// Weight-gradient products have a fixed grid of E x (M/BM) x (N/BN) tiles; K is
+// the expert's row count, 0 for an empty expert, which then writes zeros.
 //
 // Block tile 256 x 256, 8 wavefronts in a 2x4 grid, each owning a 128 x 64
 // sub-tile of 16x16 MFMA blocks (v_mfma_f32_16x16x32_bf16, fp32 accumulators).  K advances in stages of 32 through a 4-deep LDS ring (32 KB per
@@ -202,8 +207,17 @@ __global__ __launch_bounds__(NW * 64, 1) void gemm_bf16_kernel(GemmArgs args, in
   if constexpr (TR::ragged_m) total = mtile_prefix<BM, NW>(offs, args.E, mt_incl, sched) * NT;
   else total = args.E * MT * NT;
   total = uniform(total);
+  // An eighth of the tile list for each XCD, or all XCDs together (see above)
+  bool rounds = args.E <= 16 && (TR::b_kcontig || args.E > 1);
+  if constexpr (!TR::ragged_m) {
+    int most = 0;  // rows of the XCD with the most, an eighth of the experts each
+    for (int x = 0; x < 8; ++x)
+      most = max(most, offs[(x + 1) * args.E / 8] - offs[x * args.E / 8]);
+    rounds = rounds || (int64_t)most * 32 > (int64_t)offs[args.E] * 5;
+  }
+  rounds = uniform(rounds);
   auto decode = [&](int slot, TileInfo& ti) __attribute__((always_inline)) {
-    const int logical = xcd_remap_rounds<TR::b_kcontig ? 8 : 32>(slot, total);
+    const int logical = rounds ? xcd_remap_rounds<TR::b_kcontig ? 8 : 32>(slot, total) : xcd_remap(slot, total);
     if constexpr (TR::ragged_m) {
       ragged_tile(offs, mt_incl, args.E, NT, BM, logical, ti);
       ti.n0 *= BN;
