@@ -143,7 +143,7 @@ def test_python_refuses_a_stream_of_another_device():
     with pytest.raises(ValueError, match="stream is not on the current device"):
         b.stream(Stream)
     b.dev = 7
-    assert b.stream(Stream).value == 64
+    assert b.stream(Stream) == 64
 
 
 ODD = C.c_void_p(24)  # 8-byte aligned only

@@ -422,5 +422,12 @@ def test_python_refuses_short_and_misaligned_tensors():
             tre.moe_grouped_gemm_fwd_mx4(sh, a["off"], None, a["xq"], a["xs"], w, a["o"], ws)
     with pytest.raises(tre.MoeError):
         tre.moe_grouped_gemm_fwd_mx4(sh, off, None, xq, xs, w, o, None)
+    for name in w.NAMES:
+        short = tre.MX4Weights({**w.tensors, name: w[name].flatten()[:-16]})
+        with pytest.raises(ValueError, match="elements"):
+            tre.moe_grouped_gemm_fwd_mx4(sh, off, None, xq, xs, short, o, ws)
+        host = tre.MX4Weights({**w.tensors, name: w[name].cpu()})
+        with pytest.raises(ValueError, match="device"):
+            tre.moe_grouped_gemm_fwd_mx4(sh, off, None, xq, xs, host, o, ws)
     torch.cuda.synchronize()
     assert not o.float().abs().max()          # zero rows give zeros

@@ -53,9 +53,18 @@ class _Bufs:
 
     def __init__(self, call):
         self.call = call
-        self.dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+        self.dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
 
     def __call__(self, name, t, dtype, numel, align=16):
+        # (one condition where nothing is wrong: a call has up to 19 tensors)
+        if (type(t) is torch.Tensor and t.dtype is dtype and t.numel() >= numel and t.is_contiguous()
+                and t.get_device() == self.dev):
+            p = t.data_ptr()
+            if p % align == 0:
+                return p
+        return self._refuse(name, t, dtype, numel, align)
+
+    def _refuse(self, name, t, dtype, numel, align):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{self.call}: {name}: expected a torch.Tensor, got {type(t)}")
         if t.dtype != dtype:
@@ -64,20 +73,21 @@ class _Bufs:
             raise ValueError(f"{self.call}: {name} must be contiguous")
         if t.numel() < numel:
             raise ValueError(f"{self.call}: {name} has {t.numel()} elements, {numel} are needed")
-        if t.get_device() != self.dev or self.dev < 0:
+        if t.get_device() != self.dev:
             raise ValueError(f"{self.call}: {name} is not on the current device")
-        p = t.data_ptr()
-        if p % align:
+        if t.data_ptr() % align:
             raise ValueError(f"{self.call}: {name} is not aligned to {align} bytes")
-        return p
+        return t.data_ptr()  # a subclass (a parameter)
 
     def opt(self, name, t, dtype, numel, align=16):
         return None if t is None else self(name, t, dtype, numel, align)
 
     def stream(self, stream):
-        if stream is not None and stream.device_index != self.dev:
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.dev)
+        if stream.device_index != self.dev:
             raise ValueError(f"{self.call}: the stream is not on the current device")
-        return _stream(stream)
+        return stream.cuda_stream
 
 
 def _check(status, call):
@@ -382,6 +392,9 @@ class MX4Weights:
     def __init__(self, tensors: dict):
         self.tensors = {n: tensors[n] for n in self.NAMES}
         self.struct = N.moe_mx4_weights(*[_ptr(self.tensors[n], U8).value for n in self.NAMES])
+        self.numels = tuple(t.numel() for t in self.tensors.values())
+        devices = {t.get_device() for t in self.tensors.values()}
+        self.device = devices.pop() if len(devices) == 1 else -1
 
     def __getitem__(self, name):
         return self.tensors[name]
@@ -392,11 +405,15 @@ def moe_grouped_gemm_fwd_mx4(sh, offsets, token_of, xq, xs, w: MX4Weights, o, ws
     token_of[r] of xq, or row r when token_of is None); o [P][d] bf16."""
     call = "moe_grouped_gemm_fwd_mx4"
     b = _Bufs(call)
-    T, d, E, f, P = sh.T, sh.d, sh.E, sh.f, sh.T * sh.k
+    T, d, E, f = sh.T, sh.d, sh.E, sh.f
+    P, mat = T * sh.k, E * d * f
     rows = P if token_of is None else T
-    mat = E * d * f
-    b("W13", w["W13"], U8, mat), b("W2", w["W2"], U8, mat // 2)
-    b("W13s", w["W13s"], U8, mat // 16), b("W2s", w["W2s"], U8, mat // 32)
+    n13, n2, n13s, n2s = w.numels
+    if n13 < mat or 2 * n2 < mat or 16 * n13s < mat or 32 * n2s < mat:
+        raise ValueError(f"{call}: W13, W2 and their scales have {w.numels} elements, "
+                         f"{(mat, mat // 2, mat // 16, mat // 32)} are needed")
+    if w.device != b.dev:
+        raise ValueError(f"{call}: the weights are not on the current device")
     _check(N.lib().moe_grouped_gemm_fwd_mx4(
         C.byref(sh), b("offsets", offsets, I32, E + 1, 4), b.opt("token_of", token_of, I32, P, 4),
         b("xq", xq, U8, rows * d // (2 if sh.dtype == N.MOE_MXFP4 else 1)),
