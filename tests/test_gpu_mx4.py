@@ -139,12 +139,12 @@ def run_product(case, a8, E, k, T, f):
 
 
 def cut(X, W):
-    """7 * 2^-13 * sum over groups of 8 k of max |X[:, k] W[k, :]|."""
-    X, W = np.abs(X), np.abs(W)
-    out = np.zeros((X.shape[0], W.shape[1]))
+    """7 * 2^-13 * sum over groups of 8 k of max |X[:, k] W[k, :]| (float64)."""
+    X, W = (torch.from_numpy(np.abs(v)).cuda() for v in (X, W))
+    out = torch.zeros(X.shape[0], W.shape[1], dtype=torch.float64, device="cuda")
     for k in range(0, X.shape[1], 8):
-        out += np.max(X[:, k:k + 8, None] * W[None, k:k + 8], axis=1)
-    return 7 * 2.0 ** -13 * out
+        out += (X[:, k:k + 8, None] * W[None, k:k + 8]).amax(1)
+    return 7 * 2.0 ** -13 * out.cpu().numpy()
 
 
 def expected(case, w, a8):
@@ -204,23 +204,43 @@ COUNTS = {
 }
 
 
+def few_rows(P, E, d, f):
+    """The calls that take the kernel for few rows."""
+    pieces = P / 32 + 0.5 * min(P, E)
+    steps = max(1.0, pieces * (2 * f // 64) / 512) * d + max(1.0, pieces * (d // 64) / 512) * f
+    return P <= 20 * E or steps <= 1.5 * (d + f)
+
+
+def with_many(counts, d, f):
+    """An expert more, with enough rows for the kernel for many rows."""
+    n = 65
+    while few_rows(sum(counts) + n, len(counts) + 1, d, f):
+        n += 64
+    return counts + [n]
+
+
+@pytest.mark.parametrize("many", [False, True], ids=["few", "many"])
 @pytest.mark.parametrize("a8", [False, True], ids=["a4", "a8"])
 @pytest.mark.parametrize("gather", [False, True], ids=["rows", "gather"])
 @pytest.mark.parametrize("name", COUNTS)
-def test_product(name, gather, a8):
+def test_product(name, gather, a8, many):
     counts = COUNTS[name]
-    P = sum(counts)
     d, f = {"edges64": (384, 256), "edges128": (128, 640), "hot": (640, 128), "tail": (256, 384),
             "edges256": (512, 256)}.get(name, (256, 128))
+    if many:
+        counts = with_many(counts, d, f)
+    P = sum(counts)
     case = product_case(counts, d, f, a8, 3 + P, gather)
     check(case, a8, len(counts), 1, P, f)
 
 
 @pytest.mark.parametrize("a8", [False, True], ids=["a4", "a8"])
 @pytest.mark.parametrize("d,f", [(128, 128), (128, 1152), (1152, 128), (896, 384)])
-def test_product_widths(d, f, a8):
-    case = product_case([40, 0, 1, 90], d, f, a8, d + f, True)
-    check(case, a8, 4, 1, 131, f)
+@pytest.mark.parametrize("many", [False, True], ids=["few", "many"])
+def test_product_widths(d, f, a8, many):
+    counts = with_many([40, 0, 1, 90], d, f) if many else [40, 0, 1, 90]
+    case = product_case(counts, d, f, a8, d + f, True)
+    check(case, a8, len(counts), 1, sum(counts), f)
 
 
 @pytest.mark.parametrize("a8", [False, True], ids=["a4", "a8"])
@@ -228,6 +248,9 @@ def test_rows_past_the_last_expert_stay(a8):
     """offsets[E] below P (assignments that the map skipped)."""
     case = product_case([20, 0, 300], 256, 256, a8, 9, True, T=400)
     check(case, a8, 3, 1, 400, 256)
+    counts = with_many([20, 0], 256, 256)
+    case = product_case(counts, 256, 256, a8, 9, True, T=sum(counts) + 90)
+    check(case, a8, 3, 1, sum(counts) + 90, 256)
     empty = product_case([0, 0], 256, 256, a8, 9, False, T=4)
     case = (torch.ones(8, 256).bfloat16(), None) + empty[2:]
     check(case, a8, 2, 2, 4, 256)
@@ -264,7 +287,7 @@ def test_repeated_calls_give_the_same_bits(a8, per_expert):
             assert torch.equal(o, first[i & 1]), f"call {i}"
 
 
-@pytest.mark.parametrize("rows", [21, 300])
+@pytest.mark.parametrize("rows", [21, 300, 3700])
 @pytest.mark.parametrize("a8", [False, True], ids=["a4", "a8"])
 def test_a_token_that_there_is_not_reads_zeros(a8, rows):
     """Entries of token_of outside [0, T): rows of zeros, their neighbours untouched."""
@@ -282,7 +305,7 @@ def test_a_token_that_there_is_not_reads_zeros(a8, rows):
     assert np.array_equal(got, want)
 
 
-@pytest.mark.parametrize("rows", [5, 300])
+@pytest.mark.parametrize("rows", [5, 300, 4200])
 @pytest.mark.parametrize("a8", [False, True], ids=["a4", "a8"])
 def test_a_nan_stays_in_its_row(a8, rows):
     """A NaN in x (4-bit rows), or one that arises in h (a scale of 255 in a
@@ -320,7 +343,7 @@ def layer(wl, a8, inp, **kw):
 
 
 @pytest.mark.parametrize("a8", [False, True], ids=["a4", "a8"])
-@pytest.mark.parametrize("T,E,k", [(1, 8, 2), (3, 16, 4), (257, 8, 2), (301, 64, 8)])
+@pytest.mark.parametrize("T,E,k", [(1, 8, 2), (3, 16, 4), (257, 8, 2), (301, 64, 8), (2300, 8, 2)])
 def test_layer_forward(T, E, k, a8):
     """Route, map, quantise, experts, combine: the parts' own results put
     together in fp64 give y within bf16's rounding of o and of y."""
@@ -348,7 +371,7 @@ def test_layer_forward(T, E, k, a8):
 
 
 @pytest.mark.parametrize("a8", [False, True], ids=["a4", "a8"])
-@pytest.mark.parametrize("T", [2, 400])
+@pytest.mark.parametrize("T", [2, 400, 2500])
 def test_layer_graph_replays_on_new_inputs(T, a8):
     """One captured graph, replayed on changed inputs with eager work between the
     replays, against eager calls; a second graph shares the workspace."""

@@ -584,7 +584,23 @@ int launch_tiles(const Mx4Args& a, hipStream_t s) {
 // kernel took 232 and 241 us (128 experts, d 4096, f 1536), and 126 and 137 us
 // against 168 and 178 us (8 experts, f 14336); at 24 and 32 rows the tile kernel
 // wins (242 and 254 against 251 and 280 us; 172 and 177 against 198 and 232 us).
-bool few_rows(const Mx4Args& a) { return (int64_t)a.P <= 16 * (int64_t)a.E; }
+// It also wins while the latency of a block's K steps counts, of which it has a
+// quarter: while its blocks (pieces of 32 rows, an expert's last one half full on
+// average, times groups of 64 columns), in rounds of two to a compute unit, each
+// weighted with K, come to 1.5 rounds.  4 experts, d 384, f 2560: 97 rows an
+// expert (1.16 rounds) 18.6 and 21.0 against 27.6 and 33.3 us, 300 rows (1.67)
+// 26.6 and 35.7 against 25.1 and 31.7 us; 8 experts, d = f = 1024: 64 rows (1.12)
+// 18.3 and 20.3 against 21.9 and 25.6 us, 256 rows (3.19) 30.8 and 43.1 against
+// 22.8 and 29.8 us.
+bool few_rows(const Mx4Args& a) {
+  if ((int64_t)a.P <= 20 * (int64_t)a.E) return true;
+  const double pieces = a.P / 32.0 + 0.5 * (a.P < a.E ? a.P : a.E);
+  auto steps = [&](int64_t n, int64_t k) {
+    const double rounds = pieces * (double)(n / 64) / 512.0;
+    return (rounds > 1.0 ? rounds : 1.0) * (double)k;
+  };
+  return steps(2 * (int64_t)a.f, a.d) + steps(a.d, a.f) <= 1.5 * ((double)a.d + (double)a.f);
+}
 
 }  // namespace
 
