@@ -26,6 +26,8 @@ COUNTS = {
     # few rows an expert, more than one tile of 64; many rows (256 x 256 tiles)
     "few": ([63, 64, 65, 0, 128, 1, 2, 3] + [0] * 40, 384, 640),
     "many": ([300, 0, 24700], 128, 640),
+    # one expert has most of the rows: another order of the weight gradients' tiles
+    "uneven": ([9] * 11 + [400, 0] + [9] * 11, 768, 768),
 }
 
 
