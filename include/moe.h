@@ -619,7 +619,8 @@ int moe_grouped_gemm_bwd_ckpt8(const moe_shape* sh, const int32_t* offsets,
  * byte s + 127, with s the smallest integer such that max|v| <= 448 * 2^s
  * (the scale rounded up, so nothing saturates; s clamped to [-127, 127]; an
  * all-zero block has s = 0 and +0 codes); codes are E4M3FN(v * 2^-s), round
- * to nearest even.  This scale rule departs from the OCP MX v1.0 reference
+ * to nearest even.  A block that holds a NaN or an infinity has scale byte 255,
+ * E8M0's NaN: every product it enters is NaN.  This scale rule departs from the OCP MX v1.0 reference
  * conversion (s = floor(log2 max|v|) - 8 with elements above 448 clamped),
  * which can clip a block's largest element by up to 12.5 %.  gfx950's v_mfma_scale_f32_16x16x128_f8f6f4 takes one E8M0
  * scale per lane, which is one 32-value block of one row, so the scales go

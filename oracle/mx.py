@@ -13,7 +13,8 @@ of fp32 values:
 
 * amax = max |v|; s is the smallest integer with amax <= 448 * 2^s (the
   scale rounded up to a power of two, so no element saturates), clamped to
-  [-127, 127]; an all-zero block has s = 0 and every code +0.  This departs
+  [-127, 127]; an all-zero block has s = 0 and every code +0; a block with a
+  NaN or an infinity has the scale byte 255 and reads back as NaN.  This departs
   from the OCP MX v1.0 reference conversion, which takes s = floor(log2 amax)
   - 8 and clamps elements above 448: with that rule a block whose largest
   magnitude lies in (448, 512) * 2^s loses up to 12.5 % on it, where the
@@ -68,16 +69,19 @@ def _mx_groups(V):
     """Quantise every vector along the last axis of V (length 32) as one
     block: codes uint8 (shape of V), E8M0 scale bytes (V.shape[:-1])."""
     V = np.asarray(V, dtype=np.float32)
+    bad = ~np.isfinite(V).all(axis=-1)
+    V = np.where(bad[..., None], np.float32(0), V)   # (the codes of such a block carry no meaning)
     amax = np.max(np.abs(V), axis=-1)
     s = mx_scale_exp(amax)
     scaled = (V.astype(np.float64) * np.ldexp(1.0, -s)[..., None]).astype(np.float32)
     codes = e4m3_encode(scaled)
     codes[amax == 0] = 0
-    return codes, (s + 127).astype(np.uint8)
+    return codes, np.where(bad, 255, s + 127).astype(np.uint8)
 
 
 def _scale_values(sbytes):
-    return np.ldexp(1.0, np.asarray(sbytes, np.int64) - 127)
+    sb = np.asarray(sbytes, np.int64)
+    return np.where(sb == 255, np.nan, np.ldexp(1.0, sb - 127))
 
 
 def quant_mx_rows(A):

@@ -19,6 +19,7 @@ import numpy as np
 
 from .e4m3 import e4m3_decode, e4m3_encode
 from .moe import combine, permute_map, route, silu
+from .mx import dequant_mx_rows, quant_mx_rows
 
 __all__ = ["E2M1", "mx4_decode", "mx4_encode", "mx_scale_byte", "quant_mx4_rows", "dequant_mx4_rows",
            "quant_mx8_rows", "dequant_mx8_rows", "quant_mx4_weights", "dequant_mx4_weights",
@@ -162,7 +163,7 @@ def layer_fwd_mx4(logits, x, W1, W3, W2, k, a8):
     """Route, quantise x rows, experts with 4-bit weights, combine."""
     idx, p = route(logits, k)
     counts, offsets, row_of, token_of = permute_map(idx, W1.shape[0])
-    xd = dequant_mx8_rows(*quant_mx8_rows(x)) if a8 else dequant_mx4_rows(*quant_mx4_rows(x))
+    xd = dequant_mx_rows(*quant_mx_rows(x)) if a8 else dequant_mx4_rows(*quant_mx4_rows(x))
     W13d = dequant_mx4_weights(*quant_mx4_weights(W1, W3))
     W2d = dequant_mx4_weights(*quant_mx4_weights(W2))
     a, b, h, o = experts_mx4(xd[token_of], offsets, W13d, W2d, a8)

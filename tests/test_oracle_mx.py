@@ -250,3 +250,15 @@ def test_layer_forward_uses_column_blocked_weights():
     for e in range(E):
         R = slice(int(st["offsets"][e]), int(st["offsets"][e + 1]))
         assert np.array_equal(st["a"][R], xp[R] @ W[e])
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+def test_a_block_that_is_not_finite_reads_back_as_nan(bad):
+    X = np.ones((2, 96), np.float32)
+    X[0, 40] = bad
+    X[1, 64:] = bad
+    codes, sb = oracle.quant_mx_rows(X)
+    assert sb.tolist() == [[119, 255, 119], [119, 119, 255]]     # 1 <= 448 * 2^-8
+    back = oracle.dequant_mx_rows(codes, sb)
+    assert np.isnan(back[0, 32:64]).all() and np.isnan(back[1, 64:]).all()
+    assert np.isnan(back).sum() == 64 and (back[~np.isnan(back)] == 1).all()

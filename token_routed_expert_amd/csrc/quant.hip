@@ -314,7 +314,7 @@ __device__ __forceinline__ void tokblk_load(const bf16_t* __restrict__ src,
     }
   }
   // |max| on the bit patterns: for bf16 values other than NaN, the magnitude
-  // order is the integer order of the bits without the sign
+  // order is the integer order of the bits without the sign (NaNs come out largest)
   uint32_t mb[8];
 #pragma unroll
   for (int q = 0; q < 8; ++q) mb[q] = 0u;
@@ -450,18 +450,26 @@ __global__ __launch_bounds__(256) void quant_tokblk_kernel(
 // integer with amax <= 448 * 2^s (clamped to [-127, 127]; 0 for an all-zero
 // block), so the block maximum maps into (224, 448] and nothing saturates.
 // Codes are E4M3(v * 2^-s) (exact scaling), all-zero blocks give +0 codes.
+// A block that holds a NaN or an infinity gets byte 255, E8M0's NaN, whatever
+// its codes say: the products it enters are NaN.
 
-// amax = f * 2^E, f in [1, 2): s = E - 8 if f <= 1.75 (448 = 1.75 * 2^8), else E - 7.
-__device__ __forceinline__ int mx_exp(float amax) {
-  const uint32_t u = __float_as_uint(amax);
+// Magnitude bits of v: ordered like |v| for numbers, infinity above them and
+// NaNs above infinity, so one integer maximum finds amax and non-finite values
+// (a floating-point maximum drops NaNs).
+__device__ __forceinline__ uint32_t mx_mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// From the largest magnitude bits u of a block, amax = f * 2^E, f in [1, 2):
+// s = E - 8 if f <= 1.75 (448 = 1.75 * 2^8), else E - 7; 128 where amax is not finite.
+__device__ __forceinline__ int mx_exp(uint32_t u) {
   if (u == 0) return 0;
+  if (u >= 0x7f800000u) return 128;
   const int ef = (int)(u >> 23);
   if (ef == 0) return -127;  // subnormal amax: below any reachable scale
   const int s = ef - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
   return s < -127 ? -127 : s;
 }
-// 2^-s as an fp32 (s in [-127, 120])
-__device__ __forceinline__ float mx_inv(int s) { return __uint_as_float((uint32_t)(127 - s) << 23); }
+// 2^-s as an fp32 (s in [-127, 120]; 0 for 128)
+__device__ __forceinline__ float mx_inv(int s) { return __uint_as_float((uint32_t)max(127 - s, 0) << 23); }
 __device__ __forceinline__ uint32_t mx_code(float v, float inv, bool zero_block) {
   return zero_block ? 0u : e4m3_code(v * inv);
 }
@@ -489,14 +497,14 @@ __global__ __launch_bounds__(256) void quant_rows_mx_kernel(const T* __restrict_
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int64_t g = g0 + 16 * j;
-    float m = 0.0f;
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[j][i]));
-    m = fmaxf(m, __shfl_xor(m, 1, 4));
-    m = fmaxf(m, __shfl_xor(m, 2, 4));
+    for (int i = 0; i < 8; ++i) m = max(m, mx_mag(v[j][i]));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 1, 4));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 2, 4));
     const int s = mx_exp(m);
     const float inv = mx_inv(s);
-    const bool z = m == 0.0f;
+    const bool z = m == 0;
     uint32_t lo = 0, hi = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -540,13 +548,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void q
   uint8_t* Ct = codes + mat + (size_t)rb * 128 * C + (size_t)cb * 128;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    float m = fmaxf(fmaxf(fabsf(v[i][0]), fabsf(v[i][1])), fmaxf(fabsf(v[i][2]), fabsf(v[i][3])));
-    m = fmaxf(m, __shfl_xor(m, 1, 64));
-    m = fmaxf(m, __shfl_xor(m, 2, 64));
-    m = fmaxf(m, __shfl_xor(m, 4, 64));
+    uint32_t m = max(max(mx_mag(v[i][0]), mx_mag(v[i][1])), max(mx_mag(v[i][2]), mx_mag(v[i][3])));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 1, 64));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 2, 64));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 4, 64));
     const int s = mx_exp(m);
     const float inv = mx_inv(s);
-    const bool z = m == 0.0f;
+    const bool z = m == 0;
     uint32_t w = 0;
 #pragma unroll
     for (int q = 0; q < 4; ++q) w |= mx_code(v[i][q], inv, z) << (8 * q);
@@ -563,13 +571,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void q
   uint32_t colw[4][4] = {};  // [column q][word w]: rows 16 rg + 4 w .. + 3
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    float m = 0.0f;
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(v[i][q]));
-    m = fmaxf(m, __shfl_xor(m, 32, 64));
+    for (int i = 0; i < 16; ++i) m = max(m, mx_mag(v[i][q]));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
     const int s = mx_exp(m);
     const float inv = mx_inv(s);
-    const bool z = m == 0.0f;
+    const bool z = m == 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) colw[q][i >> 2] |= mx_code(v[i][q], inv, z) << (8 * (i & 3));
     if ((rg & 1) == 0) cs[col + q][rg >> 1] = (uint8_t)(s + 127);
@@ -622,7 +630,7 @@ __global__ __launch_bounds__(256) void quant_tokblk_mx_kernel(
   bool z[8];
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
-    const int s = mx_exp(m[q]);
+    const int s = mx_exp(__float_as_uint(m[q]));
     inv[q] = mx_inv(s);
     z[q] = m[q] == 0.0f;
     if ((tid & 63) < 16) cs[8 * cg + q][g] = (uint8_t)(s + 127);
@@ -644,14 +652,14 @@ __global__ __launch_bounds__(256) void quant_tokblk_mx_kernel(
     uint8_t* const rsdst = rsb + (size_t)r0 * (C >> 5) + cb * 4 + (cg >> 2);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float mx = 0.0f;
+      uint32_t mx = 0;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) mx = fmaxf(mx, fabsf(bf16_at(raw[i], q)));
-      mx = fmaxf(mx, __shfl_xor(mx, 1, 4));
-      mx = fmaxf(mx, __shfl_xor(mx, 2, 4));
+      for (int q = 0; q < 8; ++q) mx = max(mx, mx_mag(bf16_at(raw[i], q)));
+      mx = max(mx, (uint32_t)__shfl_xor((int)mx, 1, 4));
+      mx = max(mx, (uint32_t)__shfl_xor((int)mx, 2, 4));
       const int s = mx_exp(mx);
       const float rinv = mx_inv(s);
-      const bool rz = mx == 0.0f;
+      const bool rz = mx == 0;
       uint32_t lo = 0, hi = 0;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
