@@ -213,7 +213,8 @@ int moe_grouped_gemm_bwd(const moe_shape* sh, const int32_t* offsets, const void
  * summary, section 2 C, and the hyper.ai article on Hybrid-EP): row r of the
  * permuted input is row token_of[r] of x [T][d] (token_of from moe_permute's
  * map), read by fc1 forward and by the fc1 weight gradient, so no permuted
- * copy xp is written or read.  Results equal moe_grouped_gemm_fwd / _bwd on
+ * copy xp is written or read.  An entry outside [0, T) counts as a row of
+ * zeros.  Results equal moe_grouped_gemm_fwd / _bwd on
  * xp = x[token_of] bit for bit.  bf16 and fp32; MOE_ERR_UNSUPPORTED when
  * T * d * element bytes >= 2^31 - 4096.
  */
@@ -583,8 +584,8 @@ int moe_grouped_gemm_bwd_rowscaled(const moe_shape* sh, const int32_t* offsets, 
  *
  * moe_grouped_gemm_fwd_ckpt8 -- row-scaled expert forward (probabilities before
  * W2) that writes abq uint8 [P][2f] and abs uint8 [P][2f/32] in place of ab.
- * x: row r is row token_of[r] of x [T][d], or, token_of NULL, row r of the
- * permuted x [P][d].  h [P][f] is scratch (it need not be kept).
+ * x: row r is row token_of[r] of x [T][d] (an entry outside [0, T) counts as a
+ * row of zeros), or, token_of NULL, row r of the permuted x [P][d].  h [P][f] is scratch (it need not be kept).
  */
 int moe_grouped_gemm_fwd_ckpt8(const moe_shape* sh, const int32_t* offsets,
                                const int32_t* token_of, const void* x, const void* W1,

@@ -330,12 +330,13 @@ __global__ __launch_bounds__(NW * 64, 1) void gemm_bf16_kernel(GemmArgs args, in
       const int t = wid * DMA_PER_WAVE + q;
       if constexpr (GATHER && OP == OP_FC1_FWD) {
         // row `row` of the tile is x row token_of[row0 + row]; rows past the
-        // expert's end read as zero (an offset past the buffer's range)
+        // expert's end, and tokens that there are not, read as zero: they take the
+        // row behind x's last, past the buffer's range (token * a_ld itself could
+        // wrap back into it)
         const int row = 16 * t + (lane >> 2);
         const int c = (lane & 3) ^ kc_swz(row);
-        o.a_off[q] = row < ti.rows
-                         ? (uint32_t)args.gather[ti.row0 + row] * a_ld + (uint32_t)c * 16u
-                         : kPastRange;
+        const uint32_t token = row < ti.rows ? (uint32_t)args.gather[ti.row0 + row] : ~0u;
+        o.a_off[q] = min(token, (uint32_t)args.gT) * a_ld + (uint32_t)c * 16u;
       } else if constexpr (GW) {
         // the column part only: the k-row's token comes per stage
         const int ta = a_instr(q);
@@ -388,7 +389,8 @@ __global__ __launch_bounds__(NW * 64, 1) void gemm_bf16_kernel(GemmArgs args, in
          tok_base + (uint32_t)((wid * TSLOTS + ((tphase + s) & (TSLOTS - 1))) * 256));
   };
   // A offsets of stage s from its token ids (landed for this wavefront): x row
-  // token * d for the lane's k-row, past the range for k-rows past the tile's
+  // token * d for the lane's k-row, the row behind x's last (past the range) for
+  // k-rows past the tile's and for tokens outside [0, gT)
   auto read_tok = [&](int s) __attribute__((always_inline)) -> int {
     return *(const __attribute__((address_space(3))) int*)(
         lds + NS * STAGE_BYTES + (wid * TSLOTS + ((tphase + s) & (TSLOTS - 1))) * 256 +
@@ -398,10 +400,10 @@ __global__ __launch_bounds__(NW * 64, 1) void gemm_bf16_kernel(GemmArgs args, in
     const bool in_cur = s < cur.KT;
     const int ks = (in_cur ? s : s - cur.KT) * BK + 4 * wid;
     const int lim = (in_cur ? cur.rows : nxt.rows) - ks;  // valid k-rows of the four
+    const uint32_t token = min((lane >> 4) < lim ? (uint32_t)tok : ~0u, (uint32_t)args.gT);
 #pragma unroll
     for (int q = 0; q < DMA_PER_WAVE; ++q)
-      gofs[q] = (lane >> 4) < lim ? (uint32_t)tok * a_ld + (in_cur ? cur.a_off[q] : nxt.a_off[q])
-                                  : kPastRange;
+      gofs[q] = token * a_ld + (in_cur ? cur.a_off[q] : nxt.a_off[q]);
   };
   // DMA instruction q of this wavefront (q < DMA_PER_WAVE: A operand, else B)
   // for stage s of the stream, counted from the current tile's stage 0

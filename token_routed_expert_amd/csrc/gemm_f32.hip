@@ -57,6 +57,11 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs args, int NT, in
   const float* W3 = (const float*)args.W3 + e * (size_t)d * f;
   const float* W2 = (const float*)args.W2 + e * (size_t)f * d;
 
+  // element k of x row gather[r]; 0 for a token that there is not
+  auto x_at = [&](size_t r, int k) -> float {
+    const uint32_t token = (uint32_t)args.gather[r];
+    return token < (uint32_t)args.gT ? ((const float*)args.gx)[(size_t)token * d + k] : 0.f;
+  };
   // A[m][k] of the tile (m, k local to the tile's origin; 0 outside)
   auto a_at = [&](int m, int k) -> float {
     if (k >= K) return 0.f;
@@ -64,7 +69,7 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs args, int NT, in
       if (m >= M) return 0.f;
       const size_t r = (size_t)(ti.row0 + m);
       if constexpr (OP == OP_FC1_FWD) {
-        if (args.gather) return ((const float*)args.gx)[(size_t)args.gather[r] * d + k];
+        if (args.gather) return x_at(r, k);
         return xp[r * d + k];
       }
       if constexpr (OP == OP_FC2_FWD) return h[r * f + k];
@@ -75,7 +80,7 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmArgs args, int NT, in
       if (mm >= M) return 0.f;
       const size_t r = (size_t)(ti.row0 + k);
       if constexpr (OP == OP_FC2_WGRAD) return h[r * f + mm];
-      if (args.gather) return ((const float*)args.gx)[(size_t)args.gather[r] * d + mm];
+      if (args.gather) return x_at(r, mm);
       return xp[r * d + mm];
     }
   };
