@@ -10,6 +10,7 @@ import torch
 
 from gpu_common import announce, need_gpu
 from test_gpu_ckpt8 import COUNTS, Case, backward, checkpoint, few_rows, forward
+from test_gpu_mx4 import product_case, run_product
 
 pytestmark = pytest.mark.gpu
 
@@ -51,7 +52,7 @@ def test_checkpoint_calls(name):
     assert torch.equal(dp, dq)
 
 
-@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("counts,d,f", [([40, 0, 300, 7], 256, 128), ([900], 128, 384)])
 def test_gathered_products(dtype, counts, d, f):
     import token_routed_expert_amd as tre
@@ -78,3 +79,23 @@ def test_gathered_products(dtype, counts, d, f):
         outs.append(o)
     for n in outs[0]:
         assert torch.equal(outs[0][n], outs[1][n]), n
+
+
+@pytest.mark.parametrize("rows", [5, 21, 300, 3700])     # one and two fragments of the few-row kernel, tiles
+@pytest.mark.parametrize("a8", [False, True], ids=["a4", "a8"])
+def test_mxfp4_product_on_weights_with_a_nan(a8, rows):
+    """A row of zeros is no row of zero results where a block of the weights is NaN."""
+    counts = [rows, 0, 0, 2]
+    X, tok, W1, W3, W2, off = product_case(counts, 384, 256, a8, rows, True)
+    T = sum(counts)
+    bad, zeros = unknown(tok, T, 384)
+    W1[0, 5, 40] = np.nan
+    W2[3, 7, 100] = np.inf
+    Xz = torch.cat([X, torch.zeros(1, 384, dtype=torch.bfloat16)])[torch.from_numpy(zeros).long()].contiguous()
+    X[0, 3] = float("nan")     # (the row whose place a token that there is not takes in the loads)
+    keep = torch.from_numpy(zeros != 0)
+    got, _ = run_product((X, bad, W1, W3, W2, off), a8, 4, 1, T, 256)
+    want, _ = run_product((Xz, None, W1, W3, W2, off), a8, 4, 1, T, 256)
+    got, want = got.float().cpu()[keep], want.float().cpu()[keep]
+    assert torch.isnan(got[: rows // 2]).all() and not torch.isnan(got[-1, :100]).any()
+    assert torch.equal(got.nan_to_num(nan=1e30), want.nan_to_num(nan=1e30))

@@ -169,11 +169,11 @@ __global__ __launch_bounds__(NW * 64) void gemm_mx4_rows_kernel(Mx4Args args) {
   auto run = [&](auto MTC, auto UC) __attribute__((always_inline)) {
     constexpr int MT = decltype(MTC)::value, U = decltype(UC)::value;
     const uint8_t *at[MT], *ast[MT];
-    bool known[MT];
+    bool known[MT], all_known = true;
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       // rows past the last are read as the last one and not stored; a token that
-      // there is not counts as a row of zeros
+      // there is not counts as a row of zeros (not its results: 0 times a NaN is NaN)
       const int pr = row0 + min(16 * t + r, rows - 1);
       size_t ar = (size_t)pr;
       known[t] = true;
@@ -181,10 +181,12 @@ __global__ __launch_bounds__(NW * 64) void gemm_mx4_rows_kernel(Mx4Args args) {
         const uint32_t token = (uint32_t)args.token_of[pr];
         known[t] = token < (uint32_t)args.T;
         ar = known[t] ? token : 0;
+        all_known = all_known && known[t];
       }
       at[t] = args.a + ar * a_ld + g * 16;
       ast[t] = args.as + ar * as_ld + g;
     }
+    all_known = __all(all_known);
     f32x4_t acc[MT][4];
 #pragma unroll
     for (int t = 0; t < MT; ++t)
@@ -218,6 +220,13 @@ __global__ __launch_bounds__(NW * 64) void gemm_mx4_rows_kernel(Mx4Args args) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (k0 + NW * u < KT) {
+          if (!all_known) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+              xf[u][t] = known[t] ? xf[u][t] : typename Frag<A8>::type{};
+              sx[u][t] = known[t] ? sx[u][t] : 127;
+            }
+          }
 #pragma unroll
           for (int t = 0; t < MT; ++t)
             static_for<0, 4>([&](auto J) __attribute__((always_inline)) {
@@ -229,7 +238,7 @@ __global__ __launch_bounds__(NW * 64) void gemm_mx4_rows_kernel(Mx4Args args) {
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) part[t][w][j][lane] = known[t] ? acc[t][j] : f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < 4; ++j) part[t][w][j][lane] = acc[t][j];
     __syncthreads();
     if (w >= MT) return;  // wavefront t stores rows 16 t ..
     f32x4_t sum[4];
