@@ -21,20 +21,28 @@
 // with a stride of the grid; numbers past the device-side count end it.
 // Block ids are remapped so that the blocks one XCD runs at a time (ids with
 // the same value mod 8) take consecutive tiles: they share A rows and expert
-// weights in that XCD's L2.  Either each XCD has an eighth of the tile list, or,
-// with up to 16 experts, all XCDs move through the list together, 8 (data
-// gradients) or 32 tiles each at a time: an eighth would set them on matrices
-// whole experts apart.  8 experts, d 4096, f 14336, 8192 rows, an eighth against
-// together, us: forward 1950 and 1027 against 1712 and 1006, fc2 and fc1 data
-// gradients 1086 and 2154 against 1041 and 2015, weight gradients 917 and 2042
-// against 940 and 1735; 256 experts, d 7168, f 2048, 131072 rows: fc1 forward 7712
-// against 8260, its data gradient 7995 against 8425; one expert, 16384 rows: fc1
-// forward 828 against 890, its data gradient 817 against 715.  The weight
-// gradients, whose tiles take as long as their expert has rows, also go together
-// when an eighth of the experts has 5/4 of an eighth of the rows: 64 experts, d
-// 2048, f 1408, 12306 rows of which one expert has 1912: 210 and 391 against 190
-// and 322; 128 even experts, d 4096, f 1536, 65536 rows: 977 and 1885 against 1000
-// and 1925.
+// weights in that XCD's L2.  Either each XCD has an eighth of the tile list, or
+// all XCDs move through the list together, 8 (data gradients) or 32 tiles each at
+// a time.  Together with few experts, where an eighth sets the XCDs on matrices
+// whole experts apart: the ragged-M products with up to 16 experts (the forward
+// ones not with a single one), fc1's weight gradient with 2 to 15.  d 4096, 8192
+// rows, an eighth against together, us:
+//   experts, f   fc1, fc2 forward         fc2, fc1 data gradient   fc2, fc1 weight gradient
+//   1   14336    1815 836 / 1931 850      1050 1810 / 930 1556     785 1408 / 779 1417
+//   4   14336    1917 1082 / 1686 983     1014 2184 / 997 1942     798 1573 / 810 1545
+//   8   14336    1935 1038 / 1785 1018    1066 2141 / 1017 2064    918 2039 / 936 1719
+//   12  9600     1164 673 / 1142 655      745 1426 / 747 1397      691 1432 / 678 1333
+//   16  7168     1014 527 / 971 497       603 1092 / 617 1064      573 1077 / 571 1111
+//   24  4736     753 351 / 696 341        489 712 / 485 707        443 859 / 440 895
+//   48  2432     482 205 / 486 207        262 448 / 287 450        334 700 / 324 694
+// and 256 experts, d 7168, f 2048, 131072 rows: fc1 forward 7712 / 8260, its data
+// gradient 7995 / 8425.  (fc1's data gradient reads more together, 7.5 GB against
+// 3.4 with 8 experts: its operands come through all eight L2s.  It is not bound by
+// memory and no slower for it.)  The weight gradients, whose tiles take as long as
+// their expert has rows, also go together when some eighth of their list has more
+// than 5/4 of an eighth of the rows: 64 experts, d 2048, f 1408, 12306 rows of
+// which one expert has 1912: 210 and 391 / 190 and 322; 128 even experts, d 4096,
+// f 1536, 65536 rows: 977 and 1885 / 1000 and 1925.
 // Weight-gradient products have a fixed grid of E x (M/BM) x (N/BN) tiles; K is
 // the expert's row count, 0 for an empty expert, which then writes zeros.
 //
@@ -208,13 +216,9 @@ __global__ __launch_bounds__(NW * 64, 1) void gemm_bf16_kernel(GemmArgs args, in
   else total = args.E * MT * NT;
   total = uniform(total);
   // An eighth of the tile list for each XCD, or all XCDs together (see above)
-  bool rounds = args.E <= 16 && (TR::b_kcontig || args.E > 1);
-  if constexpr (!TR::ragged_m) {
-    int most = 0;  // rows of the XCD with the most, an eighth of the experts each
-    for (int x = 0; x < 8; ++x)
-      most = max(most, offs[(x + 1) * args.E / 8] - offs[x * args.E / 8]);
-    rounds = rounds || (int64_t)most * 32 > (int64_t)offs[args.E] * 5;
-  }
+  bool rounds;
+  if constexpr (TR::ragged_m) rounds = args.E <= 16 && (TR::b_kcontig || args.E > 1);
+  else rounds = (OP == OP_FC1_WGRAD && args.E > 1 && args.E < 16) || uneven_eighths(offs, args.E);
   rounds = uniform(rounds);
   auto decode = [&](int slot, TileInfo& ti) __attribute__((always_inline)) {
     const int logical = rounds ? xcd_remap_rounds<TR::b_kcontig ? 8 : 32>(slot, total) : xcd_remap(slot, total);

@@ -10,25 +10,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "tile_order.h"
+
 namespace tre {
-
-// Bijection on [0, n): block ids with the same value mod 8 (dispatched to the
-// same XCD, each XCD with its own L2) get consecutive logical tile ids.
-__device__ __forceinline__ int xcd_remap(int i, int n) {
-  const int x = i & 7, j = i >> 3;
-  const int q = n >> 3, r = n & 7;
-  return x * q + min(x, r) + j;
-}
-
-// The same in rounds of 8 C tiles: an XCD takes C consecutive ones of each
-// round, so that tiles of unequal work spread over the XCDs; what is left after
-// the last whole round is divided as above.
-template <int C>
-__device__ __forceinline__ int xcd_remap_rounds(int i, int n) {
-  const int whole = n / (8 * C) * (8 * C);
-  if (i >= whole) return whole + xcd_remap(i - whole, n - whole);
-  return i / (8 * C) * (8 * C) + (i & 7) * C + (i >> 3) % C;
-}
 
 struct TileInfo {
   int e;     // expert
