@@ -54,6 +54,11 @@ __device__ __forceinline__ float sigmoid_f32(float z) {
 }
 __device__ __forceinline__ float silu_f32(float z) { return z * sigmoid_f32(z); }
 
+// Whether a launch keeps all its threads: an x dimension of 2^32 threads or more
+// is not refused by the runtime but cut to the low 32 bits (2^24 + 1 blocks of 256
+// run as one), so every launch whose grid grows with the call is checked.
+inline bool launch_fits(int64_t blocks, int threads) { return blocks * threads < (int64_t)1 << 32; }
+
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 }  // namespace tre

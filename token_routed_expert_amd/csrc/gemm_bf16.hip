@@ -732,6 +732,7 @@ int launch(const GemmArgs& a, hipStream_t s) {
     if (ncu <= 0) return MOE_ERR_HIP;
     if (grid > ncu) grid = ncu;
   }
+  if (!launch_fits(grid, NW * 64)) return MOE_ERR_UNSUPPORTED;
   // row-scaled variants (only fc1 forward and fc2 dgrad change) and the
   // gathered fc1 operand (fc1 forward and fc1 weight gradient)
   const unsigned g = (unsigned)grid;

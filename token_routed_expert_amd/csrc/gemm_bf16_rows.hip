@@ -201,7 +201,7 @@ int launch(const GemmArgs& a, hipStream_t s) {
   const int N = OP == OP_FC1_FWD ? 2 * a.f : (OP == OP_FC2_DGRAD ? a.f : a.d);
   const int64_t NT = (N + BN - 1) / BN;
   const int64_t grid = ((int64_t)a.P / BM + a.E) * NT;
-  if (grid > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  if (!launch_fits(grid, 512)) return MOE_ERR_UNSUPPORTED;
   gemm_bf16_rows_kernel<OP, RS, CK><<<(unsigned)grid, 512, 0, s>>>(a, (int)NT);
   TRE_LAUNCH_CHECK();
   return MOE_OK;

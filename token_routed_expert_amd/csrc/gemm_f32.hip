@@ -180,7 +180,7 @@ int launch(const GemmArgs& a, hipStream_t s) {
     grid = (int64_t)a.E * MT * NT;
   }
   if (grid <= 0) return MOE_OK;
-  if (grid > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  if (!launch_fits(grid, 256)) return MOE_ERR_UNSUPPORTED;
   gemm_f32_kernel<OP><<<(unsigned)grid, 256, 0, s>>>(a, NT, MT);
   TRE_LAUNCH_CHECK();
   if (OP == OP_FC1_FWD) {

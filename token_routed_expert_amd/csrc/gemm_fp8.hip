@@ -831,6 +831,7 @@ int launch(const GemmArgs& a, hipStream_t s) {
     if (ncu <= 0) return MOE_ERR_HIP;
     if (grid > ncu) grid = ncu;
   }
+  if (!launch_fits(grid, NW * 64)) return MOE_ERR_UNSUPPORTED;
   const unsigned g = (unsigned)grid;
   bool scaled = false;  // row-scaled variant: only fc1 forward and fc2 dgrad change
   if constexpr (OP == OP_FC1_FWD || OP == OP_FC2_DGRAD) {

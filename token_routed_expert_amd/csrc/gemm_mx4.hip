@@ -267,7 +267,7 @@ int launch_rows(const Mx4Args& a, hipStream_t s) {
   const int64_t NB = (FC == 1 ? 2 * (int64_t)a.f : (int64_t)a.d) / 64;
   // at most sum_e ceil(m_e / 32) pieces, P with fewer rows than experts
   const int64_t grid = NB * (a.P / 32 + (a.P < a.E ? a.P : a.E));
-  if (grid > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  if (!launch_fits(grid, NW * 64)) return MOE_ERR_UNSUPPORTED;
   gemm_mx4_rows_kernel<FC, A8><<<(unsigned)grid, NW * 64, 0, s>>>(a);
   TRE_LAUNCH_CHECK();
   return MOE_OK;
@@ -581,7 +581,7 @@ int launch_tiles(const Mx4Args& a, hipStream_t s) {
   const int64_t NT = ((FC == 1 ? 2 * (int64_t)a.f : (int64_t)a.d) + 255) / 256;
   // at most sum_e ceil(m_e / 128) row tiles; a block past the device-side count ends at once
   const int64_t grid = ((int64_t)a.P / 128 + a.E) * NT;
-  if (grid > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  if (!launch_fits(grid, 256)) return MOE_ERR_UNSUPPORTED;
   gemm_mx4_tile_kernel<FC, A8><<<(unsigned)grid, 256, 0, s>>>(a, (int)NT);
   TRE_LAUNCH_CHECK();
   return MOE_OK;

@@ -1008,7 +1008,6 @@ int moe_quantize_rows_mx4(const void* src, int32_t src_dtype, int64_t rows, int6
                           uint8_t* codes, uint8_t* scales, void* stream) {
   if (!src || !codes || !scales || rows < 0 || cols < 0) return MOE_ERR_INVALID;
   if (src_dtype != MOE_BF16 && src_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
-  // (a block of threads takes 64 scale blocks; the grid stays below 2^31)
   if (cols % 32 != 0 || rows >= ((int64_t)1 << 40) || cols >= (1 << 30) ||
       (cols > 0 && rows > ((int64_t)1 << 36) / (cols / 32)))
     return MOE_ERR_UNSUPPORTED;

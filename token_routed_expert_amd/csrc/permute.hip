@@ -266,6 +266,7 @@ int scatter_typed(const void* src, const int32_t* row_of, const float* scale, in
                   void* dst, hipStream_t s) {
   const int C = d * (int)sizeof(T) / 16;
   const int bs = block_for_chunks(C, 256);
+  if (!launch_fits(T_, bs)) return MOE_ERR_UNSUPPORTED;
   if (scale)
     scatter_rows_kernel<T, true><<<T_, bs, 0, s>>>((const u32x4_t*)src, row_of, scale, k, C,
                                                    (u32x4_t*)dst);
@@ -281,6 +282,7 @@ int gather_typed(const void* src, const int32_t* row_of, const float* prob, cons
                  int T_, int k, int d, void* dst, hipStream_t s) {
   const int C = d * (int)sizeof(T) / 16;
   const int bs = block_for_chunks(C, 512);
+  if (!launch_fits(T_, bs)) return MOE_ERR_UNSUPPORTED;
   const u32x4_t* S = (const u32x4_t*)src;
   const u32x4_t* A = (const u32x4_t*)add;
   u32x4_t* D = (u32x4_t*)dst;
@@ -350,6 +352,7 @@ int unpermute_launch(const void* src, const int32_t* row_of, const float* prob, 
 int permute_e4m3_launch(const uint8_t* codes, const float* scales, const int32_t* row_of, int T,
                         int k, int d, uint8_t* dst_codes, float* dst_scales, hipStream_t s) {
   const int C = d / 16, KB = d / 128;
+  if (!launch_fits(T, block_for_chunks(C, 256))) return MOE_ERR_UNSUPPORTED;
   scatter_e4m3_kernel<<<T, block_for_chunks(C, 256), 0, s>>>((const u32x4_t*)codes, scales, row_of, k,
                                                          C, KB, (u32x4_t*)dst_codes, dst_scales);
   TRE_LAUNCH_CHECK();

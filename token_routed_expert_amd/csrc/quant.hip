@@ -685,6 +685,7 @@ int quant_rows_mx_launch(const void* src, bool src_f32, int64_t rows, int64_t co
   const int64_t nblk = rows * (cols / 32);
   if (nblk == 0) return MOE_OK;
   const int64_t grid = (nblk + 255) / 256;
+  if (!launch_fits(grid, 256)) return MOE_ERR_UNSUPPORTED;
   if (src_f32)
     quant_rows_mx_kernel<float><<<dim3((unsigned)grid), 256, 0, s>>>((const float*)src, nblk,
                                                                       codes, sb);
@@ -709,7 +710,7 @@ int quant_tokblk_mx_launch(const void* src, const int32_t* src_row, const int32_
                            uint8_t* sbt, hipStream_t s, uint8_t* rcodes, uint8_t* rsb) {
   const int64_t nb = tokblk_max_blocks(P, E);
   if (nb == 0) return MOE_OK;
-  if (nb * (C / 128) > INT32_MAX) return MOE_ERR_UNSUPPORTED;  // one block per (b, cb)
+  if (!launch_fits(nb * (C / 128), 256)) return MOE_ERR_UNSUPPORTED;  // one block per (b, cb)
   const dim3 grid((unsigned)(nb * (C / 128)));
   if (rcodes)
     quant_tokblk_mx_kernel<true><<<grid, 256, 0, s>>>((const bf16_t*)src, src_row, offsets, blk, E,
@@ -726,6 +727,7 @@ int quant_rows_launch(const void* src, bool src_f32, int64_t rows, int64_t cols,
   const int64_t nblk = rows * (cols / 128);
   if (nblk == 0) return MOE_OK;
   const int64_t grid = (nblk + 63) / 64;
+  if (!launch_fits(grid, 256)) return MOE_ERR_UNSUPPORTED;
   if (src_f32)
     quant_rows_kernel<float><<<dim3((unsigned)grid), 256, 0, s>>>((const float*)src, nblk, codes,
                                                                    scales);
@@ -758,7 +760,7 @@ int quant_tokblk_launch(const void* src, const int32_t* src_row, const int32_t* 
                         float* scales, hipStream_t s, uint8_t* rcodes, float* rscales) {
   const int64_t nb = tokblk_max_blocks(P, E);
   if (nb == 0) return MOE_OK;
-  if (nb * (C / 128) > INT32_MAX) return MOE_ERR_UNSUPPORTED;  // one block per (b, cb)
+  if (!launch_fits(nb * (C / 128), 256)) return MOE_ERR_UNSUPPORTED;  // one block per (b, cb)
   const dim3 grid((unsigned)(nb * (C / 128)));
   if (rcodes)
     quant_tokblk_kernel<true><<<grid, 256, 0, s>>>((const bf16_t*)src, src_row, offsets, blk, E,

@@ -167,13 +167,16 @@ __global__ __launch_bounds__(256) void dequant_weights_mx4_kernel(const uint8_t*
 int quant_rows_mx4_launch(const void* src, bool src_f32, int64_t rows, int64_t cols,
                           uint8_t* codes, uint8_t* sb, hipStream_t s) {
   const int64_t nblk = rows * (cols / 32);
-  if (nblk == 0) return MOE_OK;
-  const unsigned grid = (unsigned)((nblk * 4 + 255) / 256);
-  if (src_f32)
-    quant_rows_mx4_kernel<float><<<grid, 256, 0, s>>>((const float*)src, nblk, codes, sb);
-  else
-    quant_rows_mx4_kernel<bf16_t><<<grid, 256, 0, s>>>((const bf16_t*)src, nblk, codes, sb);
-  TRE_LAUNCH_CHECK();
+  constexpr int64_t kPart = (int64_t)1 << 29;  // blocks a launch: 2^31 threads
+  for (int64_t at = 0; at < nblk; at += kPart) {
+    const int64_t n = nblk - at < kPart ? nblk - at : kPart;
+    const unsigned grid = (unsigned)((n * 4 + 255) / 256);
+    if (src_f32)
+      quant_rows_mx4_kernel<float><<<grid, 256, 0, s>>>((const float*)src + at * 32, n, codes + at * 16, sb + at);
+    else
+      quant_rows_mx4_kernel<bf16_t><<<grid, 256, 0, s>>>((const bf16_t*)src + at * 32, n, codes + at * 16, sb + at);
+    TRE_LAUNCH_CHECK();
+  }
   return MOE_OK;
 }
 

@@ -217,6 +217,7 @@ int launch_route(const float* logits, int T, int E, int k, int32_t* idx, float* 
                  hipStream_t s) {
   constexpr int tokens_per_block = 256 / L;
   const int blocks = (T + tokens_per_block - 1) / tokens_per_block;
+  if (!launch_fits(blocks, 256)) return MOE_ERR_UNSUPPORTED;
   route_kernel<L, V><<<blocks, 256, 0, s>>>(logits, T, E, k, idx, prob);
   TRE_LAUNCH_CHECK();
   return MOE_OK;
@@ -240,6 +241,7 @@ int route_launch(const float* logits, int T, int E, int k, int32_t* idx, float* 
 int route_aux_launch(const float* logits, int T, int E, int k, int32_t* idx, float* prob,
                      float* partial, hipStream_t s) {
   const int blocks = (T + RA_TOK - 1) / RA_TOK;
+  if (!launch_fits(blocks, 1024)) return MOE_ERR_UNSUPPORTED;
   if (E <= 64) route_aux_kernel<1><<<blocks, 1024, 0, s>>>(logits, T, E, k, idx, prob, partial);
   else if (E <= 128) route_aux_kernel<2><<<blocks, 1024, 0, s>>>(logits, T, E, k, idx, prob, partial);
   else route_aux_kernel<4><<<blocks, 1024, 0, s>>>(logits, T, E, k, idx, prob, partial);

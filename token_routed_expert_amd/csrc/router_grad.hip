@@ -325,7 +325,7 @@ int combine_bwd_launch(const void* dY, const void* o, const int32_t* row_of, con
                        hipStream_t s) {
   const int C = d * elem_bytes / 16;
   const int cpt = (C + 255) / 256;
-  if (cpt > 8) return MOE_ERR_UNSUPPORTED;
+  if (cpt > 8 || !launch_fits(T, 256)) return MOE_ERR_UNSUPPORTED;
   if (elem_bytes == 4) {
     if (cpt <= 2) combine_bwd_typed<float, 2>(dY, o, row_of, prob, T, k, C, dO, dprob, s);
     else if (cpt <= 4) combine_bwd_typed<float, 4>(dY, o, row_of, prob, T, k, C, dO, dprob, s);
@@ -346,6 +346,7 @@ int route_bwd_launch(const float* logits, int T, int E, int k, const int32_t* id
       (counts && alpha != 0.0f && aux_scale != 0.0f)
           ? (float)((double)aux_scale * alpha * E / ((double)T * T * k))
           : 0.0f;
+  if (!launch_fits((T + 3) / 4, 256)) return MOE_ERR_UNSUPPORTED;
   route_bwd_kernel<<<(T + 3) / 4, 256, 0, s>>>(logits, T, E, k, idx, prob, dprob, counts, gscale,
                                               dlogits);
   TRE_LAUNCH_CHECK();
