@@ -74,7 +74,7 @@ def layer_buffers(T, d, E, k, f, f_shared=0, dtype="bf16", device="cuda", inputs
         b.update(row_prob=z(P, dtype=torch.float32), memory_efficient=int(memory_efficient))
         bwd_kind = N.MOE_WS_LAYER_BWD_ROWSCALED
         if memory_efficient == 3:
-            b.pop("ab")
+            b.pop("ab", None)  # (MXFP4 layers have none, and refuse every mode)
             b.update(ab_q=z(P, 2 * f, dtype=torch.uint8), ab_s=z(P, 2 * f // 32, dtype=torch.uint8))
     ws_b = torch.empty(max(256, moe_workspace_bytes(sh, bwd_kind)), dtype=torch.uint8,
                        device=device)
