@@ -20,7 +20,7 @@ from .ops import (E4M3Weights, MX4Weights, MXWeights, MoeError, make_shape, moe_
                   moe_probe_mfma, moe_quantize_token_blocks_with_rows,
                   moe_quantize_token_blocks_with_rows_mx, moe_quantize_rows_mx4,
                   moe_quantize_weights_mx4, moe_dequantize_weights_mx4, moe_grouped_gemm_fwd_mx4,
-                  moe_grouped_gemm_fwd_ckpt8, moe_grouped_gemm_bwd_ckpt8)
+                  moe_grouped_gemm_fwd_ckpt8, moe_grouped_gemm_bwd_ckpt8, moe_few_rows)
 
 __all__ = ["MoeError", "make_shape", "moe_route", "moe_permute", "moe_unpermute",
            "moe_grouped_gemm_fwd", "moe_grouped_gemm_bwd", "moe_layer_fwd", "moe_layer_bwd",
@@ -36,7 +36,7 @@ __all__ = ["MoeError", "make_shape", "moe_route", "moe_permute", "moe_unpermute"
            "moe_aux_loss_final", "moe_quantize_token_blocks_with_rows",
            "moe_quantize_token_blocks_with_rows_mx", "MX4Weights", "moe_quantize_rows_mx4",
            "moe_quantize_weights_mx4", "moe_dequantize_weights_mx4", "moe_grouped_gemm_fwd_mx4",
-           "moe_grouped_gemm_fwd_ckpt8", "moe_grouped_gemm_bwd_ckpt8",
+           "moe_grouped_gemm_fwd_ckpt8", "moe_grouped_gemm_bwd_ckpt8", "moe_few_rows",
            "MOE_WS_PERMUTE", "MOE_WS_GEMM_FWD", "MOE_WS_GEMM_BWD", "MOE_WS_LAYER_FWD",
            "MOE_WS_LAYER_BWD", "MOE_WS_AUX_LOSS", "MOE_WS_GEMM_BWD_ROWSCALED",
            "MOE_WS_LAYER_BWD_ROWSCALED", "_native"]

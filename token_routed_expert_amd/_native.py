@@ -121,6 +121,7 @@ _PROTOS = {
     "moe_grouped_gemm_bwd_rowscaled": (C.c_int, [_SH] + [_P] * 4 + [C.c_int32] + [_P] * 13
                                        + [C.c_size_t, _P]),
     "moe_workspace_bytes": (C.c_size_t, [_SH, C.c_int]),
+    "moe_few_rows": (C.c_int, [_SH]),
     "moe_status_str": (C.c_char_p, [C.c_int]),
     "moe_probe_mfma": (C.c_int, [C.c_int, _I64, _P, _P, C.POINTER(C.c_int64), C.POINTER(C.c_int64),
                                  _P]),

@@ -587,6 +587,8 @@ int launch_tiles(const Mx4Args& a, hipStream_t s) {
   return MOE_OK;
 }
 
+}  // namespace
+
 // Which kernel: the rows kernel reads a column group's weights once per 32 rows of
 // an expert and wins while they are read once or hardly more: at 16 rows an
 // expert on average it took 222 us (E2M1 rows) and 239 us (E4M3) where the tile
@@ -601,7 +603,7 @@ int launch_tiles(const Mx4Args& a, hipStream_t s) {
 // 26.6 and 35.7 against 25.1 and 31.7 us; 8 experts, d = f = 1024: 64 rows (1.12)
 // 18.3 and 20.3 against 21.9 and 25.6 us, 256 rows (3.19) 30.8 and 43.1 against
 // 22.8 and 29.8 us.
-bool few_rows(const Mx4Args& a) {
+bool gemm_mx4_few_rows(const Mx4Args& a) {
   if ((int64_t)a.P <= 20 * (int64_t)a.E) return true;
   const double pieces = a.P / 32.0 + 0.5 * (a.P < a.E ? a.P : a.E);
   auto steps = [&](int64_t n, int64_t k) {
@@ -611,10 +613,8 @@ bool few_rows(const Mx4Args& a) {
   return steps(2 * (int64_t)a.f, a.d) + steps(a.d, a.f) <= 1.5 * ((double)a.d + (double)a.f);
 }
 
-}  // namespace
-
 int gemm_mx4_launch(int fc, bool a8, const Mx4Args& a, hipStream_t s) {
-  if (!few_rows(a)) {
+  if (!gemm_mx4_few_rows(a)) {
     if (fc == 1) return a8 ? launch_tiles<1, true>(a, s) : launch_tiles<1, false>(a, s);
     return a8 ? launch_tiles<2, true>(a, s) : launch_tiles<2, false>(a, s);
   }

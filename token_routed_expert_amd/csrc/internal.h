@@ -187,6 +187,7 @@ struct Mx4Args {
   void* o;
 };
 int gemm_mx4_launch(int fc, bool a8, const Mx4Args& a, hipStream_t s);
+bool gemm_mx4_few_rows(const Mx4Args& a);  // which of its two kernels (E, d, f and P decide)
 
 // permute.hip: rows of e4m3 codes [T][d] and their scales [T][d/128]
 int permute_e4m3_launch(const uint8_t* codes, const float* scales, const int32_t* row_of, int T,

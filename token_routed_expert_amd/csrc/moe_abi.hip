@@ -449,6 +449,16 @@ const char* moe_status_str(int status) {
   return "MOE_ERR_UNKNOWN";
 }
 
+int moe_few_rows(const moe_shape* sh) {
+  if (check_shape(sh) != MOE_OK) return 0;
+  if (sh->dtype == MOE_BF16)
+    return check_gemm_dims(sh, sh->T * sh->k, sh->f) == MOE_OK && few_rows(sh);
+  if (!is_mx4(sh) || check_mx4_dims(sh) != MOE_OK) return 0;
+  Mx4Args a = {};
+  a.E = (int)sh->E; a.d = (int)sh->d; a.f = (int)sh->f; a.P = (int)(sh->T * sh->k);
+  return gemm_mx4_few_rows(a);
+}
+
 size_t moe_workspace_bytes(const moe_shape* sh, int kind) {
   if (check_shape(sh) != MOE_OK) return 0;
   if (is_fp8(sh)) {

@@ -105,6 +105,11 @@ def moe_workspace_bytes(sh: N.moe_shape, kind: int) -> int:
     return int(N.lib().moe_workspace_bytes(C.byref(sh), kind))
 
 
+def moe_few_rows(sh: N.moe_shape) -> bool:
+    """Whether the MXFP4 or 8-bit checkpoint products of this shape take the kernels for few rows."""
+    return bool(N.lib().moe_few_rows(C.byref(sh)))
+
+
 def moe_status_str(status: int) -> str:
     return N.lib().moe_status_str(status).decode()
 
