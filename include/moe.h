@@ -276,7 +276,9 @@ typedef struct {
      the backward reads neither o nor a scaled dO, and row_prob [P] (written
      by the forward, read by the backward) holds each permuted row's
      probability; memory_efficient == 2 also recomputes h in the backward
-     (the forward's h need not be kept, io->h is then overwritten) */
+     (the forward's h need not be kept, io->h is then overwritten), and 3 is
+     the 8-bit checkpoint below (bf16 layers; e4m3 and MXFP8 layers refuse it
+     with MOE_ERR_UNSUPPORTED); other non-zero values act as 1 */
   float* row_prob;
   int32_t memory_efficient;
   /* MXFP8 layers (sh->dtype == MOE_MXFP8): the quantised weights (W1, W3, W2
@@ -309,9 +311,10 @@ typedef struct {
  * moe_grouped_gemm_fwd_e4m3, moe_unpermute (MOE_MXFP8: the _mx calls, weights
  * io->wmx).  For MOE_MXFP4 / MOE_MXFP4_A8: moe_route, the permutation's map,
  * moe_quantize_rows_mx4 / _mx of x, moe_grouped_gemm_fwd_mx4 reading x through
- * token_of, moe_unpermute (io->memory_efficient must be 0).  With io->aux_loss set, the routing is moe_route_aux and
- * moe_aux_loss_final (alpha = io->aux_alpha) follows the permutation;
- * ws_bytes then needs MOE_WS_AUX_LOSS more bytes.  With io->memory_efficient:
+ * token_of, moe_unpermute (io->memory_efficient must be 0).  With io->aux_loss
+ * set, the routing is moe_route_aux and moe_aux_loss_final (alpha =
+ * io->aux_alpha) follows the permutation; ws_bytes then needs MOE_WS_AUX_LOSS
+ * more bytes.  With io->memory_efficient:
  * moe_row_probs into io->row_prob, the row-scaled expert forward (bf16:
  * moe_grouped_gemm_fwd_rowscaled; e4m3 / MXFP8: fc1's epilogue scales h by p
  * before h is quantised) and an unweighted moe_unpermute.
@@ -621,12 +624,13 @@ int moe_grouped_gemm_bwd_ckpt8(const moe_shape* sh, const int32_t* offsets,
  * (the scale rounded up, so nothing saturates; s clamped to [-127, 127]; an
  * all-zero block has s = 0 and +0 codes); codes are E4M3FN(v * 2^-s), round
  * to nearest even.  A block that holds a NaN or an infinity has scale byte 255,
- * E8M0's NaN: every product it enters is NaN.  This scale rule departs from the OCP MX v1.0 reference
- * conversion (s = floor(log2 max|v|) - 8 with elements above 448 clamped),
- * which can clip a block's largest element by up to 12.5 %.  gfx950's v_mfma_scale_f32_16x16x128_f8f6f4 takes one E8M0
- * scale per lane, which is one 32-value block of one row, so the scales go
- * straight into the matrix instruction.  Scale bytes are stored row-major next
- * to the codes they scale:
+ * E8M0's NaN: every product it enters is NaN.  This scale rule departs from the
+ * OCP MX v1.0 reference conversion (s = floor(log2 max|v|) - 8 with elements
+ * above 448 clamped), which can clip a block's largest element by up to 12.5 %.
+ * gfx950's v_mfma_scale_f32_16x16x128_f8f6f4 takes one E8M0 scale per lane,
+ * which is one 32-value block of one row, so the scales go straight into the
+ * matrix instruction.  Scale bytes are stored row-major next to the codes they
+ * scale:
  *  - activation rows [rows][K] -> bytes [rows][K/32];
  *  - each weight matrix in both orientations (the blocks of the two differ):
  *    codes [E][R][C] with row-block bytes [E][R][C/32] (read by the
@@ -702,7 +706,9 @@ int moe_grouped_gemm_bwd_mx(const moe_shape* sh, const int32_t* offsets, const i
  * 32 consecutive values along a product's contraction axis.  s is the smallest
  * integer with max|v| <= 6 * 2^s (nothing saturates; at least -126; 0 for an
  * all-zero block, whose codes are zeros), codes are E2M1(v * 2^-s), round to
- * nearest even, sign kept.  A block that holds a NaN or an infinity has scale
+ * nearest even, sign kept.  (As for MXFP8 the scale is rounded up where the OCP
+ * MX v1.0 reference conversion takes s = floor(log2 max|v|) - 2 and clamps what
+ * lies above 6 * 2^s, up to 25 % of a block's largest value.)  A block that holds a NaN or an infinity has scale
  * byte 255, E8M0's NaN: every product it enters is NaN.  Forward only: there
  * are no weight gradients in this format (moe_layer_bwd returns
  * MOE_ERR_UNSUPPORTED).  moe_dequantize_weights_mx4 gives the bf16 weights that
@@ -717,7 +723,11 @@ int moe_grouped_gemm_bwd_mx(const moe_shape* sh, const int32_t* offsets, const i
  *          of rows 128 kt + 32 g .. + 31 of column 64 nb + 16 j + c.
  * W1 and W3 form one matrix W13 of N = 2f columns whose 16-column groups
  * alternate (group 2 i: columns 16 i .. of W1, group 2 i + 1: of W3).
- * d and f must be multiples of 128, no shared expert.
+ * d and f must be multiples of 128.  A layer call takes no shared expert
+ * (MOE_ERR_UNSUPPORTED); with one, make the layer's calls one by one: the shared
+ * expert is moe_grouped_gemm_fwd_mx4 of a shape {T, d, 1, 1, f_shared} on the same
+ * quantised rows, offsets {0, T} and token_of NULL, and its o is moe_unpermute's
+ * `add`.
  */
 
 /* Quantised expert weights as written by moe_quantize_weights_mx4. */
@@ -754,7 +764,8 @@ int moe_dequantize_weights_mx4(const uint8_t* codes, const uint8_t* scales, int6
  * and NaN blocks as above) and o [P][d] is bf16.  xq, xs are rows as
  * moe_quantize_rows_mx4 (MOE_MXFP4) or moe_quantize_rows_mx (MOE_MXFP4_A8)
  * writes them: row r is row token_of[r] of [T] rows, or, token_of NULL, row r
- * of [P] permuted rows; an entry outside [0, T) reads a row of zeros.  Rows of o from offsets[E] on are not written.
+ * of [P] permuted rows; an entry outside [0, T) reads a row of zeros.  Rows of o
+ * from offsets[E] on are not written.
  * ws_bytes >= moe_workspace_bytes(sh, MOE_WS_GEMM_FWD).  Errors: MOE_ERR_INVALID
  * for another dtype; MOE_ERR_UNSUPPORTED for d or f not a multiple of 128,
  * P * max(d, f) >= 2^31 - 4096 or d * f >= 2^31.

@@ -28,11 +28,11 @@
 // ones not with a single one), fc1's weight gradient with 2 to 15.  d 4096, 8192
 // rows, an eighth against together, us:
 //   experts, f   fc1, fc2 forward         fc2, fc1 data gradient   fc2, fc1 weight gradient
-//   1   14336    1815 836 / 1931 850      1050 1810 / 930 1556     785 1408 / 779 1417
-//   4   14336    1917 1082 / 1686 983     1014 2184 / 997 1942     798 1573 / 810 1545
-//   8   14336    1935 1038 / 1785 1018    1066 2141 / 1017 2064    918 2039 / 936 1719
-//   12  9600     1164 673 / 1142 655      745 1426 / 747 1397      691 1432 / 678 1333
-//   16  7168     1014 527 / 971 497       603 1092 / 617 1064      573 1077 / 571 1111
+//   1   14336    1815 836 / 1931 850      1050 1810 / 924 1540     785 1408 / 779 1417
+//   4   14336    1917 1082 / 1679 992     1014 2184 / 976 1955     798 1573 / 810 1546
+//   8   14336    1935 1038 / 1769 1038    1066 2141 / 992 2143     918 2039 / 936 1729
+//   12  9600     1164 673 / 1152 666      745 1426 / 725 1407      691 1432 / 678 1327
+//   16  7168     1014 527 / 975 505       603 1092 / 592 1066      573 1077 / 571 1100
 //   24  4736     753 351 / 696 341        489 712 / 485 707        443 859 / 440 895
 //   48  2432     482 205 / 486 207        262 448 / 287 450        334 700 / 324 694
 // and 256 experts, d 7168, f 2048, 131072 rows: fc1 forward 7712 / 8260, its data
