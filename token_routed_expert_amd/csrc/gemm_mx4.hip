@@ -590,19 +590,20 @@ int launch_tiles(const Mx4Args& a, hipStream_t s) {
 }  // namespace
 
 // Which kernel: the rows kernel reads a column group's weights once per 32 rows of
-// an expert and wins while they are read once or hardly more: at 16 rows an
-// expert on average it took 222 us (E2M1 rows) and 239 us (E4M3) where the tile
-// kernel took 232 and 241 us (128 experts, d 4096, f 1536), and 126 and 137 us
-// against 168 and 178 us (8 experts, f 14336); at 24 and 32 rows the tile kernel
-// wins (242 and 254 against 251 and 280 us; 172 and 177 against 198 and 232 us).
+// an expert and wins while they are read once or hardly more.  Calls with their
+// quantiser, E2M1 and E4M3 rows, against the tile kernel, us: 128 experts, d 4096,
+// f 1536: 16 rows an expert 229 and 250 against 243 and 245, 20 rows 239 and 265
+// against 244 and 249, 24 rows 254 and 284 against 251 and 257; 8 experts, f 14336:
+// 16 rows 127 and 139 against 170 and 177, 32 rows 193 and 224 against 173 and 185
+// (at 24 rows, hardly an expert with a second piece, it would still win: 132 and
+// 149 against 170 and 178).
 // It also wins while the latency of a block's K steps counts, of which it has a
 // quarter: while its blocks (pieces of 32 rows, an expert's last one half full on
 // average, times groups of 64 columns), in rounds of two to a compute unit, each
 // weighted with K, come to 1.5 rounds.  4 experts, d 384, f 2560: 97 rows an
-// expert (1.16 rounds) 18.6 and 21.0 against 27.6 and 33.3 us, 300 rows (1.67)
-// 26.6 and 35.7 against 25.1 and 31.7 us; 8 experts, d = f = 1024: 64 rows (1.12)
-// 18.3 and 20.3 against 21.9 and 25.6 us, 256 rows (3.19) 30.8 and 43.1 against
-// 22.8 and 29.8 us.
+// expert (1.16 rounds) 19 and 24 against 30 and 36 us, 300 rows (1.67) 30 and 40
+// against 29 and 34 us; 8 experts, d = f = 1024: 64 rows (1.12) 19 and 22 against
+// 24 and 28 us, 256 rows (3.19) 36 and 46 against 26 and 31 us.
 bool gemm_mx4_few_rows(const Mx4Args& a) {
   if ((int64_t)a.P <= 20 * (int64_t)a.E) return true;
   const double pieces = a.P / 32.0 + 0.5 * (a.P < a.E ? a.P : a.E);

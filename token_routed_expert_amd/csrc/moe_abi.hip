@@ -297,12 +297,12 @@ size_t dp_part_bytes(const moe_shape* sh) {
 // tiles) and weighted with the steps of a tile's contraction, are at most 2.75
 // times those of the 256 x 256 kernels, whose step takes about that much longer.
 // Forward and backward together, few-row kernels against the others, us: 128
-// experts, d 4096, f 1536: 32 rows an expert 3060 against 3213, 64 rows 3593
-// against 3405; 8 experts, d 4096, f 14336: 45 rows 1881 against 2238, 175 rows
-// 3287 against 2707; 16 experts, d 512, f 384: 500 rows 129 against 143, 875 rows
-// 180 against 161; 4 experts, d 384, f 3840: 600 rows 225 against 334, 2400 rows
-// 712 against 593; 24 experts, d 1152, f 1408: 125 rows 308 against 321, 183 rows
-// 365 against 343.
+// experts, d 4096, f 1536: 32 rows an expert 2987 against 3186, 64 rows 3537
+// against 3517; 8 experts, d 4096, f 14336: 45 rows 1811 against 2286, 175 rows
+// 3229 against 2735; 16 experts, d 512, f 384: 500 rows 131 against 147, 875 rows
+// 181 against 159; 4 experts, d 384, f 3840: 600 rows 220 against 350, 2400 rows
+// 711 against 597; 24 experts, d 1152, f 1408: 125 rows 305 against 320, 183 rows
+// 355 against 341.
 // (The few-row fc2 dgrad writes a probability partial per 128 columns, twice what
 // the workspace holds: they lie in dW2, which is written last, so they must fit
 // there.)
