@@ -36,9 +36,10 @@
 //   24  4736     753 351 / 696 341        489 712 / 485 707        443 859 / 440 895
 //   48  2432     482 205 / 486 207        262 448 / 287 450        334 700 / 324 694
 // and 256 experts, d 7168, f 2048, 131072 rows: fc1 forward 7712 / 8260, its data
-// gradient 7995 / 8425.  (fc1's data gradient reads more together, 7.5 GB against
-// 3.4 with 8 experts: its operands come through all eight L2s.  It is not bound by
-// memory and no slower for it.)  The weight gradients, whose tiles take as long as
+// gradient 7995 / 8425.  (With 8 experts fc1's data gradient reads more together,
+// 7.5 GB against 3.4: its operands come through all eight L2s.  Alone in the other
+// order, three runs in turn: 2165 / 2149, even rows 1573 / 1502; 16384 rows, d
+// 2048, f 5632: 879 / 788, with 16 experts 899 / 836.)  The weight gradients, whose tiles take as long as
 // their expert has rows, also go together when some eighth of their list has more
 // than 5/4 of an eighth of the rows: 64 experts, d 2048, f 1408, 12306 rows of
 // which one expert has 1912: 210 and 391 / 190 and 322; 128 even experts, d 4096,
@@ -149,7 +150,10 @@ __device__ __forceinline__ bf16x8_t lds_tr_pair(const char* p) {
 // the stage's barrier, so the read's latency hides under the MFMAs between.
 //
 // CK: the row-scaled products that write (fc1 forward) or read (fc2 dgrad) the
-// pre-activations in 8 bits; only the epilogue differs (store_tile).
+// pre-activations in 8 bits; only the epilogue differs (store_tile).  The fc1
+// forwards on permuted rows spill (row-scaled 7 vector registers, with CK 11, 48
+// bytes a lane), those on gathered rows do not; with CK, 65536 rows, 128 experts, d
+// 4096, f 1536, the former take 1440 us, the latter 1510.
 template <int OP, int NW, bool RS, bool GATHER = false, bool CK = false>
 __global__ __launch_bounds__(NW * 64, 1) void gemm_bf16_kernel(GemmArgs args, int NT, int MT) {
   constexpr int WAVES_N = NW / 2;
