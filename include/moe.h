@@ -63,7 +63,8 @@ extern "C" {
 typedef enum {
   MOE_OK = 0,
   MOE_ERR_INVALID = 1,      /* null pointer, inconsistent or out-of-range sizes */
-  MOE_ERR_UNSUPPORTED = 2,  /* valid but outside this build's limits (dtype, alignment) */
+  MOE_ERR_UNSUPPORTED = 2,  /* valid but outside this build's limits (dtype, alignment, sizes
+                               whose launch would need 2^32 threads or more) */
   MOE_ERR_WORKSPACE = 3,    /* ws_bytes smaller than moe_workspace_bytes() */
   MOE_ERR_HIP = 4           /* a HIP runtime call or kernel launch failed */
 } moe_status;
