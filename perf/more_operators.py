@@ -143,15 +143,15 @@ def _i4_groups(W, group, asym):
 
 def _i4_tiles(W, pair, group, asym):
     """The stored form: codes [E][N/16][K/128][4][16][16] (k group g, column, byte 4 j + b: rows 32 j + 8 g + b in the
-    low and + 4 in the high nibble of a tile's 128) and scale words [E][N/64][K/128][128/group][64] (the fp32 scale,
-    whose low four bits are the zero point).  `pair`: a second matrix whose 16-column groups alternate with W's."""
+    low and + 4 in the high nibble of a tile's 128) and scale words [E][N/64][K/128][128/group][16][4] (column & 15, column
+    / 16 & 3: the fp32 scale, whose low four bits are the zero point).  `pair`: a second matrix whose 16-column groups alternate with W's."""
     if pair is not None:
         W = torch.stack([W.unflatten(2, (-1, 16)), pair.unflatten(2, (-1, 16))], 3).flatten(2)
     E, K, N = W.shape
     q, s, z = _i4_groups(W, group, asym)
     n = q.view(E, K // 128, 4, 4, 2, 4, N // 16, 16)                     # kt, j, g, half, b, nt, c
     codes = (n[:, :, :, :, 0] | (n[:, :, :, :, 1] << 4)).permute(0, 5, 1, 3, 6, 2, 4).reshape(E, N // 16, K // 128, 4, 16, 16)
-    words = (s.view(torch.int32) | z).view(E, K // 128, 128 // group, N // 64, 64).permute(0, 3, 1, 2, 4)
+    words = (s.view(torch.int32) | z).view(E, K // 128, 128 // group, N // 64, 4, 16).permute(0, 3, 1, 2, 5, 4)
     return codes.contiguous(), words.contiguous()
 
 
@@ -162,7 +162,7 @@ def _i4_values(codes, words):
     c = codes.view(E, NT, KT, 4, 16, 4, 4)                               # nt, kt, g, c, j, b
     q = torch.stack([c & 15, c >> 4], 6).permute(0, 2, 5, 3, 6, 7, 1, 4)   # kt, j, g, half, b, nt, c
     q = q.reshape(E, KT * U, 128 // U, NT * 16).float()
-    w = words.permute(0, 2, 3, 1, 4).reshape(E, KT * U, 1, NT * 16)
+    w = words.permute(0, 2, 3, 1, 5, 4).reshape(E, KT * U, 1, NT * 16)
     v = (w & ~15).view(torch.float32) * (q - (w & 15).float())
     return v.to(torch.bfloat16).float().reshape(E, KT * 128, NT * 16)
 
@@ -322,7 +322,7 @@ def _own_weights(tre, s):
         E, R, C = W.shape
         N = C if pair is None else 2 * C
         s["buf"] = (torch.empty(E, N // 16, R // 128, 4, 16, 16, dtype=torch.uint8, device=DEV),
-                    torch.empty(E, N // 64, R // 128, 128 // group, 64, dtype=torch.int32, device=DEV),
+                    torch.empty(E, N // 64, R // 128, 128 // group, 16, 4, dtype=torch.int32, device=DEV),
                     [torch.empty(E, R, C, dtype=torch.bfloat16, device=DEV) for m in (W, pair) if m is not None])
     codes, scales, out = s["buf"]
     tre.moe_quantize_weights_i4(W, pair, group, s["case"]["asym"], codes, scales)
@@ -417,14 +417,14 @@ def _exact_column_groups(W, group, asym):
 
 
 def _exact_matrix(codes, words):
-    """One expert's tiles [N/16][K/128][4][16][16] and words [N/64][K/128][U][64] -> its weights [N][K], fp64."""
+    """One expert's tiles [N/16][K/128][4][16][16] and words [N/64][K/128][U][16][4] -> its weights [N][K], fp64."""
     NT, KT = codes.shape[:2]
     U = words.shape[2]
     q = torch.empty(NT, 16, KT, 128, dtype=torch.float64, device=codes.device)
     for k in range(128):
         j, g, half, b = k // 32, k // 8 % 4, k // 4 % 2, k % 4
         q[:, :, :, k] = ((codes[:, :, g, :, 4 * j + b] >> (4 * half)) & 15).permute(0, 2, 1).double()
-    w = words.permute(0, 3, 1, 2).reshape(NT, 16, KT, U).repeat_interleave(128 // U, dim=3)
+    w = words.permute(0, 4, 3, 1, 2).reshape(NT, 16, KT, U).repeat_interleave(128 // U, dim=3)
     z = w % 16
     s = (w - z).view(torch.float32).double()
     return (s * (q - z)).to(torch.bfloat16).double().reshape(NT * 16, KT * 128)
