@@ -94,7 +94,8 @@ typedef enum {
   MOE_WS_LAYER_BWD = 4,
   MOE_WS_AUX_LOSS = 5,
   MOE_WS_GEMM_BWD_ROWSCALED = 6,
-  MOE_WS_LAYER_BWD_ROWSCALED = 7
+  MOE_WS_LAYER_BWD_ROWSCALED = 7,
+  MOE_WS_NORM_BWD = 8 /* moe_add_rms_norm_bwd: the shape's T and d count */
 } moe_ws_kind;
 
 /*
@@ -301,6 +302,11 @@ typedef struct {
      bytes ab_s [P][2f/32] between forward and backward; ab is not used */
   uint8_t* ab_q;
   uint8_t* ab_s;
+  /* e4m3, MXFP8 and MXFP4 layers: when x_quantized != 0, xq and xs hold x's
+     quantised rows already (from moe_add_rms_norm) and moe_layer_fwd reads them
+     in place of quantising x (x itself is read by the backward alone and may be
+     NULL in the forward); other layers ignore it */
+  int32_t x_quantized;
 } moe_layer_io;
 
 /*
@@ -777,6 +783,66 @@ int moe_dequantize_weights_mx4(const uint8_t* codes, const uint8_t* scales, int6
 int moe_grouped_gemm_fwd_mx4(const moe_shape* sh, const int32_t* offsets, const int32_t* token_of,
                              const uint8_t* xq, const uint8_t* xs, const moe_mx4_weights* w,
                              void* o, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The norm in front of a layer
+ * ----------------------------
+ * A transformer block hands the layer x = norm(residual stream).  The pages
+ * keep activations in 8 bits and fuse the elementwise steps into few kernels
+ * (German summary, section 2 D and 2 E) without a recipe; the norm is the root-
+ * mean-square one, and the rows that a layer's products read are quantised from
+ * it in the same pass.
+ *
+ * moe_add_rms_norm -- for each of T rows of d values (dtype MOE_BF16 or MOE_F32:
+ * the type of x, residual, gamma, sum and y)
+ *   s = x + residual, rounded to dtype (residual NULL: s = x)
+ *   rstd = 1 / sqrt(mean(s^2) + eps),  v = s rstd gamma   (fp32)
+ *   sum  out [T][d]: s (may be NULL; with a residual it is the new residual
+ *        stream and what the backward reads)
+ *   y    out [T][d]: v rounded to dtype (may be NULL)
+ *   rstd out fp32 [T] (may be NULL)
+ *   codes, scales out (both or neither): v quantised row by row, straight from
+ *        fp32, q_dtype (ignored without them) MOE_E4M3 (moe_quantize_rows'
+ *        rule: codes [T][d], fp32 scales [T][d/128]), MOE_MXFP8
+ *        (moe_quantize_rows_mx's with s at least -126: codes [T][d], bytes
+ *        [T][d/32]) or MOE_MXFP4 (moe_quantize_rows_mx4's: codes [T][d/2], bytes
+ *        [T][d/32]).  A block with a NaN or an infinity reads back as NaN (scale
+ *        byte 255; MOE_E4M3: the scale is NaN).
+ * A layer takes them as io->xq and io->xs with io->x_quantized set.  sum may be
+ * x or residual, and y may be x, residual or sum.  The squares are added in fp32,
+ * so |s| up to 2^63 / sqrt(d) is in range.  T = 0 does nothing.  Errors:
+ * MOE_ERR_INVALID for null x or gamma, no output, codes without scales, T < 0, d
+ * < 1, eps negative or not finite; MOE_ERR_UNSUPPORTED for d not a multiple of 8
+ * (128 for E4M3 rows, 32 for MX rows) or above 32768, T >= 2^31, other types,
+ * misaligned pointers.
+ */
+int moe_add_rms_norm(const void* x, const void* residual, const void* gamma, int32_t dtype, int64_t T, int64_t d,
+                     float eps, void* sum, void* y, float* rstd, int32_t q_dtype, uint8_t* codes, void* scales,
+                     void* stream);
+
+/*
+ * moe_add_rms_norm_bwd -- its gradients for the upstream gradient dy [T][d] of y
+ * and, dsum not NULL, dsum [T][d] of sum: with g = dy gamma
+ *   dx     out [T][d] = dsum + rstd (g - s rstd^2 mean(g s))  (of x and of the
+ *          residual alike), rounded once
+ *   dgamma out [d] = sum over the rows of dy s rstd, in fp32, rounded once (T = 0:
+ *          zeros)
+ * from the forward's sum and rstd (without a residual: x).  Deterministic.
+ * dx may be dy or dsum.  ws_bytes >= moe_workspace_bytes of a shape with this T
+ * and d, MOE_WS_NORM_BWD.  Types, limits and errors as moe_add_rms_norm.
+ */
+int moe_add_rms_norm_bwd(const void* dy, const void* sum, const float* rstd, const void* gamma, const void* dsum,
+                         int32_t dtype, int64_t T, int64_t d, void* dx, void* dgamma, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/*
+ * moe_dequantize_rows -- the values that quantised rows [rows][cols] stand for
+ * (q_dtype MOE_E4M3, MOE_MXFP8 or MOE_MXFP4, as moe_quantize_rows, _rows_mx,
+ * _rows_mx4 and moe_add_rms_norm write them), dst [rows][cols] MOE_BF16 or
+ * MOE_F32: code times scale in fp32, rounded once.
+ */
+int moe_dequantize_rows(const uint8_t* codes, const void* scales, int32_t q_dtype, int64_t rows, int64_t cols,
+                        void* dst, int32_t dst_dtype, void* stream);
 
 /* moe_probe_mfma -- measurement helper, not a step of the layer: the dense
  * matrix-core rate and the shader clock this GPU sustains under MFMAs alone,

@@ -23,3 +23,4 @@ from .router import *  # noqa: F401,F403
 from .mx import *  # noqa: F401,F403
 from .mx4 import *  # noqa: F401,F403
 from .ckpt8 import *  # noqa: F401,F403
+from .norm import *  # noqa: F401,F403

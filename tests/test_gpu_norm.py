@@ -1,0 +1,440 @@
+"""The norm with residual addition and quantised rows, its gradients and the rows'
+reading back, on the GPU against the oracle, through the C ABI.
+
+Tolerances.  u = 2^-24 is the fp32 half step, h the storage type's (bf16 2^-8,
+fp32 2^-24; a bf16 result also has its fp32 value's error).
+* sum: fp32 addition rounded to storage: bit-exact.  (The fp32 sum of two bf16
+  numbers is exact unless their exponents are over 16 apart, and then it is not
+  next to a midpoint of bf16.)
+* rstd: a sum of d squares in any order is off by at most (d + 1) u (all terms are
+  positive), the quotient, eps, root and reciprocal by 4 u: rstd by (d / 2 + 5) u.
+* v = s rstd gamma: two products more: e = (d / 2 + 7) u relative; y: h + e.
+* codes of v: the E4M3 scale is off by e + 2 u, the MX scale is that of an amax
+  within e; the value read back is within half a step of v: 2^-4 |v| plus half the
+  format's smallest step, 2^-10 scales (E2M1: 2^-2 |v| and 0.25 scales), plus e |v|.
+  fp32 norms store v itself as y, so their codes are exactly those of y.
+* dx: the mean's sum rounds by (d + 4) u mean|g s|, the rest by 8 u of the terms' sizes.
+* dgamma: (T + 8) u sum|dy s rstd|, plus h.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from moe_workloads import Workload, make_inputs, to_f64
+
+from gpu_common import announce, need_gpu
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+BF16, F32 = torch.bfloat16, torch.float32
+H = {BF16: 2.0 ** -8, F32: U}
+EPS = 1e-6
+
+
+@pytest.fixture(autouse=True)
+def _gpu(request):
+    need_gpu()
+    announce(request.node.nodeid)
+    yield
+    torch.cuda.synchronize()
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def rows_buffers(T, d, fmt, guard=0):
+    n = T * d
+    codes = torch.full((n // (2 if fmt == "mxfp4" else 1) + guard,), 0xA5, dtype=torch.uint8, device="cuda")
+    if fmt == "e4m3":
+        return codes, torch.full((n // 128 + guard,), -7.0, device="cuda")
+    return codes, torch.full((n // 32 + guard,), 0xA5, dtype=torch.uint8, device="cuda")
+
+
+def stream_rows(T, d, dtype, seed, special=True):
+    g = torch.Generator().manual_seed(seed)
+    x, r = torch.randn(T, d, generator=g), torch.randn(T, d, generator=g) * torch.exp(torch.randn(T, 1, generator=g))
+    if special and T >= 5:
+        x[1], r[1] = 0, 0                                     # a row of zeros
+        x[2], r[2] = 0, 0
+        x[2, d // 2] = 3.0                                    # one value
+        x[3] *= 1e-18
+        r[3] *= 1e-18
+        x[4] *= 1e12
+    gamma = 1 + 0.3 * torch.randn(d, generator=g)
+    return tuple(t.to(dtype).cuda() for t in (x, r, gamma))
+
+
+SIZES = [(1, 8), (3, 40), (1, 4096), (5, 128), (7, 384), (177, 7168), (33, 8320), (2, 32768), (4096, 256), (4097, 1152),
+         (4099, 5120), (4096, 8192), (513, 2048), (4100, 16384 // 16)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("residual", [True, False])
+@pytest.mark.parametrize("T,d", SIZES)
+def test_norm(T, d, residual, dtype):
+    import token_routed_expert_amd as tre
+    x, r, gamma = stream_rows(T, d, dtype, T + d)
+    guard = 64
+    out = [torch.full((T * d + guard,), 5.0, dtype=dtype, device="cuda") for _ in range(2)]
+    rstd = torch.full((T + guard,), 5.0, device="cuda")
+    tre.moe_add_rms_norm(x, r if residual else None, gamma, EPS, out[0], out[1], rstd)
+    s = (x.float() + r.float()).to(dtype) if residual else x
+    assert torch.equal(out[0][:-guard].view(T, d), s)
+    want, wr = oracle.rms_norm(f64(s), f64(gamma), EPS)
+    got_r = f64(rstd[:-guard])
+    assert (np.abs(got_r - wr) <= (d / 2 + 5) * U * wr).all()
+    e = (d / 2 + 7) * U
+    tol = (e + H[dtype] * (1 + e)) * np.abs(want) + 2.0 ** -149
+    assert (np.abs(f64(out[1][:-guard].view(T, d)) - want) <= tol).all()
+    for t in (*out, rstd):
+        assert (t[-guard:] == 5.0).all()
+
+
+def read_back(fmt, codes, scales, T, d, dtype=F32):
+    import token_routed_expert_amd as tre
+    v = torch.empty(T, d, dtype=dtype, device="cuda")
+    tre.moe_dequantize_rows(codes, scales, fmt, v)
+    return v
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "mxfp8", "mxfp4"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,d", [s for s in SIZES if s[1] % 128 == 0] + [(9, 96), (4096, 32)])
+def test_quantised_rows(T, d, dtype, fmt):
+    import token_routed_expert_amd as tre
+    if d % 128 and fmt == "e4m3":
+        pytest.skip("E4M3 blocks have 128 values")
+    x, r, gamma = stream_rows(T, d, dtype, T + d)
+    codes, scales = rows_buffers(T, d, fmt, 16)
+    y = torch.empty_like(x)
+    tre.moe_add_rms_norm(x, r, gamma, EPS, None, y, None, fmt, codes, scales)
+    assert (codes[-16:] == 0xA5).all() and (scales[-16:] == (-7.0 if fmt == "e4m3" else 0xA5)).all()
+    want, _ = oracle.rms_norm(f64((x.float() + r.float()).to(dtype)), f64(gamma), EPS)
+    got = f64(read_back(fmt, codes, scales, T, d))
+    per = 128 if fmt == "e4m3" else 32
+    if fmt == "e4m3":
+        sc = f64(scales[:-16])
+        ref = np.abs(want).reshape(-1, per).max(1)
+        ref = np.where(ref == 0, 1.0, ref / 448)
+        assert (np.abs(sc - ref) <= ((d / 2 + 9) * U) * ref).all()
+    else:
+        sc = np.exp2(f64(scales[:-16]) - 127)
+        amax = np.abs(want).reshape(-1, per).max(1)
+        top = 448 if fmt == "mxfp8" else 6
+        e = (d / 2 + 7) * U
+        assert (amax <= top * sc * (1 + e)).all()                              # nothing saturates
+        assert ((amax >= top / 2 * sc * (1 - e)) | (amax == 0) | (sc == 2.0 ** -126)).all()   # and no binade is lost
+    sc = np.repeat(sc, per).reshape(T, d)
+    half, least = (0.25, 0.25) if fmt == "mxfp4" else (2.0 ** -4, 2.0 ** -10)
+    assert (np.abs(got - want) <= (half + (d + 20) * U) * np.abs(want) + least * sc * (1 + 1e-6)).all()
+    if dtype == F32:                                                           # y is v: the quantisers' own codes
+        c2, s2 = rows_buffers(T, d, fmt)
+        quant = {"e4m3": tre.moe_quantize_rows, "mxfp8": tre.moe_quantize_rows_mx, "mxfp4": tre.moe_quantize_rows_mx4}[fmt]
+        quant(y, c2, s2)
+        assert torch.equal(codes[:-16], c2) and torch.equal(scales[:-16], s2)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "mxfp8", "mxfp4"])
+def test_rows_read_back_every_code(fmt):
+    """All codes under several scales, against the oracle's tables."""
+    rng = np.random.default_rng(5)
+    T, d = 37, 512
+    if fmt == "mxfp4":
+        codes = rng.integers(0, 256, (T, d // 2)).astype(np.uint8)
+    else:
+        codes = np.tile(np.arange(256, dtype=np.uint8), T * d // 256).reshape(T, d)
+        codes[(codes & 127) == 127] = 0x13                                     # (NaN codes apart)
+    if fmt == "e4m3":
+        scales = np.exp2(rng.uniform(-20, 20, (T, d // 128))).astype(np.float32)
+        scales[3, 1] = np.nan
+        want = oracle.dequant_rows(codes, scales)
+    else:
+        scales = rng.integers(1, 250, (T, d // 32)).astype(np.uint8)
+        scales[3, 1], scales[4, 0] = 255, 0
+        want = (oracle.dequant_mx4_rows if fmt == "mxfp4" else oracle.dequant_mx8_rows)(codes, scales)
+    for dtype in (F32, BF16):
+        got = read_back(fmt, torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), T, d, dtype)
+        with np.errstate(over="ignore", invalid="ignore"):
+            ref = torch.from_numpy(np.asarray(want, np.float64).astype(np.float32)).to(dtype)
+        assert torch.equal(torch.nan_to_num(got.cpu(), nan=1e30), torch.nan_to_num(ref, nan=1e30))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_non_finite_rows(bad, dtype):
+    """A NaN or an infinity makes its own row NaN (an infinity: zeros and a NaN) in every form; others keep their bits."""
+    import token_routed_expert_amd as tre
+    T, d = 9, 384
+    x, r, gamma = stream_rows(T, d, dtype, 3, special=False)
+    for fmt in ("e4m3", "mxfp8", "mxfp4"):
+        res = []
+        for v in (0.5, bad):
+            x[4, 130] = v
+            codes, scales = rows_buffers(T, d, fmt)
+            y = torch.empty_like(x)
+            tre.moe_add_rms_norm(x, r, gamma, EPS, None, y, None, fmt, codes, scales)
+            res.append((y, read_back(fmt, codes, scales, T, d)))
+        (y0, v0), (y1, v1) = res
+        keep = [i for i in range(T) if i != 4]
+        assert torch.equal(y0[keep], y1[keep]) and torch.equal(v0[keep], v1[keep])
+        assert torch.isnan(y1[4, 130]) and torch.isnan(v1[4, 130])
+        block = slice(128, 256) if fmt == "e4m3" else slice(128, 160)
+        assert torch.isnan(v1[4, block]).all()
+        if bad != bad:
+            assert torch.isnan(y1[4]).all() and torch.isnan(v1[4]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,d", [(6, 512), (5000, 512), (300, 16384), (3, 40)])
+def test_in_place(T, d, dtype):
+    """sum over x or the residual, y over any of them, dx over dy or dsum."""
+    import token_routed_expert_amd as tre
+    x, r, gamma = stream_rows(T, d, dtype, 11)
+    sum_, y, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(T, device="cuda")
+    tre.moe_add_rms_norm(x, r, gamma, EPS, sum_, y, rstd)
+    for over in ("x", "r"):
+        x2, r2 = x.clone(), r.clone()
+        tre.moe_add_rms_norm(x2, r2, gamma, EPS, x2 if over == "x" else r2, r2 if over == "x" else x2, None)
+        a, b = (x2, r2) if over == "x" else (r2, x2)
+        assert torch.equal(a, sum_) and torch.equal(b, y)
+    x2 = x.clone()
+    tre.moe_add_rms_norm(x2, r, gamma, EPS, None, x2, None)
+    assert torch.equal(x2, y)
+    dy, ds = torch.randn_like(x), torch.randn_like(x)
+    ws = bwd_ws(T, d)
+    dx, dg = torch.empty_like(x), torch.empty_like(gamma)
+    tre.moe_add_rms_norm_bwd(dy, sum_, rstd, gamma, ds, dx, dg, ws)
+    for over in (0, 1):
+        t = [dy.clone(), ds.clone()]
+        dg2 = torch.empty_like(gamma)
+        tre.moe_add_rms_norm_bwd(t[0], sum_, rstd, gamma, t[1], t[over], dg2, ws)
+        assert torch.equal(t[over], dx) and torch.equal(dg, dg2)
+
+
+def bwd_ws(T, d):
+    import token_routed_expert_amd as tre
+    n = tre.moe_workspace_bytes(tre.make_shape(T, d, 1, 1, 128), tre.MOE_WS_NORM_BWD)
+    return torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")           # NaNs: the call may not read them
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dsum", [True, False])
+@pytest.mark.parametrize("T,d", SIZES + [(2049, 1024), (257, 512), (1025, 4096), (1, 16384)])
+def test_bwd(T, d, dsum, dtype):
+    import token_routed_expert_amd as tre
+    x, r, gamma = stream_rows(T, d, dtype, T + d, special=False)
+    g = torch.Generator().manual_seed(9)
+    dy, ds = (torch.randn(T, d, generator=g).to(dtype).cuda() for _ in range(2))
+    sum_, rstd = torch.empty_like(x), torch.empty(T, device="cuda")
+    tre.moe_add_rms_norm(x, r, gamma, EPS, sum_, None, rstd)
+    guard = 64
+    dx = torch.full((T * d + guard,), 5.0, dtype=dtype, device="cuda")
+    dg = torch.full((d + guard,), 5.0, dtype=dtype, device="cuda")
+    tre.moe_add_rms_norm_bwd(dy, sum_, rstd, gamma, ds if dsum else None, dx, dg, bwd_ws(T, d))
+    assert (dx[-guard:] == 5.0).all() and (dg[-guard:] == 5.0).all()
+    s, dyn, gn, rn = f64(sum_), f64(dy), f64(gamma), f64(rstd)[:, None]
+    wx, wg = oracle.rms_norm_bwd(dyn, s, rn[:, 0], gn, f64(ds) if dsum else None)
+    gs, xh = np.abs(dyn * gn), np.abs(s * rn)
+    size = rn * (gs + xh * (gs * xh).mean(1, keepdims=True)) + (np.abs(f64(ds)) if dsum else 0)
+    tol = H[dtype] * (np.abs(wx) + 1e-6 * size) + 8 * U * size + (d + 4) * U * rn * xh * (gs * xh).mean(1, keepdims=True)
+    assert (np.abs(f64(dx[:-guard].view(T, d)) - wx) <= tol).all()
+    size = np.abs(dyn * s * rn).sum(0)
+    assert (np.abs(f64(dg[:-guard]) - wg) <= H[dtype] * (np.abs(wg) + 1e-3 * size) + (T + 8) * U * size).all()
+
+
+def test_gradients_against_differences():
+    """<dx, u> and <dgamma, w> of the fp32 kernels against central differences of the oracle's forward in 64 bits: the
+    difference's own error is below 1e-7 of the sizes, the kernels' (d + 12) u of them."""
+    import token_routed_expert_amd as tre
+    T, d = 5, 264
+    x, _, gamma = stream_rows(T, d, F32, 1, special=False)
+    dy = torch.randn(T, d, generator=torch.Generator().manual_seed(2)).cuda()
+    rstd, dx, dg = torch.empty(T, device="cuda"), torch.empty_like(x), torch.empty_like(gamma)
+    tre.moe_add_rms_norm(x, None, gamma, EPS, None, None, rstd)
+    tre.moe_add_rms_norm_bwd(dy, x, rstd, gamma, None, dx, dg, bwd_ws(T, d))
+    xn, gn, dyn = f64(x), f64(gamma), f64(dy)
+    rng = np.random.default_rng(4)
+    for _ in range(8):
+        u, w, h = rng.standard_normal((T, d)), rng.standard_normal(d), 1e-5
+
+        def loss(k):
+            return float((oracle.rms_norm(xn + k * h * u, gn + k * h * w, EPS)[0] * dyn).sum())
+        num = (loss(1) - loss(-1)) / (2 * h)
+        got = float((f64(dx) * u).sum() + (f64(dg) * w).sum())
+        size = np.abs(f64(dx) * u).sum() + np.abs(f64(dg) * w).sum()
+        assert abs(num - got) <= (1e-7 + (d + 12) * U) * 4 * size
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_no_rows(dtype):
+    import token_routed_expert_amd as tre
+    d = 256
+    e = torch.empty(0, d, dtype=dtype, device="cuda")
+    dg = torch.full((d,), 7.0, dtype=dtype, device="cuda")
+    one = torch.ones(d, dtype=dtype, device="cuda")
+    x = torch.zeros(1, d, dtype=dtype, device="cuda")          # (a tensor without values has no address)
+    from token_routed_expert_amd import _native as N
+    import ctypes as C
+    p = [C.c_void_p(t.data_ptr()) for t in (x, one, dg)]
+    rs = C.c_void_p(torch.zeros(1, device="cuda").data_ptr())
+    code = N.MOE_BF16 if dtype == BF16 else N.MOE_F32
+    st = torch.cuda.current_stream().cuda_stream
+    assert N.lib().moe_add_rms_norm_bwd(p[0], p[0], rs, p[1], None, code, 0, d, p[0], p[2], None, 0, st) == N.MOE_OK
+    assert (dg == 0).all() and e.numel() == 0 and (x == 0).all()
+
+
+def test_python_calls_check_their_tensors():
+    import token_routed_expert_amd as tre
+    x, g, r = (torch.zeros(*s, device="cuda") for s in ((4, 128), (128,), (4,)))
+    c, s = torch.zeros(4, 128, dtype=torch.uint8, device="cuda"), torch.zeros(4, 1, device="cuda")
+    ws = torch.zeros(4 * 128 * 4, dtype=torch.uint8, device="cuda")
+    good = dict(x=x, residual=x, gamma=g, eps=1e-6, sum_=None, y=x.clone(), rstd=r, q_dtype="e4m3", codes=c, scales=s)
+    tre.moe_add_rms_norm(**good)
+    for bad, text in ((dict(gamma=g[:64]), "gamma has"), (dict(gamma=g.bfloat16()), "gamma: expected"),
+                      (dict(residual=x[:3]), "residual has"), (dict(sum_=x.bfloat16()), "sum: expected"),
+                      (dict(rstd=r.double()), "rstd: expected"), (dict(codes=c[:3]), "codes has"),
+                      (dict(scales=s[:3]), "scales has"), (dict(scales=s.to(torch.uint8)), "scales: expected"),
+                      (dict(q_dtype="bf16"), "rows are"), (dict(q_dtype=None), "need q_dtype"),
+                      (dict(x=x.half()), "bfloat16 or float32"), (dict(y=x.t()), "contiguous"),
+                      (dict(residual=x.cpu()), "device"), (dict(y=torch.zeros(513, device="cuda")[1:]), "aligned")):
+        with pytest.raises((TypeError, ValueError), match=text):
+            tre.moe_add_rms_norm(**{**good, **bad})
+    good = dict(dy=x, sum_=x, rstd=r, gamma=g, dsum=x, dx=x.clone(), dgamma=g.clone(), ws=ws)
+    tre.moe_add_rms_norm_bwd(**good)
+    for bad, text in ((dict(sum_=x[:3]), "sum has"), (dict(rstd=r[:3]), "rstd has"), (dict(gamma=g[:64]), "gamma has"),
+                      (dict(dsum=x[:3]), "dsum has"), (dict(dx=x.bfloat16()), "dx: expected"),
+                      (dict(dgamma=g[:64]), "dgamma has"), (dict(ws=ws[:-1]), "WORKSPACE"), (dict(ws=None), "WORKSPACE")):
+        with pytest.raises((TypeError, ValueError, tre.MoeError), match=text):
+            tre.moe_add_rms_norm_bwd(**{**good, **bad})
+    for bad, text in ((dict(codes=c[:3]), "codes has"), (dict(scales=s[:3]), "scales has"),
+                      (dict(q_dtype="f32"), "rows are"), (dict(dst=x.half()), "bfloat16 or float32")):
+        with pytest.raises((TypeError, ValueError), match=text):
+            tre.moe_dequantize_rows(**{**dict(codes=c, scales=s, q_dtype="e4m3", dst=x.clone()), **bad})
+
+
+LAYERS = [Workload("norm_e4m3", T=70, d=256, E=8, k=2, f=256, dtype="e4m3"),
+          Workload("norm_mx", T=70, d=256, E=8, k=2, f=256, dtype="mxfp8"),
+          Workload("norm_mx4", T=70, d=256, E=8, k=2, f=256, dtype="mxfp4"),
+          Workload("norm_mx4a8", T=1, d=256, E=8, k=2, f=256, dtype="mxfp4_a8")]
+
+
+def layer_of(wl, seed=0, **kw):
+    """Buffers of a layer; MXFP4 ones with quantised weights of their own (fp32 masters otherwise)."""
+    from token_routed_expert_amd.buffers import layer_buffers
+    mx4 = wl.dtype.startswith("mxfp4")
+    inp = make_inputs(wl.with_(dtype="bf16") if mx4 else wl, seed=seed, device="cuda")
+    return layer_buffers(wl.T, wl.d, wl.E, wl.k, wl.f, 0, wl.dtype, "cuda", inp, **kw)
+
+
+@pytest.mark.parametrize("me", [0, 1])
+@pytest.mark.parametrize("wl", LAYERS, ids=lambda w: w.name)
+def test_layer_takes_quantised_rows(wl, me):
+    """The layer on rows that are there already: the bits of the layer that makes them, without reading x."""
+    import token_routed_expert_amd as tre
+    if me and wl.dtype.startswith("mxfp4"):
+        pytest.skip("MXFP4 layers have no memory-efficient form")
+    sh, b, wsf, _ = layer_of(wl, **({"memory_efficient": me} if me else {}))
+    tre.moe_layer_fwd(sh, b, wsf)
+    want = b["y"].clone()
+    b["y"].fill_(float("nan"))
+    b["o"].fill_(float("nan"))
+    x = b.pop("x")
+    x.fill_(float("nan"))
+    b["x_quantized"] = 1
+    tre.moe_layer_fwd(sh, b, wsf)
+    assert torch.equal(b["y"], want)
+
+
+@pytest.mark.parametrize("wl", LAYERS, ids=lambda w: w.name)
+def test_norm_into_layer(wl):
+    """A block as a program runs it: residual addition, norm and rows in one call, router logits from y, the layer on the
+    rows.  Against the layer's calls made one by one on the same codes."""
+    import token_routed_expert_amd as tre
+    sh, b, wsf, _ = layer_of(wl)
+    T, d = wl.T, wl.d
+    g = torch.Generator().manual_seed(7)
+    stream, delta = (torch.randn(T, d, generator=g).to(BF16).cuda() for _ in range(2))
+    gamma = (1 + 0.2 * torch.randn(d, generator=g)).to(BF16).cuda()
+    gate = torch.randn(d, wl.E, generator=g).cuda()
+    y, sum_ = torch.empty_like(stream), torch.empty_like(stream)
+    fmt = "mxfp8" if wl.dtype == "mxfp4_a8" else wl.dtype
+    tre.moe_add_rms_norm(delta, stream, gamma, EPS, sum_, y, None, fmt, b["xq"], b["xs"])
+    b["logits"] = y.float() @ gate
+    b["x"], b["x_quantized"] = y, 1
+    tre.moe_layer_fwd(sh, b, wsf)
+    got = b["y"].clone()
+    # the same steps one by one, the rows permuted by hand
+    vals = read_back(fmt, b["xq"], b["xs"], T, d)
+    err = (vals - y.float()).abs()
+    step = {"e4m3": 2.0 ** -4, "mxfp8": 2.0 ** -4, "mxfp4": 0.25}[fmt]
+    amax = y.float().abs().amax(1, keepdim=True)
+    assert (err <= (step + 2.0 ** -8) * y.float().abs() + amax * {"mxfp4": 0.25 / 3, "mxfp8": 2.0 ** -17, "e4m3": 2.0 ** -17}[fmt] * 1.01).all()
+    tok = b["token_of"].long()
+    assert torch.equal(b["row_of"].view(-1)[torch.argsort(b["row_of"].view(-1))].long(), torch.arange(T * wl.k).cuda())
+    if not wl.dtype.startswith("mxfp4"):
+        per = {"e4m3": 128, "mxfp8": 32}[fmt]
+        assert torch.equal(b["xpq"], b["xq"][tok]) and torch.equal(b["xps"].view(-1, d // per), b["xs"].view(-1, d // per)[tok])
+    o = b["o"].float()[b["row_of"].long()]
+    want = (o * b["topk_prob"][..., None]).sum(1)
+    assert ((got.float() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20 * (o.abs() * b["topk_prob"][..., None]).sum(1)).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_side_stream_and_graph(dtype):
+    """Forward and backward captured on a side stream: every replay gives the eager bits, with other work between."""
+    import token_routed_expert_amd as tre
+    T, d = 1030, 1024
+    x, r, gamma = stream_rows(T, d, dtype, 5)
+    dy = torch.randn_like(x)
+    fmt = "mxfp8"
+    bufs = [torch.empty_like(x), torch.empty_like(x), torch.empty(T, device="cuda"), *rows_buffers(T, d, fmt),
+            torch.empty_like(x), torch.empty_like(gamma)]
+    sum_, y, rstd, codes, scales, dx, dg = bufs
+    ws = bwd_ws(T, d)
+
+    def step():
+        tre.moe_add_rms_norm(x, r, gamma, EPS, sum_, y, rstd, fmt, codes, scales)
+        tre.moe_add_rms_norm_bwd(dy, sum_, rstd, gamma, r, dx, dg, ws)
+    step()
+    torch.cuda.synchronize()
+    eager = [t.clone() for t in bufs]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    for _ in range(3):
+        for t in bufs:
+            t.fill_(3)
+        ws.fill_(255)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(eager, bufs))
+    del graph
+
+
+def test_training_through_the_norm_and_a_layer():
+    """Norm, bf16 layer, and back: the gradient of the residual stream against the oracle's chain on the device's own dX."""
+    import token_routed_expert_amd as tre
+    from token_routed_expert_amd.buffers import layer_buffers
+    wl = Workload("norm_train", T=130, d=256, E=8, k=2, f=256)
+    inp = make_inputs(wl, seed=3, device="cuda")
+    x, r, gamma = stream_rows(wl.T, wl.d, BF16, 8, special=False)
+    sum_, y, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(wl.T, device="cuda")
+    tre.moe_add_rms_norm(x, r, gamma, EPS, sum_, y, rstd)
+    inp["x"] = y
+    sh, b, wsf, wsb = layer_buffers(wl.T, wl.d, wl.E, wl.k, wl.f, 0, wl.dtype, "cuda", inp)
+    tre.moe_layer_fwd(sh, b, wsf)
+    tre.moe_layer_bwd(sh, b, wsb)
+    dx, dg = torch.empty_like(x), torch.empty_like(gamma)
+    # the stream goes on past the layer: its gradient is dY as well
+    tre.moe_add_rms_norm_bwd(b["dX"], sum_, rstd, gamma, b["dY"], dx, dg, bwd_ws(wl.T, wl.d))
+    st = oracle.layer_fwd(inp["logits"].cpu().numpy(), f64(y), to_f64(inp["W1"]), to_f64(inp["W3"]), to_f64(inp["W2"]), wl.k)
+    gr = oracle.layer_bwd(st, to_f64(inp["dY"]), to_f64(inp["W1"]), to_f64(inp["W3"]), to_f64(inp["W2"]))
+    assert oracle.row_rel_err(f64(b["dX"]), gr["dX"]) <= 2e-2
+    wx, wg = oracle.rms_norm_bwd(f64(b["dX"]), f64(sum_), f64(rstd), f64(gamma), f64(b["dY"]))
+    assert oracle.row_rel_err(f64(dx), wx) <= 2.0 ** -8 + 1e-4
+    assert (np.abs(f64(dg) - wg) <= 2.0 ** -8 * np.abs(wg) + 1e-4 * np.abs(f64(b["dX"]) * f64(sum_) * f64(rstd)[:, None]).sum(0)).all()

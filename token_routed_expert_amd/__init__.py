@@ -6,7 +6,7 @@ this package only marshals torch tensors into its calls.
 from . import _native
 from ._native import (MOE_WS_AUX_LOSS, MOE_WS_GEMM_BWD, MOE_WS_GEMM_BWD_ROWSCALED, MOE_WS_GEMM_FWD,
                       MOE_WS_LAYER_BWD, MOE_WS_LAYER_BWD_ROWSCALED, MOE_WS_LAYER_FWD,
-                      MOE_WS_PERMUTE)
+                      MOE_WS_NORM_BWD, MOE_WS_PERMUTE)
 from .ops import (E4M3Weights, MX4Weights, MXWeights, MoeError, make_shape, moe_aux_loss, moe_combine_bwd,
                   moe_quantize_rows_mx, moe_quantize_weights_mx, moe_quantize_token_blocks_mx,
                   moe_permute_mx, moe_grouped_gemm_fwd_mx, moe_grouped_gemm_bwd_mx,
@@ -20,7 +20,8 @@ from .ops import (E4M3Weights, MX4Weights, MXWeights, MoeError, make_shape, moe_
                   moe_probe_mfma, moe_quantize_token_blocks_with_rows,
                   moe_quantize_token_blocks_with_rows_mx, moe_quantize_rows_mx4,
                   moe_quantize_weights_mx4, moe_dequantize_weights_mx4, moe_grouped_gemm_fwd_mx4,
-                  moe_grouped_gemm_fwd_ckpt8, moe_grouped_gemm_bwd_ckpt8, moe_few_rows)
+                  moe_grouped_gemm_fwd_ckpt8, moe_grouped_gemm_bwd_ckpt8, moe_few_rows,
+                  moe_add_rms_norm, moe_add_rms_norm_bwd, moe_dequantize_rows)
 
 __all__ = ["MoeError", "make_shape", "moe_route", "moe_permute", "moe_unpermute",
            "moe_grouped_gemm_fwd", "moe_grouped_gemm_bwd", "moe_layer_fwd", "moe_layer_bwd",
@@ -39,4 +40,5 @@ __all__ = ["MoeError", "make_shape", "moe_route", "moe_permute", "moe_unpermute"
            "moe_grouped_gemm_fwd_ckpt8", "moe_grouped_gemm_bwd_ckpt8", "moe_few_rows",
            "MOE_WS_PERMUTE", "MOE_WS_GEMM_FWD", "MOE_WS_GEMM_BWD", "MOE_WS_LAYER_FWD",
            "MOE_WS_LAYER_BWD", "MOE_WS_AUX_LOSS", "MOE_WS_GEMM_BWD_ROWSCALED",
-           "MOE_WS_LAYER_BWD_ROWSCALED", "_native"]
+           "MOE_WS_LAYER_BWD_ROWSCALED", "MOE_WS_NORM_BWD", "moe_add_rms_norm",
+           "moe_add_rms_norm_bwd", "moe_dequantize_rows", "_native"]

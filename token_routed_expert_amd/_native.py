@@ -14,7 +14,7 @@ MOE_OK, MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = r
 MOE_F32, MOE_BF16, MOE_E4M3, MOE_MXFP8, MOE_MXFP4, MOE_MXFP4_A8 = range(6)
 (MOE_WS_PERMUTE, MOE_WS_GEMM_FWD, MOE_WS_GEMM_BWD, MOE_WS_LAYER_FWD,
  MOE_WS_LAYER_BWD, MOE_WS_AUX_LOSS, MOE_WS_GEMM_BWD_ROWSCALED,
- MOE_WS_LAYER_BWD_ROWSCALED) = range(8)
+ MOE_WS_LAYER_BWD_ROWSCALED, MOE_WS_NORM_BWD) = range(9)
 
 
 class moe_shape(C.Structure):
@@ -42,7 +42,8 @@ class moe_layer_io(C.Structure):
                 + [("aux_alpha", C.c_float), ("row_prob", C.c_void_p),
                    ("memory_efficient", C.c_int32), ("wmx", C.c_void_p),
                    ("fused_permute", C.c_int32), ("wmx4", C.c_void_p),
-                   ("ab_q", C.c_void_p), ("ab_s", C.c_void_p)])
+                   ("ab_q", C.c_void_p), ("ab_s", C.c_void_p),
+                   ("x_quantized", C.c_int32)])
 
 
 IO_FIELDS = tuple(_IO_FIELDS + _IO_FIELDS_E4M3[1:] + _IO_FIELDS_ROUTER
@@ -110,6 +111,10 @@ _PROTOS = {
     "moe_dequantize_weights_mx4": (C.c_int, [_P, _P, _I64, _I64, _I64, _P, _P, _P]),
     "moe_grouped_gemm_fwd_mx4": (C.c_int, [_SH, _P, _P, _P, _P, C.POINTER(moe_mx4_weights), _P, _P,
                                            C.c_size_t, _P]),
+    "moe_add_rms_norm": (C.c_int, [_P, _P, _P, C.c_int32, _I64, _I64, C.c_float, _P, _P, _P, C.c_int32, _P, _P,
+                                   _P]),
+    "moe_add_rms_norm_bwd": (C.c_int, [_P, _P, _P, _P, _P, C.c_int32, _I64, _I64, _P, _P, _P, C.c_size_t, _P]),
+    "moe_dequantize_rows": (C.c_int, [_P, _P, C.c_int32, _I64, _I64, _P, C.c_int32, _P]),
     "moe_aux_loss": (C.c_int, [_P, _I64, _I64, _I64, _P, C.c_float, _P, _P, C.c_size_t, _P]),
     "moe_route_aux": (C.c_int, [_P, _I64, _I64, _I64, _P, _P, _P, C.c_size_t, _P]),
     "moe_aux_loss_final": (C.c_int, [_P, _I64, _I64, _I64, _P, C.c_float, _P, _P]),

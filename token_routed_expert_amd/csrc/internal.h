@@ -189,6 +189,34 @@ struct Mx4Args {
 int gemm_mx4_launch(int fc, bool a8, const Mx4Args& a, hipStream_t s);
 bool gemm_mx4_few_rows(const Mx4Args& a);  // which of its two kernels (E, d, f and P decide)
 
+// norm.hip: s = x + residual, y = s rstd gamma, quantised rows of y; its gradients;
+// and quantised rows back to values.  Every pointer but x, gamma (sum, dy, rstd,
+// gamma, dx, part) may be NULL.
+struct NormArgs {
+  const void *x, *residual, *gamma;
+  int64_t T;
+  int d;
+  float eps;
+  void *sum, *y;
+  float* rstd;
+  int q_dtype;  // of the rows in codes
+  uint8_t* codes;
+  void* scales;
+};
+int norm_launch(const NormArgs& a, bool f32, hipStream_t s);
+struct NormBwdArgs {
+  const void *dy, *sum, *gamma, *dsum;
+  const float* rstd;
+  int64_t T, teams;
+  int d;
+  void* dx;
+  float* part;  // [teams][d]
+};
+int64_t norm_bwd_teams(int64_t T, int64_t d);
+int norm_bwd_launch(const NormBwdArgs& a, bool f32, void* dgamma, hipStream_t s);
+int dequant_rows_launch(const uint8_t* codes, const void* scales, int q_dtype, int64_t rows, int64_t cols, void* dst,
+                        bool f32, hipStream_t s);
+
 // permute.hip: rows of e4m3 codes [T][d] and their scales [T][d/128]
 int permute_e4m3_launch(const uint8_t* codes, const float* scales, const int32_t* row_of, int T,
                         int k, int d, uint8_t* dst_codes, float* dst_scales, hipStream_t s);

@@ -461,6 +461,7 @@ int moe_few_rows(const moe_shape* sh) {
 
 size_t moe_workspace_bytes(const moe_shape* sh, int kind) {
   if (check_shape(sh) != MOE_OK) return 0;
+  if (kind == MOE_WS_NORM_BWD) return (size_t)(norm_bwd_teams(sh->T, sh->d) * sh->d) * 4;
   if (is_fp8(sh)) {
     switch (kind) {
       case MOE_WS_AUX_LOSS: return aux_ws_bytes(sh->T, sh->E);
@@ -1084,6 +1085,66 @@ int moe_grouped_gemm_fwd_mx4(const moe_shape* sh, const int32_t* offsets, const 
   return gemm_mx4_launch(2, a8, a, (hipStream_t)stream);
 }
 
+namespace {
+constexpr int64_t kNormMaxD = 32768;  // a row lies in the registers of 16 wavefronts
+// Rows [rows][d] of quantised values: whole blocks
+int check_q_rows(int32_t q_dtype, int64_t d) {
+  if (q_dtype != MOE_E4M3 && q_dtype != MOE_MXFP8 && q_dtype != MOE_MXFP4) return MOE_ERR_UNSUPPORTED;
+  return d % (q_dtype == MOE_E4M3 ? 128 : 32) == 0 ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+int check_norm_rows(int32_t dtype, int64_t T, int64_t d) {
+  if (T < 0 || d < 1) return MOE_ERR_INVALID;
+  if (dtype != MOE_BF16 && dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  if (d % 8 != 0 || d > kNormMaxD || T >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+}  // namespace
+
+int moe_add_rms_norm(const void* x, const void* residual, const void* gamma, int32_t dtype, int64_t T, int64_t d,
+                     float eps, void* sum, void* y, float* rstd, int32_t q_dtype, uint8_t* codes, void* scales,
+                     void* stream) {
+  if (!x || !gamma || (!codes != !scales)) return MOE_ERR_INVALID;
+  if (!sum && !y && !rstd && !codes) return MOE_ERR_INVALID;
+  if (!(eps >= 0.0f && eps <= 3.4e38f)) return MOE_ERR_INVALID;
+  int st = check_norm_rows(dtype, T, d);
+  if (st) return st;
+  if (codes && (st = check_q_rows(q_dtype, d))) return st;
+  if (!aligned(16, (const char*)x, (const char*)residual, (const char*)gamma, (const char*)sum, (const char*)y,
+               codes) ||
+      !aligned(4, (const char*)rstd, q_dtype == MOE_E4M3 ? (const char*)scales : nullptr))
+    return MOE_ERR_UNSUPPORTED;
+  const NormArgs a = {x, residual, gamma, T, (int)d, eps, sum, y, rstd, q_dtype, codes, scales};
+  return norm_launch(a, dtype == MOE_F32, (hipStream_t)stream);
+}
+
+int moe_add_rms_norm_bwd(const void* dy, const void* sum, const float* rstd, const void* gamma, const void* dsum,
+                         int32_t dtype, int64_t T, int64_t d, void* dx, void* dgamma, void* ws, size_t ws_bytes,
+                         void* stream) {
+  if (!dy || !sum || !rstd || !gamma || !dx || !dgamma) return MOE_ERR_INVALID;
+  int st = check_norm_rows(dtype, T, d);
+  if (st) return st;
+  if (!aligned(16, (const char*)dy, (const char*)sum, (const char*)gamma, (const char*)dsum, (const char*)dx,
+               (const char*)ws) ||
+      !aligned(4, (const char*)rstd, (const char*)dgamma))
+    return MOE_ERR_UNSUPPORTED;
+  NormBwdArgs a = {dy, sum, gamma, dsum, rstd, T, norm_bwd_teams(T, d), (int)d, dx, (float*)ws};
+  if (a.teams > 0 && (!ws || ws_bytes < (size_t)(a.teams * d) * 4)) return MOE_ERR_WORKSPACE;
+  return norm_bwd_launch(a, dtype == MOE_F32, dgamma, (hipStream_t)stream);
+}
+
+int moe_dequantize_rows(const uint8_t* codes, const void* scales, int32_t q_dtype, int64_t rows, int64_t cols,
+                        void* dst, int32_t dst_dtype, void* stream) {
+  if (!codes || !scales || !dst || rows < 0 || cols < 0) return MOE_ERR_INVALID;
+  if (dst_dtype != MOE_BF16 && dst_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  int st = check_q_rows(q_dtype, cols);
+  if (st) return st;
+  if (rows >= ((int64_t)1 << 40) || cols >= (1 << 30) || (cols > 0 && rows > ((int64_t)1 << 36) / (cols / 32)))
+    return MOE_ERR_UNSUPPORTED;
+  if (!aligned(16, codes, (const char*)dst) || (q_dtype == MOE_E4M3 && !aligned(4, (const char*)scales)))
+    return MOE_ERR_UNSUPPORTED;
+  return dequant_rows_launch(codes, scales, q_dtype, rows, cols, dst, dst_dtype == MOE_F32, (hipStream_t)stream);
+}
+
 int moe_layer_fwd(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t ws_bytes,
                   void* stream) {
   int st = check_shape(sh);
@@ -1188,7 +1249,7 @@ int layer_fwd_mx4(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t 
   int st;
   if ((st = check_mx4_dims(sh))) return st;
   if (!io || !weights_ok(io->wmx4)) return MOE_ERR_INVALID;
-  if (!io->logits || !io->x || !io->topk_idx || !io->topk_prob || !io->counts || !io->offsets ||
+  if (!io->logits || (!io->x && !io->x_quantized) || !io->topk_idx || !io->topk_prob || !io->counts || !io->offsets ||
       !io->row_of || !io->token_of || !io->xq || !io->xs || !io->o || !io->y)
     return MOE_ERR_INVALID;
   if (io->memory_efficient) return MOE_ERR_UNSUPPORTED;
@@ -1205,7 +1266,8 @@ int layer_fwd_mx4(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t 
     return st;
   if ((st = layer_aux_loss(sh, io, ws, ws_bytes, stream))) return st;
   uint8_t* xs = (uint8_t*)io->xs;
-  if ((st = (sh->dtype == MOE_MXFP4
+  if (!io->x_quantized &&
+      (st = (sh->dtype == MOE_MXFP4
                  ? moe_quantize_rows_mx4(io->x, MOE_BF16, sh->T, sh->d, io->xq, xs, stream)
                  : moe_quantize_rows_mx(io->x, MOE_BF16, sh->T, sh->d, io->xq, xs, stream))))
     return st;
@@ -1223,7 +1285,7 @@ int layer_fwd_e4m3(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t
   if ((st = check_gemm_dims(sh, sh->T * sh->k, sh->f))) return st;
   if (!io || !(mx ? weights_ok(io->wmx) : weights_ok(io->wq))) return MOE_ERR_INVALID;
   if (io->memory_efficient == 3) return MOE_ERR_UNSUPPORTED;  // the 8-bit checkpoint is bf16
-  if (!io->logits || !io->x || !io->topk_idx || !io->topk_prob ||
+  if (!io->logits || (!io->x && !io->x_quantized) || !io->topk_idx || !io->topk_prob ||
       !io->counts || !io->offsets || !io->row_of || !io->token_of || !io->xq || !io->xs ||
       !io->xpq || !io->xps || !io->ab || !io->h || !io->o || !io->y)
     return MOE_ERR_INVALID;
@@ -1233,7 +1295,8 @@ int layer_fwd_e4m3(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t
   const size_t gws = fwd8_ws_bytes(sh);
   if (!ws || ws_bytes < pws + gws || !aux_ws_ok(sh, io, ws_bytes)) return MOE_ERR_WORKSPACE;
   if ((st = layer_route(sh, io, ws, ws_bytes, stream))) return st;
-  if ((st = (mx ? moe_quantize_rows_mx(io->x, MOE_BF16, sh->T, sh->d, io->xq,
+  if (!io->x_quantized &&
+      (st = (mx ? moe_quantize_rows_mx(io->x, MOE_BF16, sh->T, sh->d, io->xq,
                                        (uint8_t*)io->xs, stream)
                  : moe_quantize_rows(io->x, MOE_BF16, sh->T, sh->d, io->xq, io->xs, stream))))
     return st;

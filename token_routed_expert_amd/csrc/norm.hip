@@ -1,0 +1,432 @@
+// The root-mean-square norm in front of a layer, with the residual's addition and
+// the rows that the layer's products read quantised on the way, and its gradients.
+//
+//   s = x + residual (rounded to the storage type: the norm is that of the s that
+//   is stored, which the backward reads again)
+//   rstd = 1 / sqrt(mean s^2 + eps), y = s rstd gamma
+//
+// The quantised rows come from the fp32 y, not from the stored one: one rounding
+// each.  Block rules as in quant.hip (E4M3, 128 values) and mx4.h (32 values).
+//
+// Bound by memory: a row is read once, held in registers as fp32, and everything
+// that is asked for of it leaves in one pass.
+#include <type_traits>
+
+#include "common.h"
+#include "e4m3.h"
+#include "internal.h"
+#include "mx4.h"
+
+namespace tre {
+
+namespace {
+
+// Eight consecutive values in storage form.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<bf16_t> {
+  u32x4_t w;
+  __device__ __forceinline__ void load(const bf16_t* p) { w = *(const u32x4_t*)p; }
+  __device__ __forceinline__ void zero() { w = u32x4_t{0, 0, 0, 0}; }
+  __device__ __forceinline__ float at(int i) const {
+    return __uint_as_float((i & 1) ? (w[i >> 1] & 0xffff0000u) : (w[i >> 1] << 16));
+  }
+};
+template <>
+struct Raw<float> {
+  f32x4_t a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *(const f32x4_t*)p;
+    b = *(const f32x4_t*)(p + 4);
+  }
+  __device__ __forceinline__ void zero() { a = b = f32x4_t{0.f, 0.f, 0.f, 0.f}; }
+  __device__ __forceinline__ float at(int i) const { return i < 4 ? a[i & 3] : b[i & 3]; }
+};
+__device__ __forceinline__ void store8(bf16_t* p, const float* v) {
+  *(u32x4_t*)p = u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                         pack_bf16x2(v[6], v[7])};
+}
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  *(f32x4_t*)p = f32x4_t{v[0], v[1], v[2], v[3]};
+  *(f32x4_t*)(p + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+}
+__device__ __forceinline__ float rounded(float v, bf16_t) { return bf16_to_f32(f32_to_bf16(v)); }
+__device__ __forceinline__ float rounded(float v, float) { return v; }
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+// Largest v over 4 or 16 consecutive lanes, in each of them.
+template <int N>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  v = max(v, dpp<0xB1>(v));   // lane ^ 1
+  v = max(v, dpp<0x4E>(v));   // lane ^ 2
+  if constexpr (N == 16) {
+    v = max(v, dpp<0x141>(v));  // the other four of eight
+    v = max(v, dpp<0x140>(v));  // the other eight of sixteen
+  }
+  return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// Sum over the WPR wavefronts of a row, in wavefront order; `red` holds WPR
+// floats and is not written again before every wavefront has read it.
+template <int WPR>
+__device__ __forceinline__ float row_sum(float v, int w, float* red) {
+  v = wave_sum(v);
+  if constexpr (WPR > 1) {
+    if ((threadIdx.x & 63) == 0) red[w] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int i = 1; i < WPR; ++i) v += red[i];
+  }
+  return v;
+}
+
+// Quantised form of a lane's eight values (vector `at` of the row matrix in
+// eights); the lanes of a block are neighbours.  Every lane of the wavefront
+// calls it; `ok`: the values exist.
+template <int Q>
+__device__ __forceinline__ void quant8(const float* v, bool ok, size_t at, uint8_t* codes, void* scales) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, mx::mag(v[i]));
+  if constexpr (Q == MOE_E4M3) {
+    m = lanes_max<16>(m);
+    const bool finite = m < 0x7f800000u;
+    const float sc = e4m3::block_scale(finite ? __uint_as_float(m) : 0.0f);
+    uint32_t lo = 0, hi = 0;
+    auto pack = [&](auto fast) __attribute__((always_inline)) {
+      constexpr bool F = decltype(fast)::value;
+      const float inv = F ? 1.0f / sc : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lo |= e4m3::quant1s<F>(v[i], sc, inv, m == 0) << (8 * i);
+        hi |= e4m3::quant1s<F>(v[4 + i], sc, inv, m == 0) << (8 * i);
+      }
+    };
+    if (__all(sc >= e4m3::kFastDivMin)) pack(std::true_type{});
+    else pack(std::false_type{});
+    if (!ok) return;
+    *(uint2*)(codes + at * 8) = make_uint2(lo, hi);
+    // a block with a NaN or an infinity reads back as NaN
+    if ((at & 15) == 0) ((float*)scales)[at >> 4] = finite ? sc : __uint_as_float(0x7fc00000u);
+  } else {
+    constexpr bool F4 = Q == MOE_MXFP4;
+    m = lanes_max<4>(m);
+    const uint32_t b = mx::scale_byte<F4>(m);
+    if constexpr (F4) {
+      if (!ok) return;
+      *(uint32_t*)(codes + at * 4) = mx::pack8_fp4(v, b);
+    } else {
+      const float inv = mx::inv_scale_of(b == mx::kNanScale ? 127u : b);
+      if (!ok) return;
+      // (an all-zero block has +0 codes, whatever its signs)
+      *(uint2*)(codes + at * 8) = m == 0 ? make_uint2(0, 0) : make_uint2(mx::pack4_fp8(v, inv), mx::pack4_fp8(v + 4, inv));
+    }
+    if ((at & 3) == 0) ((uint8_t*)scales)[at >> 2] = (uint8_t)b;
+  }
+}
+
+// WPR wavefronts take one row (WPR == 1: a block has four rows), vector i of
+// lane l of wavefront w being number (i WPR + w) 64 + l of the row's d / 8.
+// x, residual, sum and y may be the same memory: a lane reads all its values of a
+// row before it writes any.
+template <typename T, int Q, int WPR, int NV>
+__global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_kernel(NormArgs a) {
+  __shared__ float red[WPR];
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+  const int w = WPR == 1 ? 0 : wid;
+  const int64_t row = WPR == 1 ? (int64_t)blockIdx.x * 4 + wid : blockIdx.x;
+  if (WPR == 1 && row >= a.T) return;
+  const int nvec = a.d >> 3;
+  const size_t base = (size_t)row * (size_t)nvec;  // in vectors
+  const T* x = (const T*)a.x + base * 8;
+  const T* res = a.residual ? (const T*)a.residual + base * 8 : nullptr;
+  Raw<T> xr[NV], rr[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int at = (i * WPR + w) * 64 + lane;
+    if (at < nvec) xr[i].load(x + (size_t)at * 8);
+    else xr[i].zero();
+  }
+  if (res) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int at = (i * WPR + w) * 64 + lane;
+      if (at < nvec) rr[i].load(res + (size_t)at * 8);
+      else rr[i].zero();
+    }
+  }
+  float v[NV][8], ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      v[i][q] = res ? rounded(xr[i].at(q) + rr[i].at(q), T{}) : xr[i].at(q);
+      ss = fmaf(v[i][q], v[i][q], ss);
+    }
+  }
+  ss = row_sum<WPR>(ss, w, red);
+  const float rstd = 1.0f / sqrtf(ss / (float)a.d + a.eps);
+  if (a.rstd && w == 0 && lane == 0) a.rstd[row] = rstd;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if ((i * WPR) * 64 >= nvec) break;
+    const int at = (i * WPR + w) * 64 + lane;
+    const bool ok = at < nvec;
+    Raw<T> g;
+    if (ok) g.load((const T*)a.gamma + (size_t)at * 8);
+    else g.zero();
+    if (ok && a.sum) store8((T*)a.sum + (base + at) * 8, v[i]);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[i][q] = v[i][q] * rstd * g.at(q);
+    if (ok && a.y) store8((T*)a.y + (base + at) * 8, v[i]);
+    if constexpr (Q >= 0) quant8<Q>(v[i], ok, base + at, a.codes, a.scales);
+  }
+}
+
+// The backward: with g = dy gamma and c = rstd / d sum(g s),
+//   dx = dsum + rstd (g - s rstd c),  dgamma = sum over rows of dy s rstd.
+// Teams of WPR wavefronts walk the rows with a stride of the number of teams and
+// keep their part of dgamma in registers; the parts, [teams][d] fp32, are summed
+// in order by a second kernel.  PRE: the next row is on its way while the current
+// one is worked on.  dx may be dy or dsum.
+template <typename T, int WPR, int NV, bool PRE>
+__global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_bwd_kernel(NormBwdArgs a) {
+  __shared__ float red[2][WPR];
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
+  const int w = WPR == 1 ? 0 : wid;
+  const int64_t team = WPR == 1 ? (int64_t)blockIdx.x * 4 + wid : blockIdx.x;
+  if (team >= a.teams) return;
+  const int nvec = a.d >> 3;
+  int at[NV];
+  bool ok[NV];
+  Raw<T> gm[NV];
+  float acc[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    at[i] = (i * WPR + w) * 64 + lane;
+    ok[i] = at[i] < nvec;
+    if (ok[i]) gm[i].load((const T*)a.gamma + (size_t)at[i] * 8);
+    else gm[i].zero();
+#pragma unroll
+    for (int q = 0; q < 8; ++q) acc[i][q] = 0.0f;
+  }
+  struct Row {
+    Raw<T> s[NV], dy[NV], ds[NV];
+    float rstd;
+  };
+  auto fetch = [&](int64_t r, Row& o) __attribute__((always_inline)) {
+    const size_t base = (size_t)r * (size_t)a.d;
+    o.rstd = a.rstd[r];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (ok[i]) {
+        o.s[i].load((const T*)a.sum + base + (size_t)at[i] * 8);
+        o.dy[i].load((const T*)a.dy + base + (size_t)at[i] * 8);
+      } else {
+        o.s[i].zero();
+        o.dy[i].zero();
+      }
+    }
+    if (a.dsum) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (ok[i]) o.ds[i].load((const T*)a.dsum + base + (size_t)at[i] * 8);
+        else o.ds[i].zero();
+      }
+    }
+  };
+  Row cur, nxt;
+  int par = 0;
+  if constexpr (PRE) fetch(team, nxt);
+  for (int64_t r = team; r < a.T; r += a.teams, par ^= 1) {
+    if constexpr (PRE) {
+      cur = nxt;
+      if (r + a.teams < a.T) fetch(r + a.teams, nxt);
+    } else {
+      fetch(r, cur);
+    }
+    float c = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) c = fmaf(cur.dy[i].at(q) * gm[i].at(q), cur.s[i].at(q), c);
+    c = row_sum<WPR>(c, w, red[par]);
+    c = c * cur.rstd / (float)a.d;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float o[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float dy = cur.dy[i].at(q), xhat = cur.s[i].at(q) * cur.rstd;
+        o[q] = cur.rstd * (dy * gm[i].at(q) - xhat * c);
+        if (a.dsum) o[q] += cur.ds[i].at(q);
+        acc[i][q] = fmaf(dy, xhat, acc[i][q]);
+      }
+      if (ok[i]) store8((T*)a.dx + (size_t)r * (size_t)a.d + (size_t)at[i] * 8, o);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (ok[i]) store8(a.part + (size_t)team * (size_t)a.d + (size_t)at[i] * 8, acc[i]);
+}
+
+// dgamma from the teams' parts: a block has 64 columns, its 16 wavefronts take
+// the parts in turn and meet in LDS, in wavefront order.
+template <typename T>
+__global__ __launch_bounds__(1024) void norm_dgamma_kernel(const float* __restrict__ part, int teams, int d,
+                                                           T* __restrict__ dgamma) {
+  __shared__ float red[16][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int col = blockIdx.x * 64 + lane;
+  float v = 0.0f;
+  if (col < d) {
+#pragma unroll 8
+    for (int t = w; t < teams; t += 16) v += part[(size_t)t * d + col];
+  }
+  red[w][lane] = v;
+  __syncthreads();
+  if (w != 0 || col >= d) return;
+  v = red[0][lane];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) v += red[i][lane];
+  Elem<T>::store(dgamma + col, v);
+}
+
+// The values that rows of codes stand for: a thread takes eight.
+template <int Q, typename T>
+__global__ __launch_bounds__(256) void dequant_rows_kernel(const uint8_t* __restrict__ codes,
+                                                           const void* __restrict__ scales, int64_t nvec,
+                                                           T* __restrict__ dst) {
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (at >= nvec) return;
+  float v[8];
+  if constexpr (Q == MOE_MXFP4) {
+    const float s = mx::scale_any(((const uint8_t*)scales)[at >> 2]);
+    const uint32_t c = *(const uint32_t*)(codes + at * 4);
+    const f32x2_t p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0),
+                          __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1),
+                          __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2),
+                          __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3)};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = p[i >> 1][i & 1] * s;
+  } else {
+    const float s = Q == MOE_E4M3 ? ((const float*)scales)[at >> 4] : mx::scale_any(((const uint8_t*)scales)[at >> 2]);
+    const uint2 c = *(const uint2*)(codes + at * 8);
+    const f32x2_t p[4] = {__builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, false), __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, true),
+                          __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, false), __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, true)};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = p[i >> 1][i & 1] * s;
+  }
+  store8(dst + at * 8, v);
+}
+
+template <typename T, int Q, int WPR, int NV>
+int fwd_as(const NormArgs& a, hipStream_t s) {
+  const int64_t grid = WPR == 1 ? (a.T + 3) / 4 : a.T;
+  if (!launch_fits(grid, WPR == 1 ? 256 : 64 * WPR)) return MOE_ERR_UNSUPPORTED;
+  norm_kernel<T, Q, WPR, NV><<<(unsigned)grid, WPR == 1 ? 256 : 64 * WPR, 0, s>>>(a);
+  TRE_LAUNCH_CHECK();
+  return MOE_OK;
+}
+template <typename T, int Q>
+int fwd_of(const NormArgs& a, hipStream_t s) {
+  const int nvec = a.d / 8;
+  if (a.T >= 4096 && nvec <= 1024) {
+    if (nvec <= 128) return fwd_as<T, Q, 1, 2>(a, s);
+    if (nvec <= 512) return fwd_as<T, Q, 1, 8>(a, s);
+    return fwd_as<T, Q, 1, 16>(a, s);
+  }
+  if (nvec <= 256) return fwd_as<T, Q, 4, 1>(a, s);
+  if (nvec <= 1024) return fwd_as<T, Q, 4, 4>(a, s);
+  return fwd_as<T, Q, 16, 4>(a, s);
+}
+template <typename T>
+int fwd_type(const NormArgs& a, hipStream_t s) {
+  if (!a.codes) return fwd_of<T, -1>(a, s);
+  if (a.q_dtype == MOE_E4M3) return fwd_of<T, MOE_E4M3>(a, s);
+  if (a.q_dtype == MOE_MXFP8) return fwd_of<T, MOE_MXFP8>(a, s);
+  return fwd_of<T, MOE_MXFP4>(a, s);
+}
+
+template <typename T, int WPR, int NV>
+int bwd_as(const NormBwdArgs& a, hipStream_t s) {
+  const int64_t grid = WPR == 1 ? (a.teams + 3) / 4 : a.teams;
+  norm_bwd_kernel<T, WPR, NV, (sizeof(T) * NV <= 8)><<<(unsigned)grid, WPR == 1 ? 256 : 64 * WPR, 0, s>>>(a);
+  TRE_LAUNCH_CHECK();
+  return MOE_OK;
+}
+template <typename T>
+int bwd_of(const NormBwdArgs& a, void* dgamma, hipStream_t s) {
+  const int nvec = a.d / 8;
+  int st = MOE_OK;
+  if (a.T > 0) {
+    if (nvec <= 128) st = bwd_as<T, 1, 2>(a, s);
+    else if (nvec <= 512) st = bwd_as<T, 4, 2>(a, s);
+    else if (nvec <= 1024) st = bwd_as<T, 4, 4>(a, s);
+    else if (nvec <= 2048) st = bwd_as<T, 16, 2>(a, s);
+    else st = bwd_as<T, 16, 4>(a, s);
+  }
+  if (st) return st;
+  norm_dgamma_kernel<T><<<(unsigned)((a.d + 63) / 64), 1024, 0, s>>>(a.part, (int)a.teams, a.d, (T*)dgamma);
+  TRE_LAUNCH_CHECK();
+  return MOE_OK;
+}
+
+template <int Q, typename T>
+int dequant_as(const uint8_t* codes, const void* scales, int64_t rows, int64_t cols, void* dst, hipStream_t s) {
+  const int64_t nvec = rows * (cols / 8);
+  constexpr int64_t kPart = (int64_t)1 << 31;  // vectors a launch
+  for (int64_t at = 0; at < nvec; at += kPart) {
+    const int64_t n = nvec - at < kPart ? nvec - at : kPart;
+    const void* sc = Q == MOE_E4M3 ? (const void*)((const float*)scales + at / 16)
+                                   : (const void*)((const uint8_t*)scales + at / 4);
+    dequant_rows_kernel<Q, T><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(codes + at * (Q == MOE_MXFP4 ? 4 : 8), sc, n,
+                                                                          (T*)dst + at * 8);
+    TRE_LAUNCH_CHECK();
+  }
+  return MOE_OK;
+}
+
+}  // namespace
+
+// Teams of the backward: as many as keep the chip busy, each with as many rows as
+// the others or one fewer.
+int64_t norm_bwd_teams(int64_t T, int64_t d) {
+  if (T < 1) return 0;
+  const int64_t most = d <= 1024 ? 2048 : d <= 8192 ? 512 : 256;
+  const int64_t rows = (T + most - 1) / most;
+  return (T + rows - 1) / rows;
+}
+
+int norm_launch(const NormArgs& a, bool f32, hipStream_t s) {
+  if (a.T == 0) return MOE_OK;
+  return f32 ? fwd_type<float>(a, s) : fwd_type<bf16_t>(a, s);
+}
+
+int norm_bwd_launch(const NormBwdArgs& a, bool f32, void* dgamma, hipStream_t s) {
+  return f32 ? bwd_of<float>(a, dgamma, s) : bwd_of<bf16_t>(a, dgamma, s);
+}
+
+int dequant_rows_launch(const uint8_t* codes, const void* scales, int q_dtype, int64_t rows, int64_t cols, void* dst,
+                        bool f32, hipStream_t s) {
+  if (q_dtype == MOE_E4M3)
+    return f32 ? dequant_as<MOE_E4M3, float>(codes, scales, rows, cols, dst, s)
+               : dequant_as<MOE_E4M3, bf16_t>(codes, scales, rows, cols, dst, s);
+  if (q_dtype == MOE_MXFP8)
+    return f32 ? dequant_as<MOE_MXFP8, float>(codes, scales, rows, cols, dst, s)
+               : dequant_as<MOE_MXFP8, bf16_t>(codes, scales, rows, cols, dst, s);
+  return f32 ? dequant_as<MOE_MXFP4, float>(codes, scales, rows, cols, dst, s)
+             : dequant_as<MOE_MXFP4, bf16_t>(codes, scales, rows, cols, dst, s);
+}
+
+}  // namespace tre

@@ -443,6 +443,7 @@ def _io(buffers: dict) -> N.moe_layer_io:
     io.aux_alpha = float(buffers.get("aux_alpha", 0.0))
     io.memory_efficient = int(buffers.get("memory_efficient", 0))
     io.fused_permute = int(buffers.get("fused_permute", 0))
+    io.x_quantized = int(buffers.get("x_quantized", 0))
     return io
 
 
@@ -506,6 +507,54 @@ def moe_grouped_gemm_bwd_ckpt8(sh, offsets, token_of, x, abq, abs_, dO, W1, W3, 
         b("dW1", dW1, BF16, mat), b("dW3", dW3, BF16, mat), b("dW2", dW2, BF16, mat),
         b.opt("row_of", row_of, I32, P, 4), b.opt("dprob", dprob, F32, P, 4),
         None if ws is None else b("ws", ws, ws.dtype, 0), _nbytes(ws), b.stream(stream)), call)
+
+
+_ROWS = {"e4m3": N.MOE_E4M3, "mxfp8": N.MOE_MXFP8, "mxfp4": N.MOE_MXFP4}
+
+
+def _q_rows(b, call, q_dtype, n, codes, scales):
+    """(type code, codes, scales) of n quantised values in rows."""
+    if q_dtype not in _ROWS:
+        raise ValueError(f"{call}: rows are 'e4m3', 'mxfp8' or 'mxfp4', not {q_dtype!r}")
+    sc = b("scales", scales, F32, n // 128, 4) if q_dtype == "e4m3" else b("scales", scales, U8, n // 32, 1)
+    return _ROWS[q_dtype], b("codes", codes, U8, n // 2 if q_dtype == "mxfp4" else n), sc
+
+
+def moe_add_rms_norm(x, residual, gamma, eps, sum_, y, rstd, q_dtype=None, codes=None, scales=None, stream=None):
+    """s = x + residual (x [T][d] bf16 or fp32; residual or None), the root-mean-square norm y = s rstd gamma
+    and, q_dtype "e4m3", "mxfp8" or "mxfp4", its quantised rows; any of sum_, y, rstd may be None."""
+    call = "moe_add_rms_norm"
+    T, d = x.shape
+    code, b, n, dt = _src_dtype(call, x), _Bufs(call), T * d, x.dtype
+    if q_dtype is None and (codes is not None or scales is not None):
+        raise ValueError(f"{call}: codes and scales need q_dtype")
+    q, c, sc = (0, None, None) if q_dtype is None else _q_rows(b, call, q_dtype, n, codes, scales)
+    _check(N.lib().moe_add_rms_norm(
+        b("x", x, dt, n), b.opt("residual", residual, dt, n), b("gamma", gamma, dt, d), code, T, d, float(eps),
+        b.opt("sum", sum_, dt, n), b.opt("y", y, dt, n), b.opt("rstd", rstd, F32, T, 4), q, c, sc,
+        b.stream(stream)), call)
+
+
+def moe_add_rms_norm_bwd(dy, sum_, rstd, gamma, dsum, dx, dgamma, ws, stream=None):
+    """Gradients of moe_add_rms_norm: dx [T][d] (of x and of the residual) and dgamma [d] from dy, the
+    forward's sum and rstd, and (or None) the gradient dsum of the sum."""
+    call = "moe_add_rms_norm_bwd"
+    T, d = dy.shape
+    code, b, n, dt = _src_dtype(call, dy), _Bufs(call), T * d, dy.dtype
+    _check(N.lib().moe_add_rms_norm_bwd(
+        b("dy", dy, dt, n), b("sum", sum_, dt, n), b("rstd", rstd, F32, T, 4), b("gamma", gamma, dt, d),
+        b.opt("dsum", dsum, dt, n), code, T, d, b("dx", dx, dt, n), b("dgamma", dgamma, dt, d),
+        None if ws is None else b("ws", ws, ws.dtype, 0), _nbytes(ws), b.stream(stream)), call)
+
+
+def moe_dequantize_rows(codes, scales, q_dtype, dst, stream=None):
+    """The values (dst [rows][cols] bf16 or fp32) that quantised rows stand for."""
+    call = "moe_dequantize_rows"
+    rows, cols = dst.shape
+    code, b = _src_dtype(call, dst), _Bufs(call)
+    q, c, sc = _q_rows(b, call, q_dtype, rows * cols, codes, scales)
+    _check(N.lib().moe_dequantize_rows(c, sc, q, rows, cols, b("dst", dst, dst.dtype, rows * cols), code,
+                                       b.stream(stream)), call)
 
 
 def moe_aux_loss(logits, k, counts, alpha, loss, ws, stream=None):
