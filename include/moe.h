@@ -46,7 +46,8 @@
  *    MOE_MXFP8 (the same with MXFP8 operands: E4M3FN codes with one
  *    power-of-two E8M0 scale byte per 32 values -- see "MXFP8 expert GEMMs"
  *    below).  MOE_MXFP4 and MOE_MXFP4_A8 run the forward alone, with 4-bit
- *    expert weights ("MXFP4 experts" below) and bf16 x and y.  Router
+ *    expert weights ("MXFP4 experts" below) and bf16 x and y; MOE_INT4 does with
+ *    integer ones ("Integer expert weights" below).  Router
  *    logits and probabilities are always fp32 (German summary, section 2 E:
  *    the router stays in high precision).
  */
@@ -75,7 +76,8 @@ typedef enum {
   MOE_E4M3 = 2,
   MOE_MXFP8 = 3,
   MOE_MXFP4 = 4,    /* forward only: MXFP4 weights and activations */
-  MOE_MXFP4_A8 = 5  /* forward only: MXFP4 weights, MXFP8 activations */
+  MOE_MXFP4_A8 = 5, /* forward only: MXFP4 weights, MXFP8 activations */
+  MOE_INT4 = 6      /* forward only: integer weights in scaled groups, bf16 activations */
 } moe_dtype;
 
 typedef struct {
@@ -307,6 +309,10 @@ typedef struct {
      in place of quantising x (x itself is read by the backward alone and may be
      NULL in the forward); other layers ignore it */
   int32_t x_quantized;
+  /* integer-weight layers (sh->dtype == MOE_INT4; moe_layer_fwd only): the packed
+     weights.  xp, ab, h, xq and xs are not used; a shared expert has bf16 weights
+     and its buffers s_ab, s_h, ys */
+  const struct moe_i4_weights* wi4;
 } moe_layer_io;
 
 /*
@@ -318,7 +324,9 @@ typedef struct {
  * moe_grouped_gemm_fwd_e4m3, moe_unpermute (MOE_MXFP8: the _mx calls, weights
  * io->wmx).  For MOE_MXFP4 / MOE_MXFP4_A8: moe_route, the permutation's map,
  * moe_quantize_rows_mx4 / _mx of x, moe_grouped_gemm_fwd_mx4 reading x through
- * token_of, moe_unpermute (io->memory_efficient must be 0).  With io->aux_loss
+ * token_of, moe_unpermute (io->memory_efficient must be 0).  For MOE_INT4:
+ * moe_route, the map, moe_grouped_gemm_fwd_i4 reading x through token_of (and the
+ * bf16 shared expert), moe_unpermute (no memory_efficient either).  With io->aux_loss
  * set, the routing is moe_route_aux and moe_aux_loss_final (alpha =
  * io->aux_alpha) follows the permutation; ws_bytes then needs MOE_WS_AUX_LOSS
  * more bytes.  With io->memory_efficient:
@@ -783,6 +791,82 @@ int moe_dequantize_weights_mx4(const uint8_t* codes, const uint8_t* scales, int6
 int moe_grouped_gemm_fwd_mx4(const moe_shape* sh, const int32_t* offsets, const int32_t* token_of,
                              const uint8_t* xq, const uint8_t* xs, const moe_mx4_weights* w,
                              void* o, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Integer expert weights
+ * ----------------------
+ * The 4-bit checkpoints that are common beside FP4: codes q in 0 .. 15, with a
+ * scale s and a zero point z for each group of 32, 64 or 128 consecutive rows
+ * (the contraction) of a column.  The weight that a code stands for is
+ * bf16(s (q - z)): the difference's product is exact in fp32 and rounded once, so
+ * products on the codes use the numbers that moe_dequantize_weights_i4 writes,
+ * and its bf16 weights serve a backward (as for MXFP4 there are no weight
+ * gradients in this format).  Activations are bf16.
+ *
+ * Layout.  As for MXFP4 a matrix of R rows and N columns is stored in tiles of
+ * 128 rows x 16 columns, 1 KB each:
+ *   codes  [E][N/16][R/128][4][16][16]: byte 4 j + b of (group g, column c) of
+ *          tile (nt, kt) holds rows 128 kt + 32 j + 8 g + b (low nibble) and + 4
+ *          (high nibble) of column 16 nt + c;
+ *   scales [E][N/64][R/128][128/group][16][4] 32-bit words: word i of (u, c) of
+ *          (nb, kt) is the scale of rows 128 kt + group u .. of column 64 nb +
+ *          16 i + c: the fp32 number s, whose low four bits hold z (s has 20
+ *          significant bits: fp16 and bf16 scales are kept exactly).
+ * W1 and W3 form one matrix W13 of N = 2f columns whose 16-column groups alternate
+ * (group 2 i: columns 16 i .. of W1, group 2 i + 1: of W3).  d and f must be
+ * multiples of 128.  A layer takes a shared expert with bf16 weights.
+ */
+
+/* Packed expert weights as written by moe_quantize_weights_i4 or
+ * moe_pack_weights_i4. */
+typedef struct moe_i4_weights {
+  const uint8_t *W13, *W2;    /* codes of [E][d][2f] (W1 with W_pair = W3) and [E][f][d] */
+  const uint32_t *W13s, *W2s; /* their scale words */
+  int64_t group;              /* rows of a group: 32, 64 or 128 */
+} moe_i4_weights;
+
+/* moe_quantize_weights_i4 -- E matrices W [E][R][C] (MOE_F32 masters or MOE_BF16;
+ * R, C multiples of 128) into the layout above, N = C; with W_pair (a second
+ * [E][R][C], same type) N = 2C and the 16-column groups of W and W_pair alternate.
+ * For a group's weights w, with s the smallest number of 20 significant bits, at
+ * least 2^-126, that
+ *   asymmetric == 0:  max|w| <= 7 s, z = 8;
+ *   asymmetric != 0:  hi - lo <= 15 s, lo = min(w, 0), hi = max(w, 0), z = the
+ *                     nearest integer to -lo / s;
+ * q = the nearest integer to w / s, plus z, held to 0 .. 15; all ties to even and
+ * of the exact quotients.  A group of zeros has s = 1 and codes equal to z.  A
+ * group with a NaN or an infinity, or whose s would be 2^124 or more, has s = NaN:
+ * its weights and every product they enter are NaN. */
+int moe_quantize_weights_i4(const void* W, const void* W_pair, int32_t src_dtype, int32_t asymmetric, int64_t group,
+                            int64_t E, int64_t R, int64_t C, uint8_t* codes, uint32_t* scales, void* stream);
+
+/* moe_pack_weights_i4 -- the same layout from a checkpoint's codes q uint8
+ * [E][R][C] (one to a byte, the low four bits count), scales s fp32 [E][R/group][C]
+ * (rounded to 20 significant bits; not finite, or 2^124 and more: NaN) and zero points z uint8
+ * [E][R/group][C] (the low four bits count; NULL: 8); q_pair, s_pair, z_pair: a second matrix whose
+ * groups alternate, or NULL. */
+int moe_pack_weights_i4(const uint8_t* q, const float* s, const uint8_t* z, const uint8_t* q_pair, const float* s_pair,
+                        const uint8_t* z_pair, int64_t group, int64_t E, int64_t R, int64_t C, uint8_t* codes,
+                        uint32_t* scales, void* stream);
+
+/* moe_dequantize_weights_i4 -- the weights bf16 [E][R][C] that codes and scales
+ * stand for, W_pair NULL for a single matrix. */
+int moe_dequantize_weights_i4(const uint8_t* codes, const uint32_t* scales, int64_t group, int64_t E, int64_t R,
+                              int64_t C, void* W, void* W_pair, void* stream);
+
+/*
+ * moe_grouped_gemm_fwd_i4 -- the experts' forward on bf16 rows: for expert e and
+ * its rows r in [offsets[e], offsets[e+1])
+ *   [a|b] = x_r W13_e, h = silu(a) b rounded to bf16, o = h W2_e
+ * with fp32 accumulation; o [P][d] is bf16.  Row r is row token_of[r] of x [T][d]
+ * (an entry outside [0, T) reads a row of zeros), or, token_of NULL, row r of the
+ * permuted x [P][d].  Rows of o from offsets[E] on are not written.  ws_bytes >=
+ * moe_workspace_bytes(sh, MOE_WS_GEMM_FWD) (h).  Errors: MOE_ERR_INVALID for
+ * another dtype; MOE_ERR_UNSUPPORTED for d or f not a multiple of 128, another
+ * group than 32, 64 or 128, P * max(d, f) >= 2^30 - 2048 or d * f >= 2^31.
+ */
+int moe_grouped_gemm_fwd_i4(const moe_shape* sh, const int32_t* offsets, const int32_t* token_of, const void* x,
+                            const moe_i4_weights* w, void* o, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * The norm in front of a layer

@@ -24,3 +24,4 @@ from .mx import *  # noqa: F401,F403
 from .mx4 import *  # noqa: F401,F403
 from .ckpt8 import *  # noqa: F401,F403
 from .norm import *  # noqa: F401,F403
+from .i4 import *  # noqa: F401,F403

@@ -11,7 +11,7 @@ import os
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtre_moe.so")
 
 MOE_OK, MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(5)
-MOE_F32, MOE_BF16, MOE_E4M3, MOE_MXFP8, MOE_MXFP4, MOE_MXFP4_A8 = range(6)
+MOE_F32, MOE_BF16, MOE_E4M3, MOE_MXFP8, MOE_MXFP4, MOE_MXFP4_A8, MOE_INT4 = range(7)
 (MOE_WS_PERMUTE, MOE_WS_GEMM_FWD, MOE_WS_GEMM_BWD, MOE_WS_LAYER_FWD,
  MOE_WS_LAYER_BWD, MOE_WS_AUX_LOSS, MOE_WS_GEMM_BWD_ROWSCALED,
  MOE_WS_LAYER_BWD_ROWSCALED, MOE_WS_NORM_BWD) = range(9)
@@ -43,7 +43,7 @@ class moe_layer_io(C.Structure):
                    ("memory_efficient", C.c_int32), ("wmx", C.c_void_p),
                    ("fused_permute", C.c_int32), ("wmx4", C.c_void_p),
                    ("ab_q", C.c_void_p), ("ab_s", C.c_void_p),
-                   ("x_quantized", C.c_int32)])
+                   ("x_quantized", C.c_int32), ("wi4", C.c_void_p)])
 
 
 IO_FIELDS = tuple(_IO_FIELDS + _IO_FIELDS_E4M3[1:] + _IO_FIELDS_ROUTER
@@ -52,6 +52,10 @@ IO_FIELDS = tuple(_IO_FIELDS + _IO_FIELDS_E4M3[1:] + _IO_FIELDS_ROUTER
 
 class moe_mx4_weights(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in ("W13", "W2", "W13s", "W2s")]
+
+
+class moe_i4_weights(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("W13", "W2", "W13s", "W2s")] + [("group", C.c_int64)]
 
 
 class moe_mx_weights(C.Structure):
@@ -111,6 +115,10 @@ _PROTOS = {
     "moe_dequantize_weights_mx4": (C.c_int, [_P, _P, _I64, _I64, _I64, _P, _P, _P]),
     "moe_grouped_gemm_fwd_mx4": (C.c_int, [_SH, _P, _P, _P, _P, C.POINTER(moe_mx4_weights), _P, _P,
                                            C.c_size_t, _P]),
+    "moe_quantize_weights_i4": (C.c_int, [_P, _P, C.c_int32, C.c_int32, _I64, _I64, _I64, _I64, _P, _P, _P]),
+    "moe_pack_weights_i4": (C.c_int, [_P] * 6 + [_I64] * 4 + [_P] * 3),
+    "moe_dequantize_weights_i4": (C.c_int, [_P, _P, _I64, _I64, _I64, _I64, _P, _P, _P]),
+    "moe_grouped_gemm_fwd_i4": (C.c_int, [_SH, _P, _P, _P, C.POINTER(moe_i4_weights), _P, _P, C.c_size_t, _P]),
     "moe_add_rms_norm": (C.c_int, [_P, _P, _P, C.c_int32, _I64, _I64, C.c_float, _P, _P, _P, C.c_int32, _P, _P,
                                    _P]),
     "moe_add_rms_norm_bwd": (C.c_int, [_P, _P, _P, _P, _P, C.c_int32, _I64, _I64, _P, _P, _P, C.c_size_t, _P]),

@@ -4,13 +4,14 @@ from __future__ import annotations
 import torch
 
 from . import _native as N
-from .ops import (E4M3Weights, MX4Weights, MXWeights, make_shape, moe_quantize_weights,
-                  moe_quantize_weights_mx, moe_quantize_weights_mx4, moe_workspace_bytes)
+from .ops import (E4M3Weights, I4Weights, MX4Weights, MXWeights, make_shape, moe_quantize_weights,
+                  moe_quantize_weights_i4, moe_quantize_weights_mx, moe_quantize_weights_mx4,
+                  moe_workspace_bytes)
 
 
 def layer_buffers(T, d, E, k, f, f_shared=0, dtype="bf16", device="cuda", inputs=None,
                   router_grad=False, aux_alpha=0.01, memory_efficient=False,
-                  fused_permute=False):
+                  fused_permute=False, group=128, asymmetric=False):
     """Every buffer moe_layer_fwd/bwd touch, as a dict keyed like moe_layer_io.
 
     `inputs` (logits, x, W1, W3, W2, Ws1, Ws3, Ws2, dY) are used as given.
@@ -20,6 +21,7 @@ def layer_buffers(T, d, E, k, f, f_shared=0, dtype="bf16", device="cuda", inputs
     2 also recomputes h in the backward; 3 (bf16) also keeps [a|b] in 8 bits
     (ab_q, ab_s in place of ab).
     fused_permute: the experts read x through token_of; no xp buffer.
+    group, asymmetric: of the integer weights made for dtype "int4".
     Returns (shape, buffers, ws_fwd, ws_bwd).
     """
     sh = make_shape(T, d, E, k, f, f_shared, dtype)
@@ -57,12 +59,20 @@ def layer_buffers(T, d, E, k, f, f_shared=0, dtype="bf16", device="cuda", inputs
         b.update(xq=z(T, d // 2 if dtype == "mxfp4" else d, dtype=u8), xs=z(T, d // 32, dtype=u8))
         if "W1" in b:
             b["wmx4"] = quantized_weights_mx4(b["W1"], b["W3"], b["W2"])
+    if dtype == "int4":
+        for n in ("xp", "ab", "h", "dO", "dab", "dXp", "dX", "dW1", "dW3", "dW2"):  # forward only
+            b.pop(n)
+        if "W1" in b:
+            b["wi4"] = quantized_weights_i4(b["W1"], b["W3"], b["W2"], group, asymmetric)
     if fused_permute:
         b.pop("xp", None)
         b["fused_permute"] = 1
     if f_shared:
         b.update(s_ab=z(T, 2 * f_shared), s_h=z(T, f_shared), ys=z(T, d), s_dab=z(T, 2 * f_shared),
                  dXs=z(T, d), dWs1=z(d, f_shared), dWs3=z(d, f_shared), dWs2=z(f_shared, d))
+        if dtype == "int4":
+            for n in ("s_dab", "dXs", "dWs1", "dWs3", "dWs2"):
+                b.pop(n)
     ws_f_bytes = moe_workspace_bytes(sh, N.MOE_WS_LAYER_FWD)
     if router_grad:
         b.update(aux_loss=z(1, dtype=torch.float32), dprob=z(T, k, dtype=torch.float32),
@@ -137,3 +147,17 @@ def quantized_weights_mx4(W1, W3, W2, stream=None) -> MX4Weights:
                                     device=W.device)
         moe_quantize_weights_mx4(W, pair, t[name], t[name + "s"], stream)
     return MX4Weights(t)
+
+
+def quantized_weights_i4(W1, W3, W2, group=128, asymmetric=False, stream=None) -> I4Weights:
+    """Integer codes and scale words of bf16 or fp32 expert weights (W1, W3
+    [E][d][f], W2 [E][f][d]), made by moe_quantize_weights_i4."""
+    E, d, f = W1.shape
+    t = {}
+    for name, W, pair, N_ in (("W13", W1, W3, 2 * f), ("W2", W2, None, d)):
+        R = W.shape[1]
+        t[name] = torch.empty(E, N_ // 16, R // 128, 4, 16, 16, dtype=torch.uint8, device=W.device)
+        t[name + "s"] = torch.empty(E, N_ // 64, R // 128, 128 // group, 16, 4, dtype=torch.int32,
+                                    device=W.device)
+        moe_quantize_weights_i4(W, pair, group, asymmetric, t[name], t[name + "s"], stream)
+    return I4Weights(t, group)

@@ -217,6 +217,36 @@ int norm_bwd_launch(const NormBwdArgs& a, bool f32, void* dgamma, hipStream_t s)
 int dequant_rows_launch(const uint8_t* codes, const void* scales, int q_dtype, int64_t rows, int64_t cols, void* dst,
                         bool f32, hipStream_t s);
 
+// quant_i4.hip: integer weights in groups (i4.h): from values, from a checkpoint's
+// codes (q one to a byte [E][R][C], s and z [E][R/group][C], z NULL: 8), and back to
+// bf16; a pair's 16-column groups alternate
+struct I4Source {
+  const uint8_t* q;
+  const float* s;
+  const uint8_t* z;
+};
+int quant_weights_i4_launch(const void* W, const void* Wp, bool src_f32, int64_t E, int64_t R, int64_t C, int group,
+                            bool asym, uint8_t* codes, uint32_t* words, hipStream_t s);
+int pack_weights_i4_launch(const I4Source& a, const I4Source& b, int64_t E, int64_t R, int64_t C, int group,
+                           uint8_t* codes, uint32_t* words, hipStream_t s);
+int dequant_weights_i4_launch(const uint8_t* codes, const uint32_t* words, int64_t E, int64_t R, int64_t C, int group,
+                              void* W, void* Wp, hipStream_t s);
+
+// gemm_i4.hip: one product of the experts' forward with integer weights.  fc 1: a = x
+// (row token_of[r] of it when token_of is set), w/ws = W13, writes h; fc 2: a = h, w/ws
+// = W2, writes o.  All bf16.
+struct I4Args {
+  const int32_t* offsets;
+  const int32_t* token_of;
+  int E, d, f, P, T, group;
+  const uint16_t* a;
+  const uint8_t* w;
+  const uint32_t* ws;
+  uint16_t* h;
+  uint16_t* o;
+};
+int gemm_i4_launch(int fc, const I4Args& a, hipStream_t s);
+
 // permute.hip: rows of e4m3 codes [T][d] and their scales [T][d/128]
 int permute_e4m3_launch(const uint8_t* codes, const float* scales, const int32_t* row_of, int T,
                         int k, int d, uint8_t* dst_codes, float* dst_scales, hipStream_t s);

@@ -27,6 +27,8 @@ int elem_bytes(const moe_shape* sh) { return sh->dtype == MOE_F32 ? 4 : 2; }
 bool is_fp8(const moe_shape* sh) { return sh->dtype == MOE_E4M3 || sh->dtype == MOE_MXFP8; }
 // MXFP4 expert weights (forward only; bf16 x and y)
 bool is_mx4(const moe_shape* sh) { return sh->dtype == MOE_MXFP4 || sh->dtype == MOE_MXFP4_A8; }
+// integer expert weights in groups (forward only; bf16 x and y)
+bool is_i4(const moe_shape* sh) { return sh->dtype == MOE_INT4; }
 
 // Shape checks shared by every call.  Returns MOE_OK or an error code.
 int check_shape(const moe_shape* sh) {
@@ -35,7 +37,7 @@ int check_shape(const moe_shape* sh) {
     return MOE_ERR_INVALID;
   if (sh->k > sh->E || sh->reserved != 0) return MOE_ERR_INVALID;
   if (sh->dtype != MOE_F32 && sh->dtype != MOE_BF16 && sh->dtype != MOE_E4M3 &&
-      sh->dtype != MOE_MXFP8 && !is_mx4(sh))
+      sh->dtype != MOE_MXFP8 && !is_mx4(sh) && !is_i4(sh))
     return MOE_ERR_UNSUPPORTED;
   if ((is_fp8(sh) || is_mx4(sh)) && sh->f_shared != 0) return MOE_ERR_UNSUPPORTED;
   if (sh->E > kMaxE) return MOE_ERR_UNSUPPORTED;
@@ -167,6 +169,24 @@ int check_mx4_dims(const moe_shape* sh) {
   return MOE_OK;
 }
 
+// Integer weights: the workspace holds h; 32-bit byte offsets as for MXFP4, of rows
+// of two bytes a value.
+size_t i4_ws_bytes(const moe_shape* sh) { return align_up((size_t)(sh->T * sh->k * sh->f) * 2, 256); }
+int check_i4_dims(const moe_shape* sh) {
+  if (!is_i4(sh)) return MOE_ERR_INVALID;
+  if (sh->d % 128 != 0 || sh->f % 128 != 0) return MOE_ERR_UNSUPPORTED;
+  const int64_t lim = (int64_t)1 << 31;
+  if (sh->T * sh->k * std::max(sh->d, sh->f) >= (lim - 4096) / 2 || sh->d * sh->f >= lim)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+bool group_ok(int64_t g) { return g == 32 || g == 64 || g == 128; }
+int check_weights(const moe_i4_weights* w) {
+  if (!w || !w->W13 || !w->W2 || !w->W13s || !w->W2s) return MOE_ERR_INVALID;
+  if (!group_ok(w->group) || !aligned(16, w->W13, w->W2, w->W13s, w->W2s)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 // The weight operands of the fp8 products: codes in both orientations and
 // the scales read with each (e4m3: one tile-scale array serves both; MXFP8:
 // row-block bytes with W1/W3/W2, column-block bytes with the transposed codes).
@@ -273,6 +293,8 @@ int bwd_sequence(const moe_shape* sh, GemmArgs a, hipStream_t s) {
 
 int layer_fwd_mx4(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t ws_bytes,
                   void* stream);
+int layer_fwd_i4(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t ws_bytes,
+                 void* stream);
 int layer_fwd_e4m3(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t ws_bytes,
                    void* stream);
 int layer_bwd_e4m3(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t ws_bytes,
@@ -483,6 +505,15 @@ size_t moe_workspace_bytes(const moe_shape* sh, int kind) {
     }
     return 0;
   }
+  if (is_i4(sh)) {
+    switch (kind) {
+      case MOE_WS_AUX_LOSS: return aux_ws_bytes(sh->T, sh->E);
+      case MOE_WS_PERMUTE: return permute_ws_bytes(sh->T, sh->E);
+      case MOE_WS_GEMM_FWD: return i4_ws_bytes(sh);
+      case MOE_WS_LAYER_FWD: return permute_ws_bytes(sh->T, sh->E) + 256 + i4_ws_bytes(sh);
+    }
+    return 0;
+  }
   switch (kind) {
     case MOE_WS_AUX_LOSS: return aux_ws_bytes(sh->T, sh->E);
     case MOE_WS_PERMUTE: return permute_ws_bytes(sh->T, sh->E);
@@ -565,7 +596,7 @@ int moe_grouped_gemm_fwd(const moe_shape* sh, const int32_t* offsets, const void
   int st = check_shape(sh);
   if (st) return st;
   if ((st = check_gemm_dims(sh, sh->T * sh->k, sh->f))) return st;
-  if (is_fp8(sh) || is_mx4(sh)) return MOE_ERR_UNSUPPORTED;  // moe_grouped_gemm_fwd_e4m3 / _mx / _mx4
+  if (is_fp8(sh) || is_mx4(sh) || is_i4(sh)) return MOE_ERR_UNSUPPORTED;  // moe_grouped_gemm_fwd_e4m3 / _mx / _mx4 / _i4
   if (!offsets || !xp || !W1 || !W3 || !W2 || !ab || !h || !o) return MOE_ERR_INVALID;
   GemmArgs a = expert_args(sh, offsets);
   a.xp = xp; a.W1 = W1; a.W3 = W3; a.W2 = W2;
@@ -582,7 +613,7 @@ int moe_grouped_gemm_bwd(const moe_shape* sh, const int32_t* offsets, const void
   int st = check_shape(sh);
   if (st) return st;
   if ((st = check_gemm_dims(sh, sh->T * sh->k, sh->f))) return st;
-  if (is_fp8(sh) || is_mx4(sh)) return MOE_ERR_UNSUPPORTED;  // moe_grouped_gemm_bwd_e4m3 / _mx
+  if (is_fp8(sh) || is_mx4(sh) || is_i4(sh)) return MOE_ERR_UNSUPPORTED;  // moe_grouped_gemm_bwd_e4m3 / _mx
   if (!offsets || !xp || !ab || !h || !dO || !W1 || !W3 || !W2 || !dab || !dXp || !dW1 || !dW3 ||
       !dW2)
     return MOE_ERR_INVALID;
@@ -1086,6 +1117,69 @@ int moe_grouped_gemm_fwd_mx4(const moe_shape* sh, const int32_t* offsets, const 
 }
 
 namespace {
+int check_i4_matrix(int64_t group, int64_t E, int64_t R, int64_t C, bool pair) {
+  int st = check_mx4_matrix(E, R, C, pair);
+  return st ? st : group_ok(group) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+}  // namespace
+
+int moe_quantize_weights_i4(const void* W, const void* W_pair, int32_t src_dtype, int32_t asymmetric, int64_t group,
+                            int64_t E, int64_t R, int64_t C, uint8_t* codes, uint32_t* scales, void* stream) {
+  if (!W || !codes || !scales) return MOE_ERR_INVALID;
+  int st = check_i4_matrix(group, E, R, C, W_pair != nullptr);
+  if (st) return st;
+  if (src_dtype != MOE_BF16 && src_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  if (!aligned(16, (const char*)W, (const char*)W_pair, codes, (const uint8_t*)scales)) return MOE_ERR_UNSUPPORTED;
+  return quant_weights_i4_launch(W, W_pair, src_dtype == MOE_F32, E, R, C, (int)group, asymmetric != 0, codes, scales,
+                                 (hipStream_t)stream);
+}
+
+int moe_pack_weights_i4(const uint8_t* q, const float* s, const uint8_t* z, const uint8_t* q_pair, const float* s_pair,
+                        const uint8_t* z_pair, int64_t group, int64_t E, int64_t R, int64_t C, uint8_t* codes,
+                        uint32_t* scales, void* stream) {
+  if (!q || !s || !codes || !scales || (!q_pair != !s_pair) || (z_pair && !q_pair)) return MOE_ERR_INVALID;
+  int st = check_i4_matrix(group, E, R, C, q_pair != nullptr);
+  if (st) return st;
+  if (!aligned(16, q, q_pair, (const uint8_t*)s, (const uint8_t*)s_pair, codes, (const uint8_t*)scales))
+    return MOE_ERR_UNSUPPORTED;
+  return pack_weights_i4_launch(I4Source{q, s, z}, I4Source{q_pair, s_pair, z_pair}, E, R, C, (int)group, codes, scales,
+                                (hipStream_t)stream);
+}
+
+int moe_dequantize_weights_i4(const uint8_t* codes, const uint32_t* scales, int64_t group, int64_t E, int64_t R,
+                              int64_t C, void* W, void* W_pair, void* stream) {
+  if (!W || !codes || !scales) return MOE_ERR_INVALID;
+  int st = check_i4_matrix(group, E, R, C, W_pair != nullptr);
+  if (st) return st;
+  if (!aligned(16, codes, (const uint8_t*)scales, (const uint8_t*)W, (const uint8_t*)W_pair))
+    return MOE_ERR_UNSUPPORTED;
+  return dequant_weights_i4_launch(codes, scales, E, R, C, (int)group, W, W_pair, (hipStream_t)stream);
+}
+
+int moe_grouped_gemm_fwd_i4(const moe_shape* sh, const int32_t* offsets, const int32_t* token_of, const void* x,
+                            const moe_i4_weights* w, void* o, void* ws, size_t ws_bytes, void* stream) {
+  int st = check_shape(sh);
+  if (st) return st;
+  if ((st = check_i4_dims(sh))) return st;
+  if (!offsets || !x || !o) return MOE_ERR_INVALID;
+  if ((st = check_weights(w))) return st;
+  if (!aligned(16, (const char*)x, (const char*)o, (const char*)ws) || !aligned(4, offsets, token_of))
+    return MOE_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < i4_ws_bytes(sh)) return MOE_ERR_WORKSPACE;
+  I4Args a = {};
+  a.offsets = offsets; a.token_of = token_of;
+  a.E = (int)sh->E; a.d = (int)sh->d; a.f = (int)sh->f; a.P = (int)(sh->T * sh->k); a.T = (int)sh->T;
+  a.group = (int)w->group;
+  a.a = (const uint16_t*)x; a.w = w->W13; a.ws = w->W13s;
+  a.h = (uint16_t*)ws;
+  if ((st = gemm_i4_launch(1, a, (hipStream_t)stream))) return st;
+  a.token_of = nullptr;
+  a.a = (const uint16_t*)ws; a.w = w->W2; a.ws = w->W2s;
+  a.o = (uint16_t*)o;
+  return gemm_i4_launch(2, a, (hipStream_t)stream);
+}
+
+namespace {
 constexpr int64_t kNormMaxD = 32768;  // a row lies in the registers of 16 wavefronts
 // Rows [rows][d] of quantised values: whole blocks
 int check_q_rows(int32_t q_dtype, int64_t d) {
@@ -1150,6 +1244,7 @@ int moe_layer_fwd(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t 
   int st = check_shape(sh);
   if (st) return st;
   if (is_mx4(sh)) return layer_fwd_mx4(sh, io, ws, ws_bytes, stream);
+  if (is_i4(sh)) return layer_fwd_i4(sh, io, ws, ws_bytes, stream);
   if (is_fp8(sh)) return layer_fwd_e4m3(sh, io, ws, ws_bytes, stream);
   if (io && io->memory_efficient) return layer_fwd_rowscaled(sh, io, ws, ws_bytes, stream);
   if ((st = check_gemm_dims(sh, sh->T * sh->k, sh->f))) return st;
@@ -1197,7 +1292,7 @@ int moe_layer_bwd(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t 
                   void* stream) {
   int st = check_shape(sh);
   if (st) return st;
-  if (is_mx4(sh)) return MOE_ERR_UNSUPPORTED;
+  if (is_mx4(sh) || is_i4(sh)) return MOE_ERR_UNSUPPORTED;
   if (is_fp8(sh)) return layer_bwd_e4m3(sh, io, ws, ws_bytes, stream);
   if (io && io->memory_efficient) return layer_bwd_rowscaled(sh, io, ws, ws_bytes, stream);
   if ((st = check_gemm_dims(sh, sh->T * sh->k, sh->f))) return st;
@@ -1275,6 +1370,49 @@ int layer_fwd_mx4(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t 
                                      (char*)ws + pws, gws, stream)))
     return st;
   return moe_unpermute(sh, io->o, io->row_of, io->topk_prob, nullptr, io->y, stream);
+}
+
+// Integer-weight layers: x is read through the map; a shared expert has bf16 weights
+int layer_fwd_i4(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t ws_bytes,
+                 void* stream) {
+  int st;
+  if ((st = check_i4_dims(sh))) return st;
+  moe_shape bf = *sh;
+  bf.dtype = MOE_BF16;
+  if (sh->f_shared && (st = check_gemm_dims(&bf, sh->T, sh->f_shared))) return st;
+  if (!io || !io->logits || !io->x || !io->topk_idx || !io->topk_prob || !io->counts || !io->offsets ||
+      !io->row_of || !io->token_of || !io->o || !io->y)
+    return MOE_ERR_INVALID;
+  if ((st = check_weights(io->wi4))) return st;
+  if (sh->f_shared && (!io->Ws1 || !io->Ws3 || !io->Ws2 || !io->s_ab || !io->s_h || !io->ys))
+    return MOE_ERR_INVALID;
+  if (io->memory_efficient) return MOE_ERR_UNSUPPORTED;
+  if (!aligned(16, (const char*)io->x, (const char*)io->o, (const char*)io->y, (const char*)ws))
+    return MOE_ERR_UNSUPPORTED;
+  const size_t pws = permute_ws_bytes(sh->T, sh->E);
+  const size_t gws = i4_ws_bytes(sh);
+  if (!ws || ws_bytes < pws + 256 + gws || !aux_ws_ok(sh, io, ws_bytes)) return MOE_ERR_WORKSPACE;
+  if ((st = layer_route(sh, io, ws, ws_bytes, stream))) return st;
+  if ((st = moe_permute(sh, nullptr, io->topk_idx, nullptr, 1, io->counts, io->offsets, io->row_of,
+                        io->token_of, nullptr, ws, pws, stream)))
+    return st;
+  if ((st = layer_aux_loss(sh, io, ws, ws_bytes, stream))) return st;
+  if ((st = moe_grouped_gemm_fwd_i4(sh, io->offsets, io->token_of, io->x, io->wi4, io->o,
+                                    (char*)ws + pws + 256, gws, stream)))
+    return st;
+  const void* add = nullptr;
+  if (sh->f_shared) {
+    hipStream_t s = (hipStream_t)stream;
+    int32_t* off2 = (int32_t*)((char*)ws + pws);
+    fill_offsets_kernel<<<1, 64, 0, s>>>(off2, (int32_t)sh->T);
+    TRE_LAUNCH_CHECK();
+    GemmArgs a = shared_args(sh, off2);
+    a.xp = io->x; a.W1 = io->Ws1; a.W3 = io->Ws3; a.W2 = io->Ws2;
+    a.ab_out = io->s_ab; a.h_out = io->s_h; a.h = io->s_h; a.o_out = io->ys;
+    if ((st = fwd_sequence(&bf, a, s))) return st;
+    add = io->ys;
+  }
+  return moe_unpermute(sh, io->o, io->row_of, io->topk_prob, add, io->y, stream);
 }
 
 // e4m3 and MXFP8 layers

@@ -97,7 +97,7 @@ def _check(status, call):
 
 def make_shape(T, d, E, k, f, f_shared=0, dtype="bf16") -> N.moe_shape:
     code = {"f32": N.MOE_F32, "bf16": N.MOE_BF16, "e4m3": N.MOE_E4M3, "mxfp8": N.MOE_MXFP8,
-            "mxfp4": N.MOE_MXFP4, "mxfp4_a8": N.MOE_MXFP4_A8}[dtype]
+            "mxfp4": N.MOE_MXFP4, "mxfp4_a8": N.MOE_MXFP4_A8, "int4": N.MOE_INT4}[dtype]
     return N.moe_shape(int(T), int(d), int(E), int(k), int(f), int(f_shared), code, 0)
 
 
@@ -426,6 +426,91 @@ def moe_grouped_gemm_fwd_mx4(sh, offsets, token_of, xq, xs, w: MX4Weights, o, ws
         None if ws is None else b("ws", ws, ws.dtype, 0), _nbytes(ws), b.stream(stream)), call)
 
 
+def _i4_group(call, group):
+    if group not in (32, 64, 128):
+        raise ValueError(f"{call}: groups have 32, 64 or 128 rows, not {group}")
+    return int(group)
+
+
+def moe_quantize_weights_i4(W, W_pair, group, asymmetric, codes, scales, stream=None):
+    """Integer tiles of bf16 or fp32 matrices W [E][R][C] with a scale word (int32 storage) for each `group` rows;
+    W_pair (or None): a second matrix whose 16-column groups alternate with W's."""
+    call = "moe_quantize_weights_i4"
+    E, R, Cc = W.shape
+    if W_pair is not None and W_pair.shape != W.shape:
+        raise ValueError("W_pair must have W's shape")
+    code, b, one, group = _src_dtype(call, W), _Bufs(call), E * R * Cc, _i4_group(call, group)
+    n = one if W_pair is None else 2 * one
+    _check(N.lib().moe_quantize_weights_i4(
+        b("W", W, W.dtype, one), b.opt("W_pair", W_pair, W.dtype, one), code, int(bool(asymmetric)), group, E, R, Cc,
+        b("codes", codes, U8, n // 2), b("scales", scales, I32, n // group), b.stream(stream)), call)
+
+
+def moe_pack_weights_i4(q, s, z, pair, group, codes, scales, stream=None):
+    """The same tiles from a checkpoint's codes q uint8 [E][R][C], scales s fp32 [E][R/group][C] and zero points z
+    uint8 (None: 8); pair: None or the second matrix's (q, s, z)."""
+    call = "moe_pack_weights_i4"
+    E, R, Cc = q.shape
+    b, one, group = _Bufs(call), E * R * Cc, _i4_group(call, group)
+    n = one if pair is None else 2 * one
+
+    def source(q_, s_, z_):
+        return (b("q", q_, U8, one), b("s", s_, F32, one // group), b.opt("z", z_, U8, one // group, 1))
+    second = (None, None, None) if pair is None else source(*pair)
+    _check(N.lib().moe_pack_weights_i4(*source(q, s, z), *second, group, E, R, Cc, b("codes", codes, U8, n // 2),
+                                       b("scales", scales, I32, n // group), b.stream(stream)), call)
+
+
+def moe_dequantize_weights_i4(codes, scales, group, W, W_pair=None, stream=None):
+    """The bf16 weights W [E][R][C] (and W_pair) that integer tiles stand for."""
+    call = "moe_dequantize_weights_i4"
+    E, R, Cc = W.shape
+    if W_pair is not None and W_pair.shape != W.shape:
+        raise ValueError("W_pair must have W's shape")
+    b, one, group = _Bufs(call), E * R * Cc, _i4_group(call, group)
+    n = one if W_pair is None else 2 * one
+    _check(N.lib().moe_dequantize_weights_i4(
+        b("codes", codes, U8, n // 2), b("scales", scales, I32, n // group), group, E, R, Cc, b("W", W, BF16, one),
+        b.opt("W_pair", W_pair, BF16, one), b.stream(stream)), call)
+
+
+class I4Weights:
+    """The moe_i4_weights struct over torch tensors (kept alive here)."""
+
+    NAMES = ("W13", "W2", "W13s", "W2s")
+
+    def __init__(self, tensors: dict, group: int):
+        self.tensors = {n: tensors[n] for n in self.NAMES}
+        self.group = _i4_group("I4Weights", group)
+        self.struct = N.moe_i4_weights(*[_ptr(self.tensors[n], I32 if n.endswith("s") else U8).value
+                                         for n in self.NAMES], self.group)
+        self.numels = tuple(t.numel() for t in self.tensors.values())
+        devices = {t.get_device() for t in self.tensors.values()}
+        self.device = devices.pop() if len(devices) == 1 else -1
+
+    def __getitem__(self, name):
+        return self.tensors[name]
+
+
+def moe_grouped_gemm_fwd_i4(sh, offsets, token_of, x, w: I4Weights, o, ws, stream=None):
+    """The experts' forward with integer weights on bf16 rows (row r is row token_of[r] of x, or row r when
+    token_of is None); o [P][d] bf16."""
+    call = "moe_grouped_gemm_fwd_i4"
+    b = _Bufs(call)
+    T, d, E, f = sh.T, sh.d, sh.E, sh.f
+    P, mat = T * sh.k, E * d * f
+    n13, n2, n13s, n2s = w.numels
+    if n13 < mat or 2 * n2 < mat or n13s * w.group < 2 * mat or n2s * w.group < mat:
+        raise ValueError(f"{call}: W13, W2 and their scales have {w.numels} elements, "
+                         f"{(mat, mat // 2, 2 * mat // w.group, mat // w.group)} are needed")
+    if w.device != b.dev:
+        raise ValueError(f"{call}: the weights are not on the current device")
+    _check(N.lib().moe_grouped_gemm_fwd_i4(
+        C.byref(sh), b("offsets", offsets, I32, E + 1, 4), b.opt("token_of", token_of, I32, P, 4),
+        b("x", x, BF16, (P if token_of is None else T) * d), C.byref(w.struct), b("o", o, BF16, P * d),
+        None if ws is None else b("ws", ws, ws.dtype, 0), _nbytes(ws), b.stream(stream)), call)
+
+
 def _io(buffers: dict) -> N.moe_layer_io:
     io = N.moe_layer_io()
     for name in N.IO_FIELDS:
@@ -440,6 +525,9 @@ def _io(buffers: dict) -> N.moe_layer_io:
     wmx4 = buffers.get("wmx4")
     if wmx4 is not None:
         io.wmx4 = C.cast(C.pointer(wmx4.struct), C.c_void_p).value
+    wi4 = buffers.get("wi4")
+    if wi4 is not None:
+        io.wi4 = C.cast(C.pointer(wi4.struct), C.c_void_p).value
     io.aux_alpha = float(buffers.get("aux_alpha", 0.0))
     io.memory_efficient = int(buffers.get("memory_efficient", 0))
     io.fused_permute = int(buffers.get("fused_permute", 0))
