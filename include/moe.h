@@ -954,8 +954,8 @@ int moe_probe_mfma(int dtype, int64_t iters, unsigned long long* ticks, float* s
 size_t moe_workspace_bytes(const moe_shape* sh, int kind);
 
 /* 1 where the expert products of shape sh run on the kernels for few rows, else
- * 0: moe_grouped_gemm_fwd_mx4 (MOE_MXFP4, MOE_MXFP4_A8) and the 8-bit checkpoint
- * calls (MOE_BF16).  Those kernels split the contraction, so results of calls on
+ * 0: moe_grouped_gemm_fwd_mx4 (MOE_MXFP4, MOE_MXFP4_A8), moe_grouped_gemm_fwd_i4
+ * (MOE_INT4) and the 8-bit checkpoint calls (MOE_BF16).  Those kernels split the contraction, so results of calls on
  * the two sides differ in the order of their fp32 sums.  0 for other types and
  * for shapes that are refused. */
 int moe_few_rows(const moe_shape* sh);

@@ -17,6 +17,7 @@ namespace tre {
 namespace {
 using namespace gemm;
 
+typedef int i32x2_t __attribute__((ext_vector_type(2)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ f32x4_t mma(const bf16x8_t& w, const bf16x8_t& x, const f32x4_t& c) {
@@ -200,14 +201,253 @@ int launch_rows(const I4Args& a, hipStream_t s) {
   return MOE_OK;
 }
 
+// Many rows per expert: tiles of 128 rows x 256 stored columns, four wavefronts side
+// by side (each all 128 rows x 64 columns as 8 x 4 fragments), two blocks to a compute
+// unit, so that one block's prologue, epilogue and barrier waits run under the
+// other's products.  A wavefront decodes its own 64 columns, one step of 32 rows of W
+// ahead of the products that take them, between those products: 19 vector
+// instructions for the 8 weights of a fragment and lane, 76 a step of 32 products.
+//
+// A (activations): stages of 64 k through three LDS slots, 128 rows of 128 bytes, the
+// 16-byte chunk c of row r stored at chunk c ^ ((r >> 1) & 7), which spreads the 16
+// rows of a fragment read over all banks.  B: 128 k (two stages, four steps) as stored,
+// 4 KB of codes and 256 bytes of scales for each group of a wavefront's 64 columns;
+// only that wavefront reads them, into registers half by half, so one slot is
+// enough and no barrier guards it.  Every byte arrives by buffer_load ...
+// lds.  One barrier a stage: it follows the stage's last fragment read, so the slot
+// that the loads of the stage after next go to (issued in the next stage) is free.
+template <int FC, int U>
+__global__ __launch_bounds__(256, 2) void gemm_i4_tile_kernel(I4Args args, int NT) {
+  constexpr int BM = 128, BN = 256, FM = BM / 16;
+  constexpr int A_BYTES = BM * 128, BW = 4096 + U * 256;   // an A slot; a wavefront's part of B
+  constexpr int B_AT = 3 * A_BYTES;
+  constexpr int NA = A_BYTES / 4096, NBL = 4 + U;          // a wavefront's loads of a stage's A and of B
+  __shared__ __attribute__((aligned(1024))) char lds[B_AT + 4 * BW];
+  __shared__ int sched[8];
+  TileInfo ti;
+  if (!decode_ragged_m<BM, 4, 32>(args.offsets, args.E, NT, sched, ti)) return;
+  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+  const int w = uniform((int)threadIdx.x >> 6);
+  const int e = uniform(ti.e), row0 = uniform(ti.row0), rows = uniform(ti.rows);
+  const int n0 = uniform(ti.n0) * BN;
+  const int K = FC == 1 ? args.d : args.f, N = FC == 1 ? 2 * args.f : args.d;
+  const int KT = K >> 7;
+
+  // ---- sources: rows past the expert's end and columns past N read as zero
+  const bool gather = FC == 1 && args.token_of != nullptr;
+  const uint32_t a_rows = (uint32_t)(gather ? args.T : args.P), a_ld = (uint32_t)K * 2u;
+  const rsrc_t a_src = make_rsrc(args.a, a_rows * a_ld);
+  const int col = n0 + 64 * w;                  // this wavefront's 64 columns
+  const uint32_t b_size = col < N ? 4096u * (uint32_t)KT : 0u;
+  const int colc = min(col, N - 64);
+  const rsrc_t b_src = make_rsrc(args.w + ((size_t)e * (N >> 4) + (size_t)(colc >> 4)) * KT * 1024, b_size);
+  const rsrc_t bs_src = make_rsrc(args.ws + ((size_t)e * (N >> 6) + (size_t)(colc >> 6)) * KT * (U * 64), b_size / 16 * U);
+  constexpr uint32_t kPast = 0x80000000u;       // past every range
+  uint32_t a_off[NA];
+#pragma unroll
+  for (int q = 0; q < NA; ++q) {
+    const int m = 8 * (w * NA + q) + (lane >> 3);   // a load: 8 rows
+    const int c = (lane & 7) ^ ((m >> 1) & 7);
+    const int pr = row0 + min(m, rows - 1);
+    const uint32_t row = gather ? (uint32_t)args.token_of[pr] : (uint32_t)pr;
+    a_off[q] = m < rows && row < a_rows ? row * a_ld + (uint32_t)c * 16u : kPast;
+  }
+  const uint32_t lane16 = (uint32_t)lane * 16u, lane4 = (uint32_t)lane * 4u;
+  const uint32_t lds_base = (uint32_t)uniform((int)(uint32_t)(size_t)LDS_PTR(lds));
+  const uint32_t b_dst = lds_base + (uint32_t)(B_AT + w * BW);
+
+  // Loads; past the last stage nothing is read and zeros land.
+  auto src = [&](rsrc_t v, bool live) __attribute__((always_inline)) {
+    v[2] = live ? v[2] : 0;
+    return uniform_rsrc(v);
+  };
+  auto issue_a = [&](int kt, int slot, int q) __attribute__((always_inline)) {
+    const bool live = kt < 2 * KT;
+    dma16(src(a_src, live), a_off[q], (uint32_t)(live ? kt : 0) * 128u,
+          lds_base + (uint32_t)(slot * A_BYTES + (w * NA + q) * 1024));
+  };
+  auto issue_b = [&](int P, int j) __attribute__((always_inline)) {
+    const bool live = P < KT;
+    dma16(src(b_src, live), lane16, (uint32_t)(j * KT + (live ? P : 0)) * 1024u, b_dst + (uint32_t)(j * 1024));
+  };
+  auto issue_bs = [&](int P, int u) __attribute__((always_inline)) {
+    const bool live = P < KT;
+    dma4(src(bs_src, live), lane4, (uint32_t)((live ? P : 0) * U + u) * 256u, b_dst + (uint32_t)(4096 + u * 256));
+  };
+
+  // ---- fragments
+  const uint32_t sw = (uint32_t)(r >> 1) & 7u;
+  const uint32_t a_half[2] = {(uint32_t)r * 128u + (((uint32_t)g ^ sw) << 4),
+                              (uint32_t)r * 128u + (((uint32_t)(4 + g) ^ sw) << 4)};
+  auto ld16 = [&](const char* p) __attribute__((always_inline)) -> i32x4_t {
+    return *(const __attribute__((address_space(3))) i32x4_t*)p;
+  };
+  auto read_a = [&](int slot, auto H, int i) __attribute__((always_inline)) -> bf16x8_t {
+    constexpr int h = decltype(H)::value;
+    return __builtin_bit_cast(bf16x8_t, ld16(lds + (uint32_t)slot * A_BYTES + a_half[h] + i * 2048));
+  };
+  // 64 k of the wavefront's weights as stored: half HB of the slot's 128 k, and the
+  // scale words of the groups that start there
+  constexpr int UH = U == 4 ? 2 : 1;
+  i32x2_t raw[4];
+  i32x4_t words[UH];
+  auto read_b = [&](auto HB) __attribute__((always_inline)) {
+    constexpr int hb = decltype(HB)::value;
+    const char* b = lds + B_AT + w * BW;
+    if constexpr (hb == 0 || U > 1)
+      static_for<0, UH>([&](auto I) __attribute__((always_inline)) {
+        words[I.value] = ld16(b + 4096 + (hb * (U / 2) + I.value) * 256 + r * 16);
+      });
+    static_for<0, 4>([&](auto J) __attribute__((always_inline)) {
+      raw[J.value] = *(const __attribute__((address_space(3))) i32x2_t*)(b + J.value * 1024 + lane * 16 + hb * 8);
+    });
+  };
+  float sc[4], nz[4];
+  u32x4_t wd[2][4];                             // decoded fragments of this step and the next
+  // half `H` (4 of 8 k) of fragment J of step S
+  auto decode = [&](auto S, auto J, auto H) __attribute__((always_inline)) {
+    constexpr int s = decltype(S)::value, j = decltype(J)::value, h = decltype(H)::value;
+    if constexpr (h == 0 && s * U % 4 == 0) i4::unpack((uint32_t)words[U == 4 ? s & 1 : 0][j], sc[j], nz[j]);
+    const uint32_t t = (uint32_t)raw[j][s & 1];
+    float v[4];
+    i4::values4((h ? t >> 4 : t) & 0x0f0f0f0fu, sc[j], nz[j], v);
+    uint32_t x = pack_bf16x2(v[0], v[1]), y = pack_bf16x2(v[2], v[3]);
+    asm volatile("" : "+v"(x), "+v"(y));        // decoded here, between these products
+    wd[s & 1][j][2 * h] = x;
+    wd[s & 1][j][2 * h + 1] = y;
+  };
+
+  f32x4_t acc[FM][4];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  static_for<0, 4>([&](auto J) __attribute__((always_inline)) { issue_b(0, J.value); });
+  static_for<0, U>([&](auto I) __attribute__((always_inline)) { issue_bs(0, I.value); });
+  static_for<0, 2>([&](auto S) __attribute__((always_inline)) {
+    static_for<0, NA>([&](auto Q) __attribute__((always_inline)) { issue_a(S.value, S.value, Q.value); });
+  });
+  wait_vmcnt<NA>();
+  block_barrier();
+  read_b(IntC<0>{});
+  static_for<0, 4>([&](auto J) __attribute__((always_inline)) {
+    decode(IntC<0>{}, J, IntC<0>{});
+    decode(IntC<0>{}, J, IntC<1>{});
+  });
+  bf16x8_t xf[4];                               // A fragments in flight: i & 3
+  int slot = 0;                                 // of the current stage
+  xf[0] = read_a(0, IntC<0>{}, 0);
+  xf[1] = read_a(0, IntC<0>{}, 1);
+  const int nfr = min(FM, (rows + 15) >> 4);    // fragments with rows
+
+  // Step S (of 4) of the 128 k P: 32 k, half S & 1 of stage 2 P + S / 2.
+  auto step = [&](int P, auto S, auto SKIP) __attribute__((always_inline)) {
+    constexpr int s = decltype(S)::value, h = s & 1;
+    constexpr bool skip = decltype(SKIP)::value;
+    const int kt = 2 * P + (s >> 1);
+    const int next = slot == 2 ? 0 : slot + 1, after = next == 2 ? 0 : next + 1;
+    static_for<0, FM>([&](auto I) __attribute__((always_inline)) {
+      constexpr int i = I.value;
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (h == 0 && i >= 1 && i <= NA) issue_a(kt + 2, after, i - 1);
+      // the second half of B's slot, then (its reads are in registers: products waited
+      // for fragments read after them) the next 128 k into it
+      if constexpr (s == 1 && i == 0) read_b(IntC<1>{});
+      if constexpr (s == 1 && i == 3)
+        static_for<0, U>([&](auto Q) __attribute__((always_inline)) { issue_bs(P + 1, Q.value); });
+      if constexpr (s == 1 && i >= 3 && i <= 5) issue_b(P + 1, i - 3);
+      if constexpr (s == 1 && i == 5) issue_b(P + 1, 3);
+      if constexpr (s == 3 && i == 0) {
+        // the next 128 k of B have landed (and A's next stage, older): newer are this stage's A loads
+        wait_vmcnt<NA>();
+        asm volatile("" ::: "memory");
+        read_b(IntC<0>{});
+      }
+      if constexpr (i + 2 < FM) {
+        if (!skip || i + 2 < nfr) xf[(i + 2) & 3] = read_a(slot, IntC<h>{}, i + 2);
+      } else if constexpr (h == 0) {
+        xf[(i + 2) & 3] = read_a(slot, IntC<1>{}, i + 2 - FM);
+      } else {
+        xf[(i + 2) & 3] = read_a(next, IntC<0>{}, i + 2 - FM);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (!skip || i < nfr) {
+        static_for<0, 4>([&](auto J) __attribute__((always_inline)) {
+          acc[i][J.value] = mma(__builtin_bit_cast(bf16x8_t, wd[h][J.value]), xf[i & 3], acc[i][J.value]);
+        });
+      }
+      // the next step's weights, half a fragment at a time (those that come out of the
+      // reads above one place later)
+      constexpr IntC<(s + 1) & 3> SN{};
+      if constexpr (h == 0) {
+        decode(SN, IntC<i / 2>{}, IntC<i & 1>{});
+      } else {
+        if constexpr (i == 1) decode(SN, IntC<0>{}, IntC<0>{});
+        if constexpr (i >= 1) decode(SN, IntC<i / 2>{}, IntC<i & 1>{});
+      }
+      stay(acc[i]);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (h == 1 && i == FM - 3) {
+        __builtin_amdgcn_s_waitcnt(0xc07f);     // lgkmcnt(0): this stage's reads are in registers
+        // the next stage has landed: newer are the stage after next and, first stage, B
+        if constexpr (s == 1) wait_vmcnt<NA + NBL>();
+        block_barrier();
+      }
+    });
+    if constexpr (h == 1) slot = next;
+  };
+  auto run = [&](auto SKIP) __attribute__((always_inline)) {
+    for (int P = 0; P < KT; ++P)
+      static_for<0, 4>([&](auto S) __attribute__((always_inline)) { step(P, S, SKIP); });
+  };
+  if (nfr == FM) run(IntC<0>{});
+  else run(IntC<1>{});
+  wait_vmcnt<0>();  // no LDS write may be in flight when the block ends
+
+  if (col >= N) return;
+  static_for<0, FM>([&](auto I) __attribute__((always_inline)) {
+    constexpr int i = I.value;
+    const int m = 16 * i + r;
+    const size_t row = (size_t)(row0 + m);
+    if constexpr (FC == 1) store_h(acc[i], m < rows, row, col >> 1, args.f, lane, args.h);
+    else store_o(acc[i], m < rows, row, col, args.d, lane, args.o);
+  });
+}
+
+template <int FC, int U>
+int launch_tiles(const I4Args& a, hipStream_t s) {
+  const int64_t NT = ((FC == 1 ? 2 * (int64_t)a.f : (int64_t)a.d) + 255) / 256;
+  // at most sum_e ceil(m_e / 128) row tiles; a block past the device-side count ends at once
+  const int64_t grid = ((int64_t)a.P / 128 + a.E) * NT;
+  if (!launch_fits(grid, 256)) return MOE_ERR_UNSUPPORTED;
+  gemm_i4_tile_kernel<FC, U><<<(unsigned)grid, 256, 0, s>>>(a, (int)NT);
+  TRE_LAUNCH_CHECK();
+  return MOE_OK;
+}
+
+template <int FC, int U>
+int launch(const I4Args& a, hipStream_t s) {
+  return gemm_i4_few_rows(a) ? launch_rows<FC, U>(a, s) : launch_tiles<FC, U>(a, s);
+}
 template <int FC>
 int launch_fc(const I4Args& a, hipStream_t s) {
-  if (a.group == 128) return launch_rows<FC, 1>(a, s);
-  if (a.group == 64) return launch_rows<FC, 2>(a, s);
-  return launch_rows<FC, 4>(a, s);
+  if (a.group == 128) return launch<FC, 1>(a, s);
+  if (a.group == 64) return launch<FC, 2>(a, s);
+  return launch<FC, 4>(a, s);
 }
 
 }  // namespace
+
+// Which kernel (the rule of the MXFP4 products).
+bool gemm_i4_few_rows(const I4Args& a) {
+  if ((int64_t)a.P <= 20 * (int64_t)a.E) return true;
+  const double pieces = a.P / 32.0 + 0.5 * (a.P < a.E ? a.P : a.E);
+  auto steps = [&](int64_t n, int64_t k) {
+    const double rounds = pieces * (double)(n / 64) / 512.0;
+    return (rounds > 1.0 ? rounds : 1.0) * (double)k;
+  };
+  return steps(2 * (int64_t)a.f, a.d) + steps(a.d, a.f) <= 1.5 * ((double)a.d + (double)a.f);
+}
 
 int gemm_i4_launch(int fc, const I4Args& a, hipStream_t s) {
   return fc == 1 ? launch_fc<1>(a, s) : launch_fc<2>(a, s);

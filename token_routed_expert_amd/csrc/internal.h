@@ -246,6 +246,7 @@ struct I4Args {
   uint16_t* o;
 };
 int gemm_i4_launch(int fc, const I4Args& a, hipStream_t s);
+bool gemm_i4_few_rows(const I4Args& a);  // which of its two kernels (E, d, f and P decide)
 
 // permute.hip: rows of e4m3 codes [T][d] and their scales [T][d/128]
 int permute_e4m3_launch(const uint8_t* codes, const float* scales, const int32_t* row_of, int T,

@@ -475,6 +475,12 @@ int moe_few_rows(const moe_shape* sh) {
   if (check_shape(sh) != MOE_OK) return 0;
   if (sh->dtype == MOE_BF16)
     return check_gemm_dims(sh, sh->T * sh->k, sh->f) == MOE_OK && few_rows(sh);
+  if (is_i4(sh)) {
+    if (check_i4_dims(sh) != MOE_OK) return 0;
+    I4Args a = {};
+    a.E = (int)sh->E; a.d = (int)sh->d; a.f = (int)sh->f; a.P = (int)(sh->T * sh->k);
+    return gemm_i4_few_rows(a);
+  }
   if (!is_mx4(sh) || check_mx4_dims(sh) != MOE_OK) return 0;
   Mx4Args a = {};
   a.E = (int)sh->E; a.d = (int)sh->d; a.f = (int)sh->f; a.P = (int)(sh->T * sh->k);

@@ -106,7 +106,7 @@ def moe_workspace_bytes(sh: N.moe_shape, kind: int) -> int:
 
 
 def moe_few_rows(sh: N.moe_shape) -> bool:
-    """Whether the MXFP4 or 8-bit checkpoint products of this shape take the kernels for few rows."""
+    """Whether the MXFP4, integer-weight or 8-bit checkpoint products of this shape take the kernels for few rows."""
     return bool(N.lib().moe_few_rows(C.byref(sh)))
 
 
