@@ -19,6 +19,7 @@ using namespace gemm;
 
 typedef int i32x2_t __attribute__((ext_vector_type(2)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ f32x4_t mma(const bf16x8_t& w, const bf16x8_t& x, const f32x4_t& c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x, c, 0, 0, 0);
@@ -201,24 +202,46 @@ int launch_rows(const I4Args& a, hipStream_t s) {
   return MOE_OK;
 }
 
+// D += W X for a block of 32 columns of W x 32 rows x 16 k.  Lane l: column / row l &
+// 31, the eight k from 8 (l >> 5) on; D: row l & 31, column 8 (i >> 2) + 4 (l >> 5) +
+// (i & 3) in register i.
+__device__ __forceinline__ f32x16_t mma32(const u32x4_t& w, const bf16x8_t& x, const f32x16_t& c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, w), x, c, 0, 0, 0);
+}
+__device__ __forceinline__ void stay32(f32x16_t (&a)[2]) { asm volatile("" : "+v"(a[0]), "+v"(a[1])); }
+
+// Four columns each of x (4 (l >> 5) on) and y (8 further on) -> eight consecutive ones
+// as bf16, from column 8 (l >> 5) on.
+__device__ __forceinline__ u32x4_t pair32(const f32x4_t& x, const f32x4_t& y) {
+  const uint32_t x0 = pack_bf16x2(x[0], x[1]), x1 = pack_bf16x2(x[2], x[3]);
+  const uint32_t y0 = pack_bf16x2(y[0], y[1]), y1 = pack_bf16x2(y[2], y[3]);
+  const auto a = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
+  return u32x4_t{(uint32_t)a[0], (uint32_t)b[0], (uint32_t)a[1], (uint32_t)b[1]};
+}
+template <int Q>
+__device__ __forceinline__ f32x4_t quad(const f32x16_t& a) {
+  return f32x4_t{a[4 * Q], a[4 * Q + 1], a[4 * Q + 2], a[4 * Q + 3]};
+}
+
 // Many rows per expert: tiles of 128 rows x 256 stored columns, four wavefronts side
-// by side (each all 128 rows x 64 columns as 8 x 4 fragments), two blocks to a compute
-// unit, so that one block's prologue, epilogue and barrier waits run under the
-// other's products.  A wavefront decodes its own 64 columns, one step of 32 rows of W
+// by side (each all 128 rows x 64 columns as 4 x 2 fragments of 32 x 32), two blocks
+// to a compute unit, so that one block's prologue, epilogue and barrier waits run under
+// the other's products.  A wavefront decodes its own 64 columns, one step of 32 k
 // ahead of the products that take them, between those products: 19 vector
-// instructions for the 8 weights of a fragment and lane, 76 a step of 32 products.
+// instructions for 8 weights a lane, 76 a step of 16 products.
 //
 // A (activations): stages of 64 k through three LDS slots, 128 rows of 128 bytes, the
-// 16-byte chunk c of row r stored at chunk c ^ ((r >> 1) & 7), which spreads the 16
-// rows of a fragment read over all banks.  B: 128 k (two stages, four steps) as stored,
-// 4 KB of codes and 256 bytes of scales for each group of a wavefront's 64 columns;
-// only that wavefront reads them, into registers half by half, so one slot is
-// enough and no barrier guards it.  Every byte arrives by buffer_load ...
-// lds.  One barrier a stage: it follows the stage's last fragment read, so the slot
-// that the loads of the stage after next go to (issued in the next stage) is free.
+// 16-byte chunk c of row r stored at chunk c ^ ((r >> 1) & 7), which spreads the rows
+// of a fragment read over all banks.  B: 128 k (two stages, four steps) as stored, 4
+// KB of codes and 256 bytes of scales for each group of a wavefront's 64 columns; only
+// that wavefront reads them, into registers half by half, so one slot is enough and no
+// barrier guards it.  Every byte arrives by buffer_load ... lds.  One barrier a stage:
+// it follows the stage's last fragment read, so the slot that the loads of the stage
+// after next go to (issued in the next stage) is free.
 template <int FC, int U>
 __global__ __launch_bounds__(256, 2) void gemm_i4_tile_kernel(I4Args args, int NT) {
-  constexpr int BM = 128, BN = 256, FM = BM / 16;
+  constexpr int BM = 128, BN = 256, FM = BM / 32, SUB = 2 * FM;   // a step: two halves of 16 k, FM fragments each
   constexpr int A_BYTES = BM * 128, BW = 4096 + U * 256;   // an A slot; a wavefront's part of B
   constexpr int B_AT = 3 * A_BYTES;
   constexpr int NA = A_BYTES / 4096, NBL = 4 + U;          // a wavefront's loads of a stage's A and of B
@@ -226,7 +249,7 @@ __global__ __launch_bounds__(256, 2) void gemm_i4_tile_kernel(I4Args args, int N
   __shared__ int sched[8];
   TileInfo ti;
   if (!decode_ragged_m<BM, 4, 32>(args.offsets, args.E, NT, sched, ti)) return;
-  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+  const int lane = threadIdx.x & 63, kg = lane >> 5, r = lane & 31;
   const int w = uniform((int)threadIdx.x >> 6);
   const int e = uniform(ti.e), row0 = uniform(ti.row0), rows = uniform(ti.rows);
   const int n0 = uniform(ti.n0) * BN;
@@ -275,53 +298,56 @@ __global__ __launch_bounds__(256, 2) void gemm_i4_tile_kernel(I4Args args, int N
     dma4(src(bs_src, live), lane4, (uint32_t)((live ? P : 0) * U + u) * 256u, b_dst + (uint32_t)(4096 + u * 256));
   };
 
-  // ---- fragments
+  // ---- fragments.  A: half m of 16 k of the stage's four, fragment i of 32 rows
   const uint32_t sw = (uint32_t)(r >> 1) & 7u;
-  const uint32_t a_half[2] = {(uint32_t)r * 128u + (((uint32_t)g ^ sw) << 4),
-                              (uint32_t)r * 128u + (((uint32_t)(4 + g) ^ sw) << 4)};
-  auto ld16 = [&](const char* p) __attribute__((always_inline)) -> i32x4_t {
-    return *(const __attribute__((address_space(3))) i32x4_t*)p;
+  uint32_t a_at[4];
+#pragma unroll
+  for (int m = 0; m < 4; ++m) a_at[m] = (uint32_t)r * 128u + (((uint32_t)(2 * m + kg) ^ sw) << 4);
+  auto read_a = [&](int slot, auto M, int i) __attribute__((always_inline)) -> bf16x8_t {
+    return *(const __attribute__((address_space(3))) bf16x8_t*)(lds + (uint32_t)slot * A_BYTES + a_at[decltype(M)::value] +
+                                                                 i * 4096);
   };
-  auto read_a = [&](int slot, auto H, int i) __attribute__((always_inline)) -> bf16x8_t {
-    constexpr int h = decltype(H)::value;
-    return __builtin_bit_cast(bf16x8_t, ld16(lds + (uint32_t)slot * A_BYTES + a_half[h] + i * 2048));
-  };
-  // 64 k of the wavefront's weights as stored: half HB of the slot's 128 k, and the
-  // scale words of the groups that start there
+  // B: 64 k of the wavefront's weights as stored: half HB of the slot's 128 k, and the
+  // scale words of the groups that start there.  Fragment F has the 16-column tiles 2 F
+  // and 2 F + 1 (lane bit 4); the k of a lane's half m lie in row group 2 m + kg of them.
   constexpr int UH = U == 4 ? 2 : 1;
-  i32x2_t raw[4];
-  i32x4_t words[UH];
+  i32x2_t raw[2][2];
+  uint32_t words[UH][2];
+  const char* const b_codes = lds + B_AT + w * BW + ((lane >> 4) & 1) * 1024 + (16 * kg + (lane & 15)) * 16;
+  const char* const b_words = lds + B_AT + w * BW + 4096 + (lane & 15) * 16 + ((lane >> 4) & 1) * 4;
   auto read_b = [&](auto HB) __attribute__((always_inline)) {
     constexpr int hb = decltype(HB)::value;
-    const char* b = lds + B_AT + w * BW;
     if constexpr (hb == 0 || U > 1)
-      static_for<0, UH>([&](auto I) __attribute__((always_inline)) {
-        words[I.value] = ld16(b + 4096 + (hb * (U / 2) + I.value) * 256 + r * 16);
+      static_for<0, 2 * UH>([&](auto I) __attribute__((always_inline)) {
+        constexpr int u = I.value / 2, f = I.value % 2;
+        words[u][f] = *(const __attribute__((address_space(3))) uint32_t*)(b_words + (hb * (U / 2) + u) * 256 + f * 8);
       });
     static_for<0, 4>([&](auto J) __attribute__((always_inline)) {
-      raw[J.value] = *(const __attribute__((address_space(3))) i32x2_t*)(b + J.value * 1024 + lane * 16 + hb * 8);
+      constexpr int f = J.value / 2, m = J.value % 2;
+      raw[f][m] = *(const __attribute__((address_space(3))) i32x2_t*)(b_codes + f * 2048 + m * 512 + hb * 8);
     });
   };
-  float sc[4], nz[4];
-  u32x4_t wd[2][4];                             // decoded fragments of this step and the next
-  // half `H` (4 of 8 k) of fragment J of step S
-  auto decode = [&](auto S, auto J, auto H) __attribute__((always_inline)) {
-    constexpr int s = decltype(S)::value, j = decltype(J)::value, h = decltype(H)::value;
-    if constexpr (h == 0 && s * U % 4 == 0) i4::unpack((uint32_t)words[U == 4 ? s & 1 : 0][j], sc[j], nz[j]);
-    const uint32_t t = (uint32_t)raw[j][s & 1];
+  float sc[2], nz[2];
+  u32x4_t wd[2][2][2];                          // decoded: [step & 1][half][fragment]
+  // piece X (of 8: fragment, half, 4 of a lane's 8 k) of step S
+  auto decode = [&](auto S, auto X) __attribute__((always_inline)) {
+    constexpr int s = decltype(S)::value, x = decltype(X)::value;
+    constexpr int f = x >> 2, m = (x >> 1) & 1, p = x & 1;
+    if constexpr ((x & 3) == 0 && s * U % 4 == 0) i4::unpack(words[U == 4 ? s & 1 : 0][f], sc[f], nz[f]);
+    const uint32_t t = (uint32_t)raw[f][m][s & 1];
     float v[4];
-    i4::values4((h ? t >> 4 : t) & 0x0f0f0f0fu, sc[j], nz[j], v);
-    uint32_t x = pack_bf16x2(v[0], v[1]), y = pack_bf16x2(v[2], v[3]);
-    asm volatile("" : "+v"(x), "+v"(y));        // decoded here, between these products
-    wd[s & 1][j][2 * h] = x;
-    wd[s & 1][j][2 * h + 1] = y;
+    i4::values4((p ? t >> 4 : t) & 0x0f0f0f0fu, sc[f], nz[f], v);
+    uint32_t a = pack_bf16x2(v[0], v[1]), b = pack_bf16x2(v[2], v[3]);
+    asm volatile("" : "+v"(a), "+v"(b));        // decoded here, between these products
+    wd[s & 1][m][f][2 * p] = a;
+    wd[s & 1][m][f][2 * p + 1] = b;
   };
 
-  f32x4_t acc[FM][4];
+  f32x16_t acc[FM][2];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int f = 0; f < 2; ++f) acc[i][f] = f32x16_t{};
   static_for<0, 4>([&](auto J) __attribute__((always_inline)) { issue_b(0, J.value); });
   static_for<0, U>([&](auto I) __attribute__((always_inline)) { issue_bs(0, I.value); });
   static_for<0, 2>([&](auto S) __attribute__((always_inline)) {
@@ -330,15 +356,12 @@ __global__ __launch_bounds__(256, 2) void gemm_i4_tile_kernel(I4Args args, int N
   wait_vmcnt<NA>();
   block_barrier();
   read_b(IntC<0>{});
-  static_for<0, 4>([&](auto J) __attribute__((always_inline)) {
-    decode(IntC<0>{}, J, IntC<0>{});
-    decode(IntC<0>{}, J, IntC<1>{});
-  });
-  bf16x8_t xf[4];                               // A fragments in flight: i & 3
+  static_for<0, 8>([&](auto X) __attribute__((always_inline)) { decode(IntC<0>{}, X); });
+  bf16x8_t xf[4];                               // A fragments in flight
   int slot = 0;                                 // of the current stage
   xf[0] = read_a(0, IntC<0>{}, 0);
   xf[1] = read_a(0, IntC<0>{}, 1);
-  const int nfr = min(FM, (rows + 15) >> 4);    // fragments with rows
+  const int nfr = min(FM, (rows + 31) >> 5);    // fragments with rows
 
   // Step S (of 4) of the 128 k P: 32 k, half S & 1 of stage 2 P + S / 2.
   auto step = [&](int P, auto S, auto SKIP) __attribute__((always_inline)) {
@@ -346,48 +369,45 @@ __global__ __launch_bounds__(256, 2) void gemm_i4_tile_kernel(I4Args args, int N
     constexpr bool skip = decltype(SKIP)::value;
     const int kt = 2 * P + (s >> 1);
     const int next = slot == 2 ? 0 : slot + 1, after = next == 2 ? 0 : next + 1;
-    static_for<0, FM>([&](auto I) __attribute__((always_inline)) {
-      constexpr int i = I.value;
+    static_for<0, SUB>([&](auto I) __attribute__((always_inline)) {
+      constexpr int x = I.value, m = x / FM, i = x % FM;
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (h == 0 && i >= 1 && i <= NA) issue_a(kt + 2, after, i - 1);
+      if constexpr (h == 0 && x >= 1 && x <= NA) issue_a(kt + 2, after, x - 1);
       // the second half of B's slot, then (its reads are in registers: products waited
       // for fragments read after them) the next 128 k into it
-      if constexpr (s == 1 && i == 0) read_b(IntC<1>{});
-      if constexpr (s == 1 && i == 3)
+      if constexpr (s == 1 && x == 0) read_b(IntC<1>{});
+      if constexpr (s == 1 && x == 3)
         static_for<0, U>([&](auto Q) __attribute__((always_inline)) { issue_bs(P + 1, Q.value); });
-      if constexpr (s == 1 && i >= 3 && i <= 5) issue_b(P + 1, i - 3);
-      if constexpr (s == 1 && i == 5) issue_b(P + 1, 3);
-      if constexpr (s == 3 && i == 0) {
+      if constexpr (s == 1 && x >= 3 && x <= 5) issue_b(P + 1, x - 3);
+      if constexpr (s == 1 && x == 5) issue_b(P + 1, 3);
+      if constexpr (s == 3 && x == 0) {
         // the next 128 k of B have landed (and A's next stage, older): newer are this stage's A loads
         wait_vmcnt<NA>();
         asm volatile("" ::: "memory");
         read_b(IntC<0>{});
       }
-      if constexpr (i + 2 < FM) {
-        if (!skip || i + 2 < nfr) xf[(i + 2) & 3] = read_a(slot, IntC<h>{}, i + 2);
-      } else if constexpr (h == 0) {
-        xf[(i + 2) & 3] = read_a(slot, IntC<1>{}, i + 2 - FM);
-      } else {
-        xf[(i + 2) & 3] = read_a(next, IntC<0>{}, i + 2 - FM);
-      }
+      constexpr int y = x + 2, yi = y % FM;     // the fragment read ahead: of the stage's 4 FM, or the next one's
+      constexpr int ym = (2 * h + y / FM) % 4;
+      if constexpr (h == 1 && y >= SUB) xf[y & 3] = read_a(next, IntC<ym>{}, yi);
+      else if (!skip || yi < nfr) xf[y & 3] = read_a(slot, IntC<ym>{}, yi);
       __builtin_amdgcn_sched_barrier(0);
       if (!skip || i < nfr) {
-        static_for<0, 4>([&](auto J) __attribute__((always_inline)) {
-          acc[i][J.value] = mma(__builtin_bit_cast(bf16x8_t, wd[h][J.value]), xf[i & 3], acc[i][J.value]);
+        static_for<0, 2>([&](auto F) __attribute__((always_inline)) {
+          acc[i][F.value] = mma32(wd[h][m][F.value], xf[x & 3], acc[i][F.value]);
         });
       }
-      // the next step's weights, half a fragment at a time (those that come out of the
-      // reads above one place later)
+      // the next step's weights, a piece at a time (those that come out of the reads
+      // above one place later)
       constexpr IntC<(s + 1) & 3> SN{};
       if constexpr (h == 0) {
-        decode(SN, IntC<i / 2>{}, IntC<i & 1>{});
+        decode(SN, I);
       } else {
-        if constexpr (i == 1) decode(SN, IntC<0>{}, IntC<0>{});
-        if constexpr (i >= 1) decode(SN, IntC<i / 2>{}, IntC<i & 1>{});
+        if constexpr (x == 1) decode(SN, IntC<0>{});
+        if constexpr (x >= 1) decode(SN, I);
       }
-      stay(acc[i]);
+      stay32(acc[i]);
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (h == 1 && i == FM - 3) {
+      if constexpr (h == 1 && x == SUB - 3) {
         __builtin_amdgcn_s_waitcnt(0xc07f);     // lgkmcnt(0): this stage's reads are in registers
         // the next stage has landed: newer are the stage after next and, first stage, B
         if constexpr (s == 1) wait_vmcnt<NA + NBL>();
@@ -407,10 +427,29 @@ __global__ __launch_bounds__(256, 2) void gemm_i4_tile_kernel(I4Args args, int N
   if (col >= N) return;
   static_for<0, FM>([&](auto I) __attribute__((always_inline)) {
     constexpr int i = I.value;
-    const int m = 16 * i + r;
+    const int m = 32 * i + r;
     const size_t row = (size_t)(row0 + m);
-    if constexpr (FC == 1) store_h(acc[i], m < rows, row, col >> 1, args.f, lane, args.h);
-    else store_o(acc[i], m < rows, row, col, args.d, lane, args.o);
+    static_for<0, 2>([&](auto F) __attribute__((always_inline)) {
+      constexpr int f = F.value;
+      const f32x4_t q0 = quad<0>(acc[i][f]), q1 = quad<1>(acc[i][f]), q2 = quad<2>(acc[i][f]), q3 = quad<3>(acc[i][f]);
+      if constexpr (FC == 1) {                  // columns 0..15 of W1 and the same of W3
+        f32x4_t h0, h1;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          h0[q] = silu_f32(q0[q]) * q2[q];
+          h1[q] = silu_f32(q1[q]) * q3[q];
+        }
+        const u32x4_t v = pair32(h0, h1);
+        if (m < rows) *(u32x4_t*)(args.h + row * (size_t)args.f + (col >> 1) + 16 * f + 8 * kg) = v;
+      } else {
+        const u32x4_t v0 = pair32(q0, q1), v1 = pair32(q2, q3);
+        bf16_t* p = args.o + row * (size_t)args.d + col + 32 * f + 8 * kg;
+        if (m < rows) {
+          *(u32x4_t*)p = v0;
+          *(u32x4_t*)(p + 16) = v1;
+        }
+      }
+    });
   });
 }
 
