@@ -25,68 +25,116 @@ __device__ __forceinline__ f32x4_t mma(const bf16x8_t& w, const bf16x8_t& x, con
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x, c, 0, 0, 0);
 }
 
-// Epilogue of fc1 for one 16-row fragment: acc = [a0 b0 a1 b1] (16 columns of f each;
-// lane l: row l & 15, columns 4 (l >> 4)..+3) -> h of the 32 columns from col on.
-__device__ __forceinline__ void store_h(const f32x4_t (&acc)[4], bool ok, size_t row, int col, int f, int lane,
+// Epilogue of fc1 for one 16-row fragment: acc = [a0 b0 ..] (16 columns of f each; lane
+// l: row l & 15, columns 4 (l >> 4)..+3) -> h of the 8 CF columns from col on.
+template <int CF>
+__device__ __forceinline__ void store_h(const f32x4_t (&acc)[CF], bool ok, size_t row, int col, int f, int lane,
                                         bf16_t* h) {
-  f32x4_t h0, h1;
+  f32x4_t v[CF / 2];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    h0[q] = silu_f32(acc[0][q]) * acc[1][q];
-    h1[q] = silu_f32(acc[2][q]) * acc[3][q];
+  for (int i = 0; i < CF / 2; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[i][q] = silu_f32(acc[2 * i][q]) * acc[2 * i + 1][q];
+  bf16_t* p = h + row * (size_t)f + col;
+  if constexpr (CF == 4) {
+    const u32x4_t x = pair_bf16(v[0], v[1]);
+    if (ok) *(u32x4_t*)(p + ((lane >> 4) & 1) * 16 + (lane >> 5) * 8) = x;
+  } else {
+    if (ok) *(uint2*)(p + (lane >> 4) * 4) = make_uint2(pack_bf16x2(v[0][0], v[0][1]), pack_bf16x2(v[0][2], v[0][3]));
   }
-  const int pc = ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
-  const u32x4_t v = pair_bf16(h0, h1);
-  if (ok) *(u32x4_t*)(h + row * (size_t)f + col + pc) = v;
 }
 
-// Epilogue of fc2 for one 16-row fragment: 64 columns from col on.
-__device__ __forceinline__ void store_o(const f32x4_t (&acc)[4], bool ok, size_t row, int col, int d, int lane,
+// Epilogue of fc2 for one 16-row fragment: 16 CF columns from col on.
+template <int CF>
+__device__ __forceinline__ void store_o(const f32x4_t (&acc)[CF], bool ok, size_t row, int col, int d, int lane,
                                         bf16_t* o) {
-  const int pc = ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
-  const u32x4_t v0 = pair_bf16(acc[0], acc[1]), v1 = pair_bf16(acc[2], acc[3]);
-  if (!ok) return;
-  bf16_t* p = o + row * (size_t)d + col + pc;
-  *(u32x4_t*)p = v0;
-  *(u32x4_t*)(p + 32) = v1;
+  bf16_t* p = o + row * (size_t)d + col + ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
+#pragma unroll
+  for (int i = 0; i < CF / 2; ++i) {
+    const u32x4_t v = pair_bf16(acc[2 * i], acc[2 * i + 1]);
+    if (ok) *(u32x4_t*)(p + 32 * i) = v;
+  }
 }
 
-// Few rows: a block of NW wavefronts takes 64 stored columns of one expert and up to
+// 16 bytes a lane at byte offset voff + soff (soff uniform); zeros past the end.
+__device__ __forceinline__ i32x4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {
+  return __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0));
+}
+// The same for what is read once (non-temporal).
+__device__ __forceinline__ i32x4_t load16_once(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {
+  return __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 2));
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, uint32_t bytes) {
+  const uint64_t a = (uint64_t)p;
+  const uint32_t lo = (uint32_t)uniform((int)(uint32_t)a), hi = (uint32_t)uniform((int)(uint32_t)(a >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc((void*)((uint64_t)hi << 32 | lo), 0, (int)bytes, 0x00020000);
+}
+
+// A lane's scale words of CF 16-column groups.
+template <int CF>
+struct Words {
+  typedef i32x4_t type;
+  static __device__ __forceinline__ type load(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {
+    return load16(r, voff, soff);
+  }
+};
+template <>
+struct Words<2> {
+  typedef i32x2_t type;
+  static __device__ __forceinline__ type load(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {
+    return __builtin_bit_cast(i32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, voff, soff, 0));
+  }
+};
+
+// Few rows: a block of NW wavefronts takes CF 16-column groups of one expert and up to
 // 32 of its rows; the wavefronts split K (wavefront w takes the 128-row steps w,
 // w + NW, ...) and their partial sums meet in LDS, added in wavefront order.  Blocks
 // take the pieces of 32 rows that the experts have, in order, so a call with few rows
 // launches few blocks.  U: groups of a 128-row step.
-constexpr int NW = 4;
-template <int FC, int U>
-__global__ __launch_bounds__(NW * 64) void gemm_i4_rows_kernel(I4Args args) {
-  __shared__ f32x4_t part[2][NW][4][64];
+//
+// With up to 16 rows a step's operands are on their way while the step before it is
+// decoded and multiplied (23 tokens of 8 of 128 experts, d 4096, f 1536: 212 -> 197
+// us), and registers are kept to four wavefronts a SIMD (groups of 128: 197 -> 182 us)
+// or three.  Reading the weights and decoding them take turns as the bound: without
+// the decoding (19 instructions for 8 weights, 65 cycles of a SIMD for a wavefront's)
+// the same call takes 152 us, 6.6 TB/s, with it 5.5; 177 tokens, groups of 64, 241 us
+// against 274, 5.0 TB/s, of which reading x from L2 costs 14.
+template <int FC, int U, int NW, int CF>
+__global__ __launch_bounds__(NW * 64, U == 1 || NW == 16 ? 4 : 3) void gemm_i4_rows_kernel(I4Args args) {
+  __shared__ f32x4_t part[2][NW][CF][64];
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int w = uniform((int)threadIdx.x >> 6);
   const int K = FC == 1 ? args.d : args.f, N = FC == 1 ? 2 * args.f : args.d;
-  const int KT = K >> 7, NB = N >> 6;
+  const int KT = K >> 7, NB = N / (16 * CF);
   const int nb = (int)blockIdx.x % NB;
   // the piece: the (blockIdx / NB)-th of the experts' pieces of 32 rows, in order
   int e = -1, row0 = 0, rows = 0;
   {
     int want = (int)blockIdx.x / NB;
-    for (int base = 0; base < args.E; base += 64) {
-      const int x = base + lane;
-      const int o0 = x < args.E ? args.offsets[x] : 0, o1 = x < args.E ? args.offsets[x + 1] : 0;
-      const int n = (o1 - o0 + 31) >> 5;
+    int o0[4], o1[4];
+    const __amdgpu_buffer_rsrc_t ob = buffer(args.offsets, 4u * (uint32_t)args.E + 4u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // (at most 256 experts; every load before the first use)
+      o0[i] = (int)__builtin_amdgcn_raw_buffer_load_b32(ob, (uint32_t)(64 * i + lane) * 4u, 0, 0);
+      o1[i] = (int)__builtin_amdgcn_raw_buffer_load_b32(ob, (uint32_t)(64 * i + lane) * 4u + 4u, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (e >= 0 || 64 * i >= args.E) break;
+      const int n = 64 * i + lane < args.E ? (o1[i] - o0[i] + 31) >> 5 : 0;
       int end = n;  // pieces of this expert and of those before it
 #pragma unroll
-      for (int i = 1; i < 64; i *= 2) {
-        const int v = __shfl_up(end, i, 64);
-        end += lane >= i ? v : 0;
+      for (int k = 1; k < 64; k *= 2) {
+        const int v = __shfl_up(end, k, 64);
+        end += lane >= k ? v : 0;
       }
       const uint64_t past = __ballot(end > want);
       if (past) {
         const int at = __builtin_ctzll(past);
         const int first = 32 * (want - __shfl(end - n, at, 64));
-        e = base + at;
-        row0 = __shfl(o0, at, 64) + first;
-        rows = min(__shfl(o1, at, 64) - row0, 32);
-        break;
+        e = 64 * i + at;
+        row0 = __shfl(o0[i], at, 64) + first;
+        rows = min(__shfl(o1[i], at, 64) - row0, 32);
       }
       want -= __shfl(end, 63, 64);
     }
@@ -95,84 +143,97 @@ __global__ __launch_bounds__(NW * 64) void gemm_i4_rows_kernel(I4Args args) {
   if (e < 0) return;
   row0 = uniform(row0);
   rows = uniform(rows);
-  const uint8_t* wt = args.w + ((size_t)e * (N >> 4) + (size_t)nb * 4) * KT * 1024 + lane * 16;
-  const uint32_t* wst = args.ws + (((size_t)e * NB + nb) * KT * U) * 64 + r * 4;
-  const size_t wstride = (size_t)KT * 1024;  // from one 16-column group to the next
-  // the rows as MT fragments of 16, UF steps' loads of a wavefront in flight together
-  auto run = [&](auto MTC, auto UFC) __attribute__((always_inline)) {
-    constexpr int MT = decltype(MTC)::value, UF = decltype(UFC)::value;
-    const bf16_t* at[MT];
-    bool known[MT], all_known = true;
+  const __amdgpu_buffer_rsrc_t wb = buffer(args.w + ((size_t)e * (N >> 4) + (size_t)nb * CF) * KT * 1024, 1024u * CF * (uint32_t)KT);
+  const __amdgpu_buffer_rsrc_t sb = buffer(args.ws + ((size_t)e * (N >> 6) + nb * CF / 4) * KT * (U * 64), 256u * U * (uint32_t)KT);
+  const bool gather = FC == 1 && args.token_of != nullptr;
+  const uint32_t a_rows = (uint32_t)(gather ? args.T : args.P), a_ld = (uint32_t)K * 2u;
+  const __amdgpu_buffer_rsrc_t ab = buffer(args.a, a_rows * a_ld);
+  const uint32_t lane16 = (uint32_t)lane * 16u, r16 = (uint32_t)r * 16u + (CF == 2 ? (uint32_t)(nb & 1) * 8u : 0u);
+  const uint32_t wstride = (uint32_t)KT * 1024u;  // from one 16-column group to the next
+  // the rows as MT fragments of 16
+  auto run = [&](auto MTC) __attribute__((always_inline)) {
+    constexpr int MT = decltype(MTC)::value;
+    f32x4_t acc[MT][CF];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int j = 0; j < CF; ++j) acc[t][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    struct Step {
+      i32x4_t wf[CF], xf[MT][4];
+      typename Words<CF>::type sw[U];
+    };
+    auto load_w = [&](Step& o, int kt) __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < CF; ++j) o.wf[j] = load16_once(wb, lane16, (uint32_t)j * wstride + (uint32_t)kt * 1024u);
+#pragma unroll
+      for (int i = 0; i < U; ++i) o.sw[i] = Words<CF>::load(sb, r16, (uint32_t)(kt * U + i) * 256u);
+    };
+    // the first weights are on their way while the rows' token ids arrive
+    uint32_t ids[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) ids[t] = gather ? (uint32_t)args.token_of[row0 + min(16 * t + r, rows - 1)] : 0u;
+    Step a, b;
+    load_w(a, min(w, KT - 1));
+    // rows past the last read as zero, and so does a token that there is not
+    uint32_t at[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      // rows past the last are read as the last one and not stored; a token that
-      // there is not counts as a row of zeros (not its results: 0 times a NaN is NaN)
-      const int pr = row0 + min(16 * t + r, rows - 1);
-      size_t ar = (size_t)pr;
-      known[t] = true;
-      if (FC == 1 && args.token_of) {
-        const uint32_t token = (uint32_t)args.token_of[pr];
-        known[t] = token < (uint32_t)args.T;
-        ar = known[t] ? token : 0;
-        all_known = all_known && known[t];
-      }
-      at[t] = args.a + ar * (size_t)K + g * 8;
+      const int m = 16 * t + r;
+      const uint32_t row = gather ? ids[t] : (uint32_t)(row0 + min(m, rows - 1));
+      at[t] = m < rows && row < a_rows ? row * a_ld + (uint32_t)g * 16u : 0x80000000u;
     }
-    all_known = __all(all_known);
-    f32x4_t acc[MT][4];
+    auto load_x = [&](Step& o, int kt) __attribute__((always_inline)) {
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+      for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[t][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int k0 = w; k0 < KT; k0 += NW * UF) {
-      i32x4_t wf[UF][4], sw[UF][U], xf[UF][MT][4];
+        for (int j = 0; j < 4; ++j) o.xf[t][j] = load16(ab, at[t] + (uint32_t)j * 64u, (uint32_t)kt * 256u);
+    };
+    auto load = [&](Step& o, int kt) __attribute__((always_inline)) {
+      load_w(o, kt);
+      load_x(o, kt);
+    };
+    auto multiply = [&](const Step& o) __attribute__((always_inline)) {
 #pragma unroll
-      for (int u = 0; u < UF; ++u) {
-        const int kt = k0 + NW * u;
-        if (kt < KT) {
+      for (int c = 0; c < CF; ++c) {
+        float s = 0.f, nzs = 0.f;
+        __builtin_amdgcn_sched_barrier(0);  // one column group's decoded weights at a time
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            wf[u][j] = __builtin_nontemporal_load((const i32x4_t*)(wt + j * wstride + (size_t)kt * 1024));
+        for (int j = 0; j < 4; ++j) {
+          if (j * U % 4 == 0) i4::unpack((uint32_t)o.sw[j * U / 4][c], s, nzs);
+          const bf16x8_t wv = i4::operand((uint32_t)o.wf[c][j], s, nzs);
 #pragma unroll
-          for (int i = 0; i < U; ++i) sw[u][i] = *(const i32x4_t*)(wst + ((size_t)kt * U + i) * 64);
-#pragma unroll
-          for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) xf[u][t][j] = *(const i32x4_t*)(at[t] + (size_t)kt * 128 + j * 32);
+          for (int t = 0; t < MT; ++t) acc[t][c] = mma(wv, __builtin_bit_cast(bf16x8_t, o.xf[t][j]), acc[t][c]);
         }
       }
-#pragma unroll
-      for (int u = 0; u < UF; ++u) {
-        if (k0 + NW * u < KT) {
-          if (!all_known) {
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) xf[u][t][j] = known[t] ? xf[u][t][j] : i32x4_t{0, 0, 0, 0};
-          }
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float s = 0.f, nzs = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (j * U % 4 == 0) i4::unpack((uint32_t)sw[u][j * U / 4][c], s, nzs);
-              const bf16x8_t wv = i4::operand((uint32_t)wf[u][c][j], s, nzs);
-#pragma unroll
-              for (int t = 0; t < MT; ++t) acc[t][c] = mma(wv, __builtin_bit_cast(bf16x8_t, xf[u][t][j]), acc[t][c]);
-            }
-          }
+    };
+    if (w < KT) {
+      load_x(a, w);
+      if constexpr (MT == 1) {
+        for (int kt = w;; kt += 2 * NW) {
+          if (kt + NW < KT) load(b, kt + NW);
+          multiply(a);
+          if (kt + NW >= KT) break;
+          if (kt + 2 * NW < KT) load(a, kt + 2 * NW);
+          multiply(b);
+          if (kt + 2 * NW >= KT) break;
+        }
+      } else {
+        for (int kt = w;;) {
+          multiply(a);
+          if ((kt += NW) >= KT) break;
+          load(a, kt);
         }
       }
     }
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) part[t][w][j][lane] = acc[t][j];
+      for (int j = 0; j < CF; ++j) part[t][w][j][lane] = acc[t][j];
     __syncthreads();
     if (w >= MT) return;  // wavefront t stores rows 16 t ..
-    f32x4_t sum[4];
+    f32x4_t sum[CF];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < CF; ++j) {
       f32x4_t s = part[w][0][j][lane];
 #pragma unroll
       for (int i = 1; i < NW; ++i) {
@@ -184,20 +245,20 @@ __global__ __launch_bounds__(NW * 64) void gemm_i4_rows_kernel(I4Args args) {
     }
     const int m = 16 * w + r;
     const size_t row = (size_t)(row0 + m);
-    if constexpr (FC == 1) store_h(sum, m < rows, row, nb * 32, args.f, lane, args.h);
-    else store_o(sum, m < rows, row, nb * 64, args.d, lane, args.o);
+    if constexpr (FC == 1) store_h<CF>(sum, m < rows, row, nb * CF * 8, args.f, lane, args.h);
+    else store_o<CF>(sum, m < rows, row, nb * CF * 16, args.d, lane, args.o);
   };
-  if (rows <= 16) run(IntC<1>{}, IntC<2>{});
-  else run(IntC<2>{}, IntC<1>{});
+  if (rows <= 16) run(IntC<1>{});
+  else run(IntC<2>{});
 }
 
-template <int FC, int U>
+template <int FC, int U, int NW, int CF>
 int launch_rows(const I4Args& a, hipStream_t s) {
-  const int64_t NB = (FC == 1 ? 2 * (int64_t)a.f : (int64_t)a.d) / 64;
+  const int64_t NB = (FC == 1 ? 2 * (int64_t)a.f : (int64_t)a.d) / (16 * CF);
   // at most sum_e ceil(m_e / 32) pieces, P with fewer rows than experts
   const int64_t grid = NB * (a.P / 32 + (a.P < a.E ? a.P : a.E));
   if (!launch_fits(grid, NW * 64)) return MOE_ERR_UNSUPPORTED;
-  gemm_i4_rows_kernel<FC, U><<<(unsigned)grid, NW * 64, 0, s>>>(a);
+  gemm_i4_rows_kernel<FC, U, NW, CF><<<(unsigned)grid, NW * 64, 0, s>>>(a);
   TRE_LAUNCH_CHECK();
   return MOE_OK;
 }
@@ -464,9 +525,18 @@ int launch_tiles(const I4Args& a, hipStream_t s) {
   return MOE_OK;
 }
 
+// The blocks of the rows kernel: 64 columns and four wavefronts each where there are
+// four of them for each of 256 compute units, else 32 columns, and eight wavefronts
+// where those would be one to a compute unit.  64 columns, 32 columns, 32 columns with
+// eight wavefronts, us, by the number of the first: 384 (8 experts, K 4096) 18.0,
+// 15.6, 16.6; 896 (2 experts, K 4096) 29.2, 26.6, 30.6; 1024 (16, K 1536) 13.4, 15.0,
+// 19.5; 128 (2, K 14336) 30.9, 21.6, 16.7; 64 (4, K 1024) 5.6, 4.8, 4.6.
 template <int FC, int U>
 int launch(const I4Args& a, hipStream_t s) {
-  return gemm_i4_few_rows(a) ? launch_rows<FC, U>(a, s) : launch_tiles<FC, U>(a, s);
+  if (!gemm_i4_few_rows(a)) return launch_tiles<FC, U>(a, s);
+  const int64_t blocks = (FC == 1 ? 2 * (int64_t)a.f : (int64_t)a.d) / 64 * (a.P / 32 + (a.P < a.E ? a.P : a.E));
+  if (blocks >= 1024) return launch_rows<FC, U, 4, 4>(a, s);
+  return blocks > 128 ? launch_rows<FC, U, 4, 2>(a, s) : launch_rows<FC, U, 8, 2>(a, s);
 }
 template <int FC>
 int launch_fc(const I4Args& a, hipStream_t s) {
@@ -477,15 +547,25 @@ int launch_fc(const I4Args& a, hipStream_t s) {
 
 }  // namespace
 
-// Which kernel (the rule of the MXFP4 products).
+// Which kernel.  Both take a time that goes with K and with the rounds of blocks that
+// the chip runs at once: pieces of 32 rows x 64 columns, three to a compute unit, or
+// tiles of 128 x 256, two to one, of which a K step takes three times as long.  (An
+// expert has about 0.35 pieces or tiles more than its rows fill, and one at least.)
+// Both kernels, us, rows an expert:
+//   128 experts, d 4096, f 1536: 16 rows 288 against 373, 24: 343 / 373, 32: 453 / 398,
+//   64: 794 / 478; 8, d 4096, f 14336: 16 rows 187 / 352, 32: 278 / 360, 48: 386 / 369,
+//   64: 481 / 402; 8, d = f = 1024: 64 rows 22 / 39, 128: 28 / 35, 256: 40 / 36, 512:
+//   72 / 41; 4, d 384, f 2560: 400 rows 47 / 56; 32, d 2048, f 1408: 32 rows 71 / 73,
+//   64: 107 / 82.
 bool gemm_i4_few_rows(const I4Args& a) {
-  if ((int64_t)a.P <= 20 * (int64_t)a.E) return true;
-  const double pieces = a.P / 32.0 + 0.5 * (a.P < a.E ? a.P : a.E);
-  auto steps = [&](int64_t n, int64_t k) {
-    const double rounds = pieces * (double)(n / 64) / 512.0;
-    return (rounds > 1.0 ? rounds : 1.0) * (double)k;
+  const double experts = a.P < a.E ? a.P : a.E, each = a.P / experts;
+  auto steps = [&](double m, double n, double blocks, int64_t N, int64_t K) {
+    const double have = each / m + 0.35, rounds = experts * (have > 1.0 ? have : 1.0) * ((double)N / n) / blocks;
+    return (rounds > 1.0 ? rounds : 1.0) * (double)K;
   };
-  return steps(2 * (int64_t)a.f, a.d) + steps(a.d, a.f) <= 1.5 * ((double)a.d + (double)a.f);
+  const int64_t N1 = 2 * (int64_t)a.f;
+  return steps(32, 64, 768, N1, a.d) + steps(32, 64, 768, a.d, a.f) <=
+         3.0 * (steps(128, 256, 512, N1, a.d) + steps(128, 256, 512, a.d, a.f));
 }
 
 int gemm_i4_launch(int fc, const I4Args& a, hipStream_t s) {
