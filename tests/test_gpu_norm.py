@@ -67,7 +67,7 @@ def stream_rows(T, d, dtype, seed, special=True):
 
 
 SIZES = [(1, 8), (3, 40), (1, 4096), (5, 128), (7, 384), (177, 7168), (33, 8320), (2, 32768), (4096, 256), (4097, 1152),
-         (4099, 5120), (4096, 8192), (513, 2048), (4100, 16384 // 16)]
+         (4099, 5120), (4096, 8192), (513, 2048), (4100, 1024), (1024, 7168), (1025, 1536), (20000, 1024)]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])

@@ -51,6 +51,20 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
   *(f32x4_t*)p = f32x4_t{v[0], v[1], v[2], v[3]};
   *(f32x4_t*)(p + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
 }
+// The same past the caches, for what is too large for them.
+__device__ __forceinline__ void stream8(bf16_t* p, const float* v) {
+  __builtin_nontemporal_store((u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                       pack_bf16x2(v[6], v[7])}), (u32x4_t*)p);
+}
+__device__ __forceinline__ void stream8(float* p, const float* v) {
+  __builtin_nontemporal_store((f32x4_t{v[0], v[1], v[2], v[3]}), (f32x4_t*)p);
+  __builtin_nontemporal_store((f32x4_t{v[4], v[5], v[6], v[7]}), (f32x4_t*)(p + 4));
+}
+template <bool PAST, typename T>
+__device__ __forceinline__ void put8(T* p, const float* v) {
+  if constexpr (PAST) stream8(p, v);
+  else store8(p, v);
+}
 __device__ __forceinline__ float rounded(float v, bf16_t) { return bf16_to_f32(f32_to_bf16(v)); }
 __device__ __forceinline__ float rounded(float v, float) { return v; }
 
@@ -139,7 +153,7 @@ __device__ __forceinline__ void quant8(const float* v, bool ok, size_t at, uint8
 // lane l of wavefront w being number (i WPR + w) 64 + l of the row's d / 8.
 // x, residual, sum and y may be the same memory: a lane reads all its values of a
 // row before it writes any.
-template <typename T, int Q, int WPR, int NV>
+template <typename T, int Q, int WPR, int NV, bool PAST>
 __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_kernel(NormArgs a) {
   __shared__ float red[WPR];
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
@@ -165,17 +179,20 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_kernel(NormArg
       else rr[i].zero();
     }
   }
-  float v[NV][8], ss = 0.0f;
+  // Eight sums a lane, then a tree, and the root in 64 bits: an error of rstd moves a
+  // whole row's values over rounding borders of the codes (one sum and fp32: 1.6 times
+  // the error of the MXFP8 values of 7168 columns).
+  float v[NV][8], sq[8] = {};
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       v[i][q] = res ? rounded(xr[i].at(q) + rr[i].at(q), T{}) : xr[i].at(q);
-      ss = fmaf(v[i][q], v[i][q], ss);
+      sq[q] = fmaf(v[i][q], v[i][q], sq[q]);
     }
   }
-  ss = row_sum<WPR>(ss, w, red);
-  const float rstd = 1.0f / sqrtf(ss / (float)a.d + a.eps);
+  const float ss = row_sum<WPR>(((sq[0] + sq[1]) + (sq[2] + sq[3])) + ((sq[4] + sq[5]) + (sq[6] + sq[7])), w, red);
+  const float rstd = (float)(1.0 / sqrt((double)ss / (double)a.d + (double)a.eps));
   if (a.rstd && w == 0 && lane == 0) a.rstd[row] = rstd;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -185,10 +202,10 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_kernel(NormArg
     Raw<T> g;
     if (ok) g.load((const T*)a.gamma + (size_t)at * 8);
     else g.zero();
-    if (ok && a.sum) store8((T*)a.sum + (base + at) * 8, v[i]);
+    if (ok && a.sum) put8<PAST>((T*)a.sum + (base + at) * 8, v[i]);
 #pragma unroll
     for (int q = 0; q < 8; ++q) v[i][q] = v[i][q] * rstd * g.at(q);
-    if (ok && a.y) store8((T*)a.y + (base + at) * 8, v[i]);
+    if (ok && a.y) put8<PAST>((T*)a.y + (base + at) * 8, v[i]);
     if constexpr (Q >= 0) quant8<Q>(v[i], ok, base + at, a.codes, a.scales);
   }
 }
@@ -303,7 +320,7 @@ __global__ __launch_bounds__(1024) void norm_dgamma_kernel(const float* __restri
 }
 
 // The values that rows of codes stand for: a thread takes eight.
-template <int Q, typename T>
+template <int Q, typename T, bool PAST>
 __global__ __launch_bounds__(256) void dequant_rows_kernel(const uint8_t* __restrict__ codes,
                                                            const void* __restrict__ scales, int64_t nvec,
                                                            T* __restrict__ dst) {
@@ -327,28 +344,33 @@ __global__ __launch_bounds__(256) void dequant_rows_kernel(const uint8_t* __rest
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = p[i >> 1][i & 1] * s;
   }
-  store8(dst + at * 8, v);
+  put8<PAST>(dst + at * 8, v);
 }
 
-template <typename T, int Q, int WPR, int NV>
+template <typename T, int Q, int WPR, int NV, bool PAST = false>
 int fwd_as(const NormArgs& a, hipStream_t s) {
   const int64_t grid = WPR == 1 ? (a.T + 3) / 4 : a.T;
   if (!launch_fits(grid, WPR == 1 ? 256 : 64 * WPR)) return MOE_ERR_UNSUPPORTED;
-  norm_kernel<T, Q, WPR, NV><<<(unsigned)grid, WPR == 1 ? 256 : 64 * WPR, 0, s>>>(a);
+  norm_kernel<T, Q, WPR, NV, PAST><<<(unsigned)grid, WPR == 1 ? 256 : 64 * WPR, 0, s>>>(a);
   TRE_LAUNCH_CHECK();
   return MOE_OK;
 }
 template <typename T, int Q>
 int fwd_of(const NormArgs& a, hipStream_t s) {
+  // Wavefronts to a row: one where it has no more than 1024 values, else four (one,
+  // 16384 rows of 7168: 214 us against 187; 8200 of 4096, fp32: 123 against 111), and
+  // sixteen where there are too few rows for the chip (177 of 7168: 5.4 us against 7.2)
+  // or a row is longer than four hold.
+  // sum and y of 32 MB and more, all L2s together, are written past the caches: 5000
+  // rows of 4096 36.0 us against 28.1, 4096 of 7168 56 / 46, 40000 of 512 34.8 / 28.2.
+  // (The codes, which the layer reads next, are not: it would cost their reader more
+  // than it saves here.)
   const int nvec = a.d / 8;
-  if (a.T >= 4096 && nvec <= 1024) {
-    if (nvec <= 128) return fwd_as<T, Q, 1, 2>(a, s);
-    if (nvec <= 512) return fwd_as<T, Q, 1, 8>(a, s);
-    return fwd_as<T, Q, 1, 16>(a, s);
-  }
-  if (nvec <= 256) return fwd_as<T, Q, 4, 1>(a, s);
-  if (nvec <= 1024) return fwd_as<T, Q, 4, 4>(a, s);
-  return fwd_as<T, Q, 16, 4>(a, s);
+  const bool past = a.T * a.d * (int64_t)sizeof(T) >= (int64_t)1 << 25;
+  if (nvec <= 128) return past ? fwd_as<T, Q, 1, 2, true>(a, s) : fwd_as<T, Q, 1, 2>(a, s);
+  if (nvec <= 512 && a.T >= 1024) return past ? fwd_as<T, Q, 4, 2, true>(a, s) : fwd_as<T, Q, 4, 2>(a, s);
+  if (nvec <= 1024 && a.T >= 1024) return past ? fwd_as<T, Q, 4, 4, true>(a, s) : fwd_as<T, Q, 4, 4>(a, s);
+  return nvec <= 1024 ? fwd_as<T, Q, 16, 1>(a, s) : fwd_as<T, Q, 16, 4>(a, s);
 }
 template <typename T>
 int fwd_type(const NormArgs& a, hipStream_t s) {
@@ -385,13 +407,17 @@ int bwd_of(const NormBwdArgs& a, void* dgamma, hipStream_t s) {
 template <int Q, typename T>
 int dequant_as(const uint8_t* codes, const void* scales, int64_t rows, int64_t cols, void* dst, hipStream_t s) {
   const int64_t nvec = rows * (cols / 8);
+  // values of 128 MB and more past the caches (16384 rows of 7168: 71 us against 65)
+  const bool past = nvec * 8 * (int64_t)sizeof(T) >= (int64_t)1 << 27;
   constexpr int64_t kPart = (int64_t)1 << 31;  // vectors a launch
   for (int64_t at = 0; at < nvec; at += kPart) {
     const int64_t n = nvec - at < kPart ? nvec - at : kPart;
     const void* sc = Q == MOE_E4M3 ? (const void*)((const float*)scales + at / 16)
                                    : (const void*)((const uint8_t*)scales + at / 4);
-    dequant_rows_kernel<Q, T><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(codes + at * (Q == MOE_MXFP4 ? 4 : 8), sc, n,
-                                                                          (T*)dst + at * 8);
+    const uint8_t* c = codes + at * (Q == MOE_MXFP4 ? 4 : 8);
+    const unsigned grid = (unsigned)((n + 255) / 256);
+    if (past) dequant_rows_kernel<Q, T, true><<<grid, 256, 0, s>>>(c, sc, n, (T*)dst + at * 8);
+    else dequant_rows_kernel<Q, T, false><<<grid, 256, 0, s>>>(c, sc, n, (T*)dst + at * 8);
     TRE_LAUNCH_CHECK();
   }
   return MOE_OK;
