@@ -140,3 +140,32 @@ def test_layer_refuses_before_enqueuing():
         setattr(io, n, 16)
     assert call(need - 1, shared) == WS
     assert call(need, make_shape(**OK_SHAPE, f_shared=200)) == UNS
+
+
+def test_gpu_cases_reach_every_kernel():
+    """The counts that the GPU tests use: few rows alone, many with the added expert, each form of the few-row kernel."""
+    import test_gpu_i4 as G
+    for name, counts in G.COUNTS.items():
+        d, f = G.WIDTHS.get(name, (256, 128))
+        assert G.few(sum(counts), len(counts), d, f)
+        many = G.with_many(counts, d, f)
+        assert not G.few(sum(many), len(many), d, f) and sum(many) < 40000
+    forms = {n: G.blocks(*c) for n, c in G.FORMS.items()}
+    assert all(G.few(sum(c[0]), len(c[0]), *c[1:]) for c in G.FORMS.values())
+    assert max(forms["eight"]) <= 128 < min(forms["four"]) and max(forms["four"]) < 1024 <= min(forms["wide"])
+
+
+def test_few_rows_rule():
+    """Where the two kernels take about as long (few experts: later), and shapes that are refused."""
+    def few(P, E, d, f, **kw):
+        return bool(N.lib().moe_few_rows(C.byref(make_shape(**{**dict(T=P, d=d, E=E, k=1, f=f, dtype="int4"), **kw}))))
+    assert few(20 * 128, 128, 4096, 1536) and not few(32 * 128, 128, 4096, 1536)
+    assert few(32 * 8, 8, 4096, 14336) and not few(64 * 8, 8, 4096, 14336)
+    assert few(128 * 8, 8, 1024, 1024) and not few(512 * 8, 8, 1024, 1024)
+    assert few(1, 8, 128, 128) and not few(1, 8, 200, 128)
+
+
+def test_launches_of_two_to_the_32_threads():
+    f = (1 << 24) - 128
+    sh = make_shape(32, 128, 256, 1, f, dtype="int4")
+    assert N.lib().moe_grouped_gemm_fwd_i4(C.byref(sh), P, None, P, C.byref(weights()), P, P, 1 << 40, None) == UNS

@@ -286,6 +286,25 @@ def test_product_widths(d, f, group, many):
     check(case, len(counts), 1, sum(counts), d, f)
 
 
+# (counts, d, f) whose two products take blocks of 32 columns with eight wavefronts, with four, and of 64 columns
+FORMS = {"eight": ([16, 3, 17], 128, 128), "four": ([7, 16, 0, 17, 32, 33, 1] * 4, 256, 384),
+         "wide": ([7, 16, 0, 17, 32, 33, 1] * 20, 1152, 1152)}
+
+
+def blocks(counts, d, f):
+    """Blocks of 64 columns that the two products of a call with few rows have at most."""
+    P, E = sum(counts), len(counts)
+    return [n // 64 * (P // 32 + min(P, E)) for n in (2 * f, d)]
+
+
+@pytest.mark.parametrize("group,asym", [(32, False), (64, True), (128, True)])
+@pytest.mark.parametrize("form", FORMS)
+def test_product_every_form_of_the_rows_kernel(form, group, asym):
+    counts, d, f = FORMS[form]
+    case = product_case(counts, d, f, group, asym, 7, True)
+    check(case, len(counts), 1, sum(counts), d, f)
+
+
 def test_rows_past_the_last_expert_stay():
     """offsets[E] below P (assignments that the map skipped)."""
     case = product_case([20, 0, 300], 256, 256, 64, True, 9, True, T=400)
