@@ -434,13 +434,20 @@ __global__ __launch_bounds__(256, 2) void gemm_i4_tile_kernel(I4Args args, int N
       constexpr int x = I.value, m = x / FM, i = x % FM;
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (h == 0 && x >= 1 && x <= NA) issue_a(kt + 2, after, x - 1);
-      // the second half of B's slot, then (its reads are in registers: products waited
-      // for fragments read after them) the next 128 k into it
+      // The second half of B's slot, then the next 128 k into it: its reads are in
+      // registers, as the last products waited for a fragment read after them (where
+      // products are skipped: an explicit wait).
       if constexpr (s == 1 && x == 0) read_b(IntC<1>{});
-      if constexpr (s == 1 && x == 3)
+      if constexpr (s == 1 && x == 4) {
+        if constexpr (skip) __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
         static_for<0, U>([&](auto Q) __attribute__((always_inline)) { issue_bs(P + 1, Q.value); });
-      if constexpr (s == 1 && x >= 3 && x <= 5) issue_b(P + 1, x - 3);
-      if constexpr (s == 1 && x == 5) issue_b(P + 1, 3);
+        issue_b(P + 1, 0);
+        issue_b(P + 1, 1);
+      }
+      if constexpr (s == 1 && x == 5) {
+        issue_b(P + 1, 2);
+        issue_b(P + 1, 3);
+      }
       if constexpr (s == 3 && x == 0) {
         // the next 128 k of B have landed (and A's next stage, older): newer are this stage's A loads
         wait_vmcnt<NA>();

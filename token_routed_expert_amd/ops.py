@@ -614,6 +614,8 @@ def moe_add_rms_norm(x, residual, gamma, eps, sum_, y, rstd, q_dtype=None, codes
     call = "moe_add_rms_norm"
     T, d = x.shape
     code, b, n, dt = _src_dtype(call, x), _Bufs(call), T * d, x.dtype
+    if T == 0:
+        return
     if q_dtype is None and (codes is not None or scales is not None):
         raise ValueError(f"{call}: codes and scales need q_dtype")
     q, c, sc = (0, None, None) if q_dtype is None else _q_rows(b, call, q_dtype, n, codes, scales)
@@ -629,6 +631,9 @@ def moe_add_rms_norm_bwd(dy, sum_, rstd, gamma, dsum, dx, dgamma, ws, stream=Non
     call = "moe_add_rms_norm_bwd"
     T, d = dy.shape
     code, b, n, dt = _src_dtype(call, dy), _Bufs(call), T * d, dy.dtype
+    if T == 0:  # (an empty tensor has no address; the call reads none of them)
+        dy = sum_ = dx = gamma
+        rstd, dsum = torch.empty(1, dtype=F32, device=gamma.device), None
     _check(N.lib().moe_add_rms_norm_bwd(
         b("dy", dy, dt, n), b("sum", sum_, dt, n), b("rstd", rstd, F32, T, 4), b("gamma", gamma, dt, d),
         b.opt("dsum", dsum, dt, n), code, T, d, b("dx", dx, dt, n), b("dgamma", dgamma, dt, d),
