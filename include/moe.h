@@ -893,8 +893,9 @@ int moe_grouped_gemm_fwd_i4(const moe_shape* sh, const int32_t* offsets, const i
  *        [T][d/32]).  A block with a NaN or an infinity reads back as NaN (scale
  *        byte 255; MOE_E4M3: the scale is NaN).
  * A layer takes them as io->xq and io->xs with io->x_quantized set.  sum may be
- * x or residual, and y may be x, residual or sum.  The squares are added in fp32,
- * so |s| up to 2^63 / sqrt(d) is in range.  T = 0 does nothing.  Errors:
+ * x or residual, and y may be x, residual or sum.  The squares are added in
+ * fp32, scaled where they would leave its range: any finite s is in range as long
+ * as rstd is.  T = 0 does nothing.  Errors:
  * MOE_ERR_INVALID for null x or gamma, no output, codes without scales, T < 0, d
  * < 1, eps negative or not finite; MOE_ERR_UNSUPPORTED for d not a multiple of 8
  * (128 for E4M3 rows, 32 for MX rows) or above 32768, T >= 2^31, other types,

@@ -187,6 +187,36 @@ def test_non_finite_rows(bad, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,d", [(9, 512), (9, 8192), (5000, 1024), (1030, 2048), (9, 16384), (3, 40)])
+def test_squares_past_the_range(T, d, dtype):
+    """Rows of values whose squares are beyond fp32 at either end, alone and beside small ones, with eps 0, forward and
+    backward.  The scaling is by powers of two: tolerances as for other rows (and the smallest fp32 step)."""
+    import token_routed_expert_amd as tre
+    x, _, gamma = stream_rows(T, d, dtype, 4, special=False)
+    for i, scale in enumerate((2.0 ** 118, 2.0 ** 64, 2.0 ** 60, 2.0 ** -30, 2.0 ** -64, 2.0 ** -110)):
+        x[i::7] = (x[i::7].float() * scale).to(dtype)
+    x[1, 3] = 2.0 ** 122
+    y, rstd = torch.empty_like(x), torch.empty(T, device="cuda")
+    tre.moe_add_rms_norm(x, None, gamma, 0.0, None, y, rstd)
+    want, wr = oracle.rms_norm(f64(x), f64(gamma), 0.0)
+    assert (np.abs(f64(rstd) - wr) <= (d / 2 + 5) * U * wr).all()
+    e = (d / 2 + 7) * U
+    assert (np.abs(f64(y) - want) <= (e + H[dtype] * (1 + e)) * np.abs(want) + 2.0 ** -133).all()
+    dy = torch.randn(T, d, generator=torch.Generator().manual_seed(9)).to(dtype).cuda()
+    dx, dg = torch.empty_like(x), torch.empty_like(gamma)
+    tre.moe_add_rms_norm_bwd(dy, x, rstd, gamma, None, dx, dg, bwd_ws(T, d))
+    s, dyn, gn, rn = f64(x), f64(dy), f64(gamma), f64(rstd)[:, None]
+    wx, wg = oracle.rms_norm_bwd(dyn, s, rn[:, 0], gn)
+    gs, xh = np.abs(dyn * gn), np.abs(s * rn)
+    mean = (gs * xh).mean(1, keepdims=True)
+    size = rn * (gs + xh * mean)
+    tol = H[dtype] * (np.abs(wx) + 1e-6 * size) + 8 * U * size + (d + 4) * U * rn * xh * mean + 2.0 ** -133
+    assert (np.abs(f64(dx) - wx) <= tol).all()
+    size = np.abs(dyn * s * rn).sum(0)
+    assert (np.abs(f64(dg) - wg) <= H[dtype] * (np.abs(wg) + 1e-3 * size) + (T + 8) * U * size).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("T,d", [(6, 512), (5000, 512), (300, 16384), (3, 40)])
 def test_in_place(T, d, dtype):
     """sum over x or the residual, y over any of them, dx over dy or dsum."""

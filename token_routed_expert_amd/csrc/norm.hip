@@ -155,7 +155,7 @@ __device__ __forceinline__ void quant8(const float* v, bool ok, size_t at, uint8
 // row before it writes any.
 template <typename T, int Q, int WPR, int NV, bool PAST>
 __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_kernel(NormArgs a) {
-  __shared__ float red[WPR];
+  __shared__ float red[2][WPR];
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
   const int w = WPR == 1 ? 0 : wid;
   const int64_t row = WPR == 1 ? (int64_t)blockIdx.x * 4 + wid : blockIdx.x;
@@ -182,17 +182,27 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_kernel(NormArg
   // Eight sums a lane, then a tree, and the root in 64 bits: an error of rstd moves a
   // whole row's values over rounding borders of the codes (one sum and fp32: 1.6 times
   // the error of the MXFP8 values of 7168 columns).
-  float v[NV][8], sq[8] = {};
+  float v[NV][8];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
+  for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      v[i][q] = res ? rounded(xr[i].at(q) + rr[i].at(q), T{}) : xr[i].at(q);
-      sq[q] = fmaf(v[i][q], v[i][q], sq[q]);
-    }
-  }
-  const float ss = row_sum<WPR>(((sq[0] + sq[1]) + (sq[2] + sq[3])) + ((sq[4] + sq[5]) + (sq[6] + sq[7])), w, red);
-  const float rstd = (float)(1.0 / sqrt((double)ss / (double)a.d + (double)a.eps));
+    for (int q = 0; q < 8; ++q) v[i][q] = res ? rounded(xr[i].at(q) + rr[i].at(q), T{}) : xr[i].at(q);
+  auto squares = [&](float scale, float* r) __attribute__((always_inline)) {
+    float sq[8] = {};
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float t = v[i][q] * scale;
+        sq[q] = fmaf(t, t, sq[q]);
+      }
+    return (double)row_sum<WPR>(((sq[0] + sq[1]) + (sq[2] + sq[3])) + ((sq[4] + sq[5]) + (sq[6] + sq[7])), w, r);
+  };
+  // Rows whose squares leave fp32's range at either end (the same for all lanes of a
+  // row) are added again, scaled.
+  double ss = squares(1.0f, red[0]);
+  if (!(ss >= 0x1p-60 && ss <= 0x1p120)) ss = ss < 1.0 ? squares(0x1p90f, red[1]) * 0x1p-180 : squares(0x1p-90f, red[1]) * 0x1p180;
+  const float rstd = (float)(1.0 / sqrt(ss / (double)a.d + (double)a.eps));
   if (a.rstd && w == 0 && lane == 0) a.rstd[row] = rstd;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -276,9 +286,8 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_bwd_kernel(Nor
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int q = 0; q < 8; ++q) c = fmaf(cur.dy[i].at(q) * gm[i].at(q), cur.s[i].at(q), c);
-    c = row_sum<WPR>(c, w, red[par]);
-    c = c * cur.rstd / (float)a.d;
+      for (int q = 0; q < 8; ++q) c = fmaf(cur.dy[i].at(q) * gm[i].at(q), cur.s[i].at(q) * cur.rstd, c);
+    c = row_sum<WPR>(c, w, red[par]) / (float)a.d;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float o[8];
