@@ -861,7 +861,8 @@ int moe_dequantize_weights_i4(const uint8_t* codes, const uint32_t* scales, int6
  * with fp32 accumulation; o [P][d] is bf16.  Row r is row token_of[r] of x [T][d]
  * (an entry outside [0, T) reads a row of zeros), or, token_of NULL, row r of the
  * permuted x [P][d].  Rows of o from offsets[E] on are not written.  ws_bytes >=
- * moe_workspace_bytes(sh, MOE_WS_GEMM_FWD) (h).  Errors: MOE_ERR_INVALID for
+ * moe_workspace_bytes(sh, MOE_WS_GEMM_FWD) (h, and fp32 sums where the rows are too
+ * few to fill the chip with whole products).  Errors: MOE_ERR_INVALID for
  * another dtype; MOE_ERR_UNSUPPORTED for d or f not a multiple of 128, another
  * group than 32, 64 or 128, P * max(d, f) >= 2^30 - 2048 or d * f >= 2^31.
  */

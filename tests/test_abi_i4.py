@@ -160,9 +160,27 @@ def test_few_rows_rule():
     def few(P, E, d, f, **kw):
         return bool(N.lib().moe_few_rows(C.byref(make_shape(**{**dict(T=P, d=d, E=E, k=1, f=f, dtype="int4"), **kw}))))
     assert few(20 * 128, 128, 4096, 1536) and not few(32 * 128, 128, 4096, 1536)
-    assert few(32 * 8, 8, 4096, 14336) and not few(64 * 8, 8, 4096, 14336)
+    assert few(20 * 8, 8, 4096, 14336) and not few(28 * 8, 8, 4096, 14336)
     assert few(128 * 8, 8, 1024, 1024) and not few(512 * 8, 8, 1024, 1024)
     assert few(1, 8, 128, 128) and not few(1, 8, 200, 128)
+
+
+def test_parts_of_k():
+    """The workspace of calls with many rows: h, and the larger of the two products' sums over parts of K; one part
+    where the tiles fill the chip, and no sums with few rows."""
+    import test_gpu_i4 as G
+
+    def ws(P, E, d, f):
+        return N.lib().moe_workspace_bytes(C.byref(make_shape(P, d, E, 1, f, dtype="int4")), N.MOE_WS_GEMM_FWD)
+
+    def want(P, d, f, fc1, fc2):
+        up = lambda n: (n + 255) // 256 * 256
+        return up(2 * P * f) + up(max(4 * fc1 * P * 2 * f * (fc1 > 1), 4 * fc2 * P * d * (fc2 > 1)))
+    for counts, d, f, fc1, fc2 in G.PARTS.values():
+        assert not G.few(sum(counts), len(counts), d, f)
+        assert ws(sum(counts), len(counts), d, f) == want(sum(counts), d, f, fc1, fc2)
+    for P, E, d, f in ((8192 * 8, 128, 4096, 1536), (4096 * 2, 8, 4096, 14336), (8, 128, 4096, 1536), (1, 1, 8192, 128)):
+        assert ws(P, E, d, f) == want(P, d, f, 1, 1)
 
 
 def test_launches_of_two_to_the_32_threads():

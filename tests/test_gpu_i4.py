@@ -305,6 +305,53 @@ def test_product_every_form_of_the_rows_kernel(form, group, asym):
     check(case, len(counts), 1, sum(counts), d, f)
 
 
+# (counts, d, f) with too few tiles for the chip, and the parts of K of the two products
+PARTS = {"four_one": ([700, 0, 590], 4096, 512, 4, 1), "one_four": ([1, 1299], 256, 4096, 1, 4),
+         "three_one": ([400, 33, 857], 3200, 896, 3, 1), "one_three": ([128, 1162, 0], 896, 2304, 1, 3),
+         "two_four": ([390, 0], 3200, 4096, 2, 4), "one_two": ([0, 1300], 1536, 2304, 1, 2)}
+
+
+@pytest.mark.parametrize("group,asym", [(32, True), (64, False), (128, True)])
+@pytest.mark.parametrize("name", PARTS)
+def test_product_in_parts_of_k(name, group, asym):
+    counts, d, f = PARTS[name][:3]
+    case = product_case(counts, d, f, group, asym, 5, group != 64)
+    check(case, len(counts), 1, sum(counts), d, f)
+
+
+def test_parts_of_k_leave_the_other_rows():
+    """Rows behind the last expert; a NaN in one row; the same bits again, and from a replayed graph on other inputs."""
+    import token_routed_expert_amd as tre
+    counts, d, f = PARTS["two_four"][:3]
+    T = sum(counts)
+    short = product_case([200, 60], d, f, 64, True, 8, True, T=T)
+    check(short, 2, 1, T, d, f)
+    case = product_case(counts, d, f, 32, True, 6, False)
+    o = run_product(case, 2, 1, T, d, f)
+    xs = [case[0].clone().cuda(), case[0].clone().cuda()]
+    xs[1][7, 40] = float("nan")
+    bad = run_product((xs[1].cpu(),) + case[1:], 2, 1, T, d, f)
+    keep = torch.arange(T) != 7
+    assert torch.equal(bad.cpu()[keep], o.cpu()[keep]) and torch.isnan(bad[7]).all()
+    sh = tre.make_shape(T, d, 2, 1, f, dtype="int4")
+    x, out, off = xs[0].clone(), torch.empty_like(o), torch.from_numpy(case[3]).cuda()
+    ws = torch.empty(tre.moe_workspace_bytes(sh, tre.MOE_WS_GEMM_FWD), dtype=U8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        tre.moe_grouped_gemm_fwd_i4(sh, off, None, x, case[2], out, ws)
+    for i in (0, 1, 0, 1):
+        x.copy_(xs[i])
+        out.fill_(7.0)
+        ws.fill_(0xEE)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int16), (o, bad)[i].view(torch.int16))
+    del graph
+
+
 def test_rows_past_the_last_expert_stay():
     """offsets[E] below P (assignments that the map skipped)."""
     case = product_case([20, 0, 300], 256, 256, 64, True, 9, True, T=400)

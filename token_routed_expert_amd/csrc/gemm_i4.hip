@@ -4,11 +4,11 @@
 //   fc1:  [a | b] = x W13,  h = silu(a) b, rounded to bf16 in the epilogue
 //   fc2:  o = h W2
 //
-// on v_mfma_f32_16x16x32_bf16, fp32 accumulation.  The weights are the first operand
-// (rows of D = C^T: four consecutive output columns per lane), decoded to bf16 in
-// registers: a lane's 16 bytes of a 128-row tile are its operands of four products.
-// W13 holds W1's and W3's 16-column groups alternately, so a lane holds a and b of
-// the same element.
+// on v_mfma_f32_16x16x32_bf16 (many rows: 32x32x16), fp32 accumulation.  The weights
+// are the first operand (rows of D = C^T: four consecutive output columns per lane),
+// decoded to bf16 in registers: a lane's 16 bytes of a 128-row tile are its operands
+// of four products.  W13 holds W1's and W3's 16-column groups alternately, so a lane
+// holds a and b of the same element.
 #include "gemm_common.h"
 #include "i4.h"
 
@@ -292,6 +292,14 @@ __device__ __forceinline__ f32x4_t quad(const f32x16_t& a) {
 // ahead of the products that take them, between those products: 19 vector
 // instructions for 8 weights a lane, 76 a step of 16 products.
 //
+// Bound by the matrix unit with that decoding beside it: 8192 tokens through 8 of 128
+// experts (d 4096, f 1536) take 2.23 ms, 1.11 PFLOP/s; the same without decoding 1.91,
+// with half of it 1.99.  Loads that all hit take 2-3 % off, fragments read further
+// ahead nothing; a wavefront tile of 256 rows, which would decode half as often,
+// spills (3.1 ms), and decoded weights shared through LDS would be bound by its
+// bandwidth.  Where there are too few tiles for the chip, blockIdx.y takes parts of K
+// and gemm_i4_join_kernel adds them.
+//
 // A (activations): stages of 64 k through three LDS slots, 128 rows of 128 bytes, the
 // 16-byte chunk c of row r stored at chunk c ^ ((r >> 1) & 7), which spreads the rows
 // of a fragment read over all banks.  B: 128 k (two stages, four steps) as stored, 4
@@ -316,6 +324,8 @@ __global__ __launch_bounds__(256, 2) void gemm_i4_tile_kernel(I4Args args, int N
   const int n0 = uniform(ti.n0) * BN;
   const int K = FC == 1 ? args.d : args.f, N = FC == 1 ? 2 * args.f : args.d;
   const int KT = K >> 7;
+  // this block's part of K, in 128 k
+  const int P0 = KT * (int)blockIdx.y / (int)gridDim.y, P1 = KT * ((int)blockIdx.y + 1) / (int)gridDim.y;
 
   // ---- sources: rows past the expert's end and columns past N read as zero
   const bool gather = FC == 1 && args.token_of != nullptr;
@@ -346,16 +356,16 @@ __global__ __launch_bounds__(256, 2) void gemm_i4_tile_kernel(I4Args args, int N
     return uniform_rsrc(v);
   };
   auto issue_a = [&](int kt, int slot, int q) __attribute__((always_inline)) {
-    const bool live = kt < 2 * KT;
+    const bool live = kt < 2 * P1;
     dma16(src(a_src, live), a_off[q], (uint32_t)(live ? kt : 0) * 128u,
           lds_base + (uint32_t)(slot * A_BYTES + (w * NA + q) * 1024));
   };
   auto issue_b = [&](int P, int j) __attribute__((always_inline)) {
-    const bool live = P < KT;
+    const bool live = P < P1;
     dma16(src(b_src, live), lane16, (uint32_t)(j * KT + (live ? P : 0)) * 1024u, b_dst + (uint32_t)(j * 1024));
   };
   auto issue_bs = [&](int P, int u) __attribute__((always_inline)) {
-    const bool live = P < KT;
+    const bool live = P < P1;
     dma4(src(bs_src, live), lane4, (uint32_t)((live ? P : 0) * U + u) * 256u, b_dst + (uint32_t)(4096 + u * 256));
   };
 
@@ -409,10 +419,10 @@ __global__ __launch_bounds__(256, 2) void gemm_i4_tile_kernel(I4Args args, int N
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int f = 0; f < 2; ++f) acc[i][f] = f32x16_t{};
-  static_for<0, 4>([&](auto J) __attribute__((always_inline)) { issue_b(0, J.value); });
-  static_for<0, U>([&](auto I) __attribute__((always_inline)) { issue_bs(0, I.value); });
+  static_for<0, 4>([&](auto J) __attribute__((always_inline)) { issue_b(P0, J.value); });
+  static_for<0, U>([&](auto I) __attribute__((always_inline)) { issue_bs(P0, I.value); });
   static_for<0, 2>([&](auto S) __attribute__((always_inline)) {
-    static_for<0, NA>([&](auto Q) __attribute__((always_inline)) { issue_a(S.value, S.value, Q.value); });
+    static_for<0, NA>([&](auto Q) __attribute__((always_inline)) { issue_a(2 * P0 + S.value, S.value, Q.value); });
   });
   wait_vmcnt<NA>();
   block_barrier();
@@ -485,7 +495,7 @@ __global__ __launch_bounds__(256, 2) void gemm_i4_tile_kernel(I4Args args, int N
     if constexpr (h == 1) slot = next;
   };
   auto run = [&](auto SKIP) __attribute__((always_inline)) {
-    for (int P = 0; P < KT; ++P)
+    for (int P = P0; P < P1; ++P)
       static_for<0, 4>([&](auto S) __attribute__((always_inline)) { step(P, S, SKIP); });
   };
   if (nfr == FM) run(IntC<0>{});
@@ -500,7 +510,15 @@ __global__ __launch_bounds__(256, 2) void gemm_i4_tile_kernel(I4Args args, int N
     static_for<0, 2>([&](auto F) __attribute__((always_inline)) {
       constexpr int f = F.value;
       const f32x4_t q0 = quad<0>(acc[i][f]), q1 = quad<1>(acc[i][f]), q2 = quad<2>(acc[i][f]), q3 = quad<3>(acc[i][f]);
-      if constexpr (FC == 1) {                  // columns 0..15 of W1 and the same of W3
+      if (gridDim.y > 1) {                      // sums over a part of K, as they are
+        float* p = args.part + ((size_t)blockIdx.y * args.P + row) * (size_t)N + col + 32 * f + 4 * kg;
+        if (m < rows) {
+          *(f32x4_t*)p = q0;
+          *(f32x4_t*)(p + 8) = q1;
+          *(f32x4_t*)(p + 16) = q2;
+          *(f32x4_t*)(p + 24) = q3;
+        }
+      } else if constexpr (FC == 1) {           // columns 0..15 of W1 and the same of W3
         f32x4_t h0, h1;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -521,13 +539,51 @@ __global__ __launch_bounds__(256, 2) void gemm_i4_tile_kernel(I4Args args, int N
   });
 }
 
+// The parts of K (fp32 [parts][P][N]) added in order, and the epilogue: a thread takes
+// eight columns of h or o.  Rows outside the experts' are left as they were.
+template <int FC>
+__global__ __launch_bounds__(256) void gemm_i4_join_kernel(I4Args args, int parts) {
+  const int C = FC == 1 ? args.f : args.d;
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8, row = at / C;
+  if (row < args.offsets[0] || row >= min(args.offsets[args.E], args.P)) return;
+  const int64_t all = (int64_t)args.P * (FC == 1 ? 2 * C : C);
+  auto sum8 = [&](const float* p, f32x4_t (&v)[2]) __attribute__((always_inline)) {
+    v[0] = *(const f32x4_t*)p;
+    v[1] = *(const f32x4_t*)(p + 4);
+    for (int i = 1; i < parts; ++i) {
+      v[0] += *(const f32x4_t*)(p + i * all);
+      v[1] += *(const f32x4_t*)(p + i * all + 4);
+    }
+  };
+  f32x4_t v[2];
+  if constexpr (FC == 1) {                      // 16 columns of W1, then the same of W3
+    const int c = (int)(at - row * C);
+    const float* p = args.part + row * 2 * C + 2 * (c & ~15) + (c & 15);
+    f32x4_t b[2];
+    sum8(p, v);
+    sum8(p + 16, b);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q >> 2][q & 3] = silu_f32(v[q >> 2][q & 3]) * b[q >> 2][q & 3];
+  } else {
+    sum8(args.part + at, v);
+  }
+  *(u32x4_t*)((FC == 1 ? args.h : args.o) + at) =
+      u32x4_t{pack_bf16x2(v[0][0], v[0][1]), pack_bf16x2(v[0][2], v[0][3]), pack_bf16x2(v[1][0], v[1][1]),
+              pack_bf16x2(v[1][2], v[1][3])};
+}
+
 template <int FC, int U>
 int launch_tiles(const I4Args& a, hipStream_t s) {
   const int64_t NT = ((FC == 1 ? 2 * (int64_t)a.f : (int64_t)a.d) + 255) / 256;
   // at most sum_e ceil(m_e / 128) row tiles; a block past the device-side count ends at once
   const int64_t grid = ((int64_t)a.P / 128 + a.E) * NT;
-  if (!launch_fits(grid, 256)) return MOE_ERR_UNSUPPORTED;
-  gemm_i4_tile_kernel<FC, U><<<(unsigned)grid, 256, 0, s>>>(a, (int)NT);
+  const int parts = gemm_i4_parts(a, FC);
+  if (!launch_fits(grid * parts, 256)) return MOE_ERR_UNSUPPORTED;
+  gemm_i4_tile_kernel<FC, U><<<dim3((unsigned)grid, (unsigned)parts), 256, 0, s>>>(a, (int)NT);
+  TRE_LAUNCH_CHECK();
+  if (parts == 1) return MOE_OK;
+  const int64_t n = (int64_t)a.P * (FC == 1 ? a.f : a.d) / 8;
+  gemm_i4_join_kernel<FC><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a, parts);
   TRE_LAUNCH_CHECK();
   return MOE_OK;
 }
@@ -554,25 +610,58 @@ int launch_fc(const I4Args& a, hipStream_t s) {
 
 }  // namespace
 
-// Which kernel.  Both take a time that goes with K and with the rounds of blocks that
-// the chip runs at once: pieces of 32 rows x 64 columns, three to a compute unit, or
-// tiles of 128 x 256, two to one, of which a K step takes three times as long.  (An
-// expert has about 0.35 pieces or tiles more than its rows fill, and one at least.)
-// Both kernels, us, rows an expert:
-//   128 experts, d 4096, f 1536: 16 rows 288 against 373, 24: 343 / 373, 32: 453 / 398,
-//   64: 794 / 478; 8, d 4096, f 14336: 16 rows 187 / 352, 32: 278 / 360, 48: 386 / 369,
-//   64: 481 / 402; 8, d = f = 1024: 64 rows 22 / 39, 128: 28 / 35, 256: 40 / 36, 512:
-//   72 / 41; 4, d 384, f 2560: 400 rows 47 / 56; 32, d 2048, f 1408: 32 rows 71 / 73,
-//   64: 107 / 82.
+static int64_t stored_columns(const I4Args& a, int fc) { return fc == 1 ? 2 * (int64_t)a.f : a.d; }
+static int64_t contraction(const I4Args& a, int fc) { return fc == 1 ? a.d : a.f; }
+
+// Blocks of m rows x n columns of a product, as the host can tell: an expert has about
+// 0.35 of them down its rows more than the rows fill, and one at least.
+static double blocks_of(const I4Args& a, int fc, double m, double n) {
+  const double experts = a.P < a.E ? a.P : a.E, have = a.P / experts / m + 0.35;
+  return experts * (have > 1.0 ? have : 1.0) * ((double)stored_columns(a, fc) / n);
+}
+
+// The tiles' time, in k that a full chip of them (two blocks to each of 256 compute
+// units) goes through, and the parts of K, one block each, that make it least: half a
+// chip of blocks takes three quarters of a full one's time a step, and the parts' sums
+// cost a launch and their way through memory.  One part against these, us, rows an
+// expert: 8 experts, d 4096, f 14336: 36 rows 372 against 267 (four parts in fc2), 64:
+// 413 / 315, 100: 447 / 361, 150: 562 / 550 (two), 259: 802 / 794; 1, d 2048, f 8192: 512
+// rows 133 / 76 (two, four); 2, d 7168, f 2048: 200 rows 157 / 95; 4, d 384, f 2560: 400
+// rows 58 / 38.
+struct TileCost {
+  int parts;
+  double time;
+};
+static TileCost tile_cost(const I4Args& a, int fc) {
+  const double K = (double)contraction(a, fc), tiles = blocks_of(a, fc, 128, 256);
+  const double values = (double)a.P * (double)stored_columns(a, fc);
+  TileCost best = {1, 0.0};
+  for (int parts = 1; parts <= 4 && parts * 128 <= K; ++parts) {
+    const double r = tiles * parts / 512;
+    const double time = (r < 1.0 ? 0.5 + 0.5 * r : r) * K / parts + (parts > 1 ? 160 + 1e-4 * values * parts : 0.0);
+    if (parts == 1 || time < best.time) best = {parts, time};
+  }
+  return best;
+}
+
+int gemm_i4_parts(const I4Args& a, int fc) { return gemm_i4_few_rows(a) ? 1 : tile_cost(a, fc).parts; }
+
+// Which kernel.  The rows kernel's time goes with the rounds of its pieces of 32 rows x
+// 64 columns, three to a compute unit; a step of a chip of tiles takes three times as
+// long as one of theirs.  Both kernels, us, rows an expert:
+//   128 experts, d 4096, f 1536: 16 rows 298 against 386, 32: 467 / 415, 64: 808 / 508;
+//   8, d 4096, f 14336: 16 rows 185 / 232, 20: 211 / 237, 28: 272 / 250, 64: 490 / 315;
+//   8, d = f = 1024: 64 rows 22 / 41, 256: 40 / 38, 512: 72 / 42; 4, d 384, f 2560: 200
+//   rows 32 / 34, 400: 47 / 38; 16, d 2048, f 8192: 24 rows 144 / 143, 32: 177 / 155; 32, d
+//   2048, f 1408: 32 rows 72 / 75, 64: 107 / 84.
 bool gemm_i4_few_rows(const I4Args& a) {
-  const double experts = a.P < a.E ? a.P : a.E, each = a.P / experts;
-  auto steps = [&](double m, double n, double blocks, int64_t N, int64_t K) {
-    const double have = each / m + 0.35, rounds = experts * (have > 1.0 ? have : 1.0) * ((double)N / n) / blocks;
-    return (rounds > 1.0 ? rounds : 1.0) * (double)K;
-  };
-  const int64_t N1 = 2 * (int64_t)a.f;
-  return steps(32, 64, 768, N1, a.d) + steps(32, 64, 768, a.d, a.f) <=
-         3.0 * (steps(128, 256, 512, N1, a.d) + steps(128, 256, 512, a.d, a.f));
+  double rows = 0, tiles = 0;
+  for (int fc = 1; fc <= 2; ++fc) {
+    const double r = blocks_of(a, fc, 32, 64) / 768;
+    rows += (r > 0.35 ? r : 0.35) * (double)contraction(a, fc);
+    tiles += tile_cost(a, fc).time;
+  }
+  return rows <= 3.0 * tiles;
 }
 
 int gemm_i4_launch(int fc, const I4Args& a, hipStream_t s) {

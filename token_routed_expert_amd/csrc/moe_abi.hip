@@ -169,9 +169,14 @@ int check_mx4_dims(const moe_shape* sh) {
   return MOE_OK;
 }
 
-// Integer weights: the workspace holds h; 32-bit byte offsets as for MXFP4, of rows
-// of two bytes a value.
-size_t i4_ws_bytes(const moe_shape* sh) { return align_up((size_t)(sh->T * sh->k * sh->f) * 2, 256); }
+// Integer weights: the workspace holds h and, where K is taken in parts, those
+// sums; 32-bit byte offsets as for MXFP4, of rows of two bytes a value.
+I4Args i4_sizes(const moe_shape* sh) {
+  I4Args a = {};
+  a.E = (int)sh->E; a.d = (int)sh->d; a.f = (int)sh->f; a.P = (int)(sh->T * sh->k); a.T = (int)sh->T;
+  return a;
+}
+size_t i4_h_bytes(const moe_shape* sh) { return align_up((size_t)(sh->T * sh->k * sh->f) * 2, 256); }
 int check_i4_dims(const moe_shape* sh) {
   if (!is_i4(sh)) return MOE_ERR_INVALID;
   if (sh->d % 128 != 0 || sh->f % 128 != 0) return MOE_ERR_UNSUPPORTED;
@@ -179,6 +184,15 @@ int check_i4_dims(const moe_shape* sh) {
   if (sh->T * sh->k * std::max(sh->d, sh->f) >= (lim - 4096) / 2 || sh->d * sh->f >= lim)
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
+}
+size_t i4_ws_bytes(const moe_shape* sh) {
+  if (check_i4_dims(sh) != MOE_OK) return i4_h_bytes(sh);
+  const I4Args a = i4_sizes(sh);
+  auto sums = [&](int fc, int64_t N) -> size_t {
+    const int parts = gemm_i4_parts(a, fc);
+    return parts > 1 ? (size_t)parts * (size_t)(sh->T * sh->k * N) * 4 : 0;
+  };
+  return i4_h_bytes(sh) + align_up(std::max(sums(1, 2 * sh->f), sums(2, sh->d)), 256);
 }
 bool group_ok(int64_t g) { return g == 32 || g == 64 || g == 128; }
 int check_weights(const moe_i4_weights* w) {
@@ -477,9 +491,7 @@ int moe_few_rows(const moe_shape* sh) {
     return check_gemm_dims(sh, sh->T * sh->k, sh->f) == MOE_OK && few_rows(sh);
   if (is_i4(sh)) {
     if (check_i4_dims(sh) != MOE_OK) return 0;
-    I4Args a = {};
-    a.E = (int)sh->E; a.d = (int)sh->d; a.f = (int)sh->f; a.P = (int)(sh->T * sh->k);
-    return gemm_i4_few_rows(a);
+    return gemm_i4_few_rows(i4_sizes(sh));
   }
   if (!is_mx4(sh) || check_mx4_dims(sh) != MOE_OK) return 0;
   Mx4Args a = {};
@@ -1172,12 +1184,12 @@ int moe_grouped_gemm_fwd_i4(const moe_shape* sh, const int32_t* offsets, const i
   if (!aligned(16, (const char*)x, (const char*)o, (const char*)ws) || !aligned(4, offsets, token_of))
     return MOE_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < i4_ws_bytes(sh)) return MOE_ERR_WORKSPACE;
-  I4Args a = {};
+  I4Args a = i4_sizes(sh);
   a.offsets = offsets; a.token_of = token_of;
-  a.E = (int)sh->E; a.d = (int)sh->d; a.f = (int)sh->f; a.P = (int)(sh->T * sh->k); a.T = (int)sh->T;
   a.group = (int)w->group;
   a.a = (const uint16_t*)x; a.w = w->W13; a.ws = w->W13s;
   a.h = (uint16_t*)ws;
+  a.part = (float*)((char*)ws + i4_h_bytes(sh));
   if ((st = gemm_i4_launch(1, a, (hipStream_t)stream))) return st;
   a.token_of = nullptr;
   a.a = (const uint16_t*)ws; a.w = w->W2; a.ws = w->W2s;
