@@ -217,7 +217,7 @@ def test_squares_past_the_range(T, d, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("T,d", [(6, 512), (5000, 512), (300, 16384), (3, 40)])
+@pytest.mark.parametrize("T,d", [(6, 512), (5000, 512), (300, 16384), (3, 40), (200, 9000), (500, 2056)])
 def test_in_place(T, d, dtype):
     """sum over x or the residual, y over any of them, dx over dy or dsum."""
     import token_routed_expert_amd as tre
@@ -251,7 +251,7 @@ def bwd_ws(T, d):
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("dsum", [True, False])
-@pytest.mark.parametrize("T,d", SIZES + [(2049, 1024), (257, 512), (1025, 4096), (1, 16384)])
+@pytest.mark.parametrize("T,d", SIZES + [(2049, 1024), (257, 512), (1025, 4096), (1, 16384), (256, 8328), (1024, 264)])
 def test_bwd(T, d, dsum, dtype):
     import token_routed_expert_amd as tre
     x, r, gamma = stream_rows(T, d, dtype, T + d, special=False)
@@ -307,6 +307,8 @@ def test_no_rows(dtype):
     tre.moe_add_rms_norm(e, e, one, EPS, e, e, None)
     tre.moe_add_rms_norm_bwd(e, e, torch.empty(0, device="cuda"), one, e, e, dg, None)
     assert (dg == 0).all() and (one == 1).all()
+    tre.moe_dequantize_rows(torch.empty(0, d, dtype=torch.uint8, device="cuda"),
+                            torch.empty(0, d // 32, dtype=torch.uint8, device="cuda"), "mxfp8", e)
 
 
 def test_python_calls_check_their_tensors():

@@ -100,7 +100,7 @@ struct Words<2> {
 // the same call takes 152 us, 6.6 TB/s, with it 5.5; 177 tokens, groups of 64, 241 us
 // against 274, 5.0 TB/s, of which reading x from L2 costs 14.
 template <int FC, int U, int NW, int CF>
-__global__ __launch_bounds__(NW * 64, U == 1 || NW == 16 ? 4 : 3) void gemm_i4_rows_kernel(I4Args args) {
+__global__ __launch_bounds__(NW * 64, U == 1 ? 4 : 3) void gemm_i4_rows_kernel(I4Args args) {
   __shared__ f32x4_t part[2][NW][CF][64];
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int w = uniform((int)threadIdx.x >> 6);

@@ -210,10 +210,12 @@ struct NormBwdArgs {
   int64_t T, teams;
   int d;
   void* dx;
+  void* dgamma;
   float* part;  // [teams][d]
+  bool few;     // (the launch's own choice)
 };
 int64_t norm_bwd_teams(int64_t T, int64_t d);
-int norm_bwd_launch(const NormBwdArgs& a, bool f32, void* dgamma, hipStream_t s);
+int norm_bwd_launch(const NormBwdArgs& a, bool f32, hipStream_t s);
 int dequant_rows_launch(const uint8_t* codes, const void* scales, int q_dtype, int64_t rows, int64_t cols, void* dst,
                         bool f32, hipStream_t s);
 

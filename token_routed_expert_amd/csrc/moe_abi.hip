@@ -1239,9 +1239,9 @@ int moe_add_rms_norm_bwd(const void* dy, const void* sum, const float* rstd, con
                (const char*)ws) ||
       !aligned(4, (const char*)rstd, (const char*)dgamma))
     return MOE_ERR_UNSUPPORTED;
-  NormBwdArgs a = {dy, sum, gamma, dsum, rstd, T, norm_bwd_teams(T, d), (int)d, dx, (float*)ws};
+  NormBwdArgs a = {dy, sum, gamma, dsum, rstd, T, norm_bwd_teams(T, d), (int)d, dx, dgamma, (float*)ws, false};
   if (a.teams > 0 && (!ws || ws_bytes < (size_t)(a.teams * d) * 4)) return MOE_ERR_WORKSPACE;
-  return norm_bwd_launch(a, dtype == MOE_F32, dgamma, (hipStream_t)stream);
+  return norm_bwd_launch(a, dtype == MOE_F32, (hipStream_t)stream);
 }
 
 int moe_dequantize_rows(const uint8_t* codes, const void* scales, int32_t q_dtype, int64_t rows, int64_t cols,

@@ -67,6 +67,13 @@ __device__ __forceinline__ void put8(T* p, const float* v) {
   if constexpr (PAST) stream8(p, v);
   else store8(p, v);
 }
+// Four consecutive values.
+__device__ __forceinline__ f32x4_t four(const float* p) { return *(const f32x4_t*)p; }
+__device__ __forceinline__ f32x4_t four(const bf16_t* p) {
+  const uint2 w = *(const uint2*)p;
+  return f32x4_t{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                 __uint_as_float(w.y & 0xffff0000u)};
+}
 __device__ __forceinline__ float rounded(float v, bf16_t) { return bf16_to_f32(f32_to_bf16(v)); }
 __device__ __forceinline__ float rounded(float v, float) { return v; }
 
@@ -222,16 +229,64 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_kernel(NormArg
   }
 }
 
+// a b, rounded by itself (never part of a fused addition).
+__device__ __forceinline__ float product(float a, float b) {
+#pragma clang fp contract(off)
+  return a * b;
+}
+
+// dgamma of THREADS / 4 columns from dy, sum and rstd: a thread takes every 16th row of
+// four columns, and the 16 parts meet in LDS.  The sums are those of the two kernels
+// below, where a team has one row, in the same order.
+template <typename T, int THREADS>
+__device__ __forceinline__ void few_dgamma(const NormBwdArgs& a, int block) {
+  constexpr int L = THREADS / 16;
+  __shared__ f32x4_t part[16][L];
+  const int l = threadIdx.x % L, w = threadIdx.x / L;
+  const int col = (block * L + l) * 4;
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+  if (col < a.d) {
+#pragma unroll 8
+    for (int r = w; r < (int)a.T; r += 16) {
+      const size_t at = (size_t)r * (size_t)a.d + (size_t)col;
+      const f32x4_t dy = four((const T*)a.dy + at), s = four((const T*)a.sum + at);
+      const float rstd = a.rstd[r];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] += product(dy[q], s[q] * rstd);
+    }
+  }
+  part[w][l] = v;
+  __syncthreads();
+  if (w != 0 || col >= a.d) return;
+  v = part[0][l];
+#pragma unroll
+  for (int i = 1; i < 16; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] += part[i][l][q];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) Elem<T>::store((T*)a.dgamma + col + q, v[q]);
+}
+
 // The backward: with g = dy gamma and c = rstd / d sum(g s),
 //   dx = dsum + rstd (g - s rstd c),  dgamma = sum over rows of dy s rstd.
 // Teams of WPR wavefronts walk the rows with a stride of the number of teams and
 // keep their part of dgamma in registers; the parts, [teams][d] fp32, are summed
 // in order by a second kernel.  PRE: the next row is on its way while the current
 // one is worked on.  dx may be dy or dsum.  Bound by memory: 16384 rows of 7168 bf16 with
-// dsum 178 us (5.3 TB/s) and 5 for dgamma; 257 rows of 512 fp32 3.6 and 3.2 us.
-template <typename T, int WPR, int NV, bool PRE>
+// dsum 178 us (5.3 TB/s) and 5 for dgamma.
+//
+// FEW: one launch for few rows.  Every team has one row, and blocks after theirs take
+// dgamma from dy, sum and rstd again.
+template <typename T, int WPR, int NV, bool PRE, bool FEW>
 __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_bwd_kernel(NormBwdArgs a) {
   __shared__ float red[2][WPR];
+  if constexpr (FEW) {
+    const int rows = WPR == 1 ? (int)(a.T + 3) / 4 : (int)a.T;  // blocks for the rows
+    if ((int)blockIdx.x >= rows) {
+      few_dgamma<T, WPR == 1 ? 256 : 64 * WPR>(a, (int)blockIdx.x - rows);
+      return;
+    }
+  }
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
   const int w = WPR == 1 ? 0 : wid;
   const int64_t team = WPR == 1 ? (int64_t)blockIdx.x * 4 + wid : blockIdx.x;
@@ -297,13 +352,15 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_bwd_kernel(Nor
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         const float dy = cur.dy[i].at(q), xhat = cur.s[i].at(q) * cur.rstd;
-        o[q] = cur.rstd * (dy * gm[i].at(q) - xhat * c);
-        if (a.dsum) o[q] += cur.ds[i].at(q);
+        // (every fused operation by name: the same bits from every form of this kernel)
+        const float v = fmaf(-xhat, c, dy * gm[i].at(q));
+        o[q] = a.dsum ? fmaf(cur.rstd, v, cur.ds[i].at(q)) : cur.rstd * v;
         acc[i][q] = fmaf(dy, xhat, acc[i][q]);
       }
       if (ok[i]) store8((T*)a.dx + (size_t)r * (size_t)a.d + (size_t)at[i] * 8, o);
     }
   }
+  if constexpr (FEW) return;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
     if (ok[i]) store8(a.part + (size_t)team * (size_t)a.d + (size_t)at[i] * 8, acc[i]);
@@ -393,17 +450,31 @@ int fwd_type(const NormArgs& a, hipStream_t s) {
   return fwd_of<T, MOE_MXFP4>(a, s);
 }
 
+// One launch where a row is a team: two launches and one, calls in a row, us: 257 rows of
+// 512 fp32 10.4 and 8.0, 512 of 4096 13.0 / 9.9, 512 of 8192 19.8 / 16.9, 1024 of 1024 11.5 /
+// 10.0, 2048 of 512 14.2 / 15.2; bf16 256 of 16384 19.8 / 12.2.  (Its blocks for dgamma read
+// dy while others write dx, so these may not be one.)
+bool few_rows(const NormBwdArgs& a, size_t bytes) {
+  const char *dx = (const char*)a.dx, *dy = (const char*)a.dy;
+  return a.T > 0 && a.T <= 1024 && a.teams == a.T && (dx + bytes <= dy || dy + bytes <= dx);
+}
+
 template <typename T, int WPR, int NV>
 int bwd_as(const NormBwdArgs& a, hipStream_t s) {
+  constexpr int THREADS = WPR == 1 ? 256 : 64 * WPR;
   const int64_t grid = WPR == 1 ? (a.teams + 3) / 4 : a.teams;
-  norm_bwd_kernel<T, WPR, NV, (sizeof(T) * NV <= 8)><<<(unsigned)grid, WPR == 1 ? 256 : 64 * WPR, 0, s>>>(a);
+  if (a.few)
+    norm_bwd_kernel<T, WPR, NV, false, true><<<(unsigned)(grid + (a.d + THREADS / 4 - 1) / (THREADS / 4)), THREADS, 0, s>>>(a);
+  else
+    norm_bwd_kernel<T, WPR, NV, (sizeof(T) * NV <= 8), false><<<(unsigned)grid, THREADS, 0, s>>>(a);
   TRE_LAUNCH_CHECK();
   return MOE_OK;
 }
 template <typename T>
-int bwd_of(const NormBwdArgs& a, void* dgamma, hipStream_t s) {
+int bwd_of(NormBwdArgs a, hipStream_t s) {
   const int nvec = a.d / 8;
   int st = MOE_OK;
+  a.few = few_rows(a, (size_t)a.T * (size_t)a.d * sizeof(T));
   if (a.T > 0) {
     if (nvec <= 128) st = bwd_as<T, 1, 2>(a, s);
     else if (nvec <= 512) st = bwd_as<T, 4, 2>(a, s);
@@ -411,8 +482,8 @@ int bwd_of(const NormBwdArgs& a, void* dgamma, hipStream_t s) {
     else if (nvec <= 2048) st = bwd_as<T, 16, 2>(a, s);
     else st = bwd_as<T, 16, 4>(a, s);
   }
-  if (st) return st;
-  norm_dgamma_kernel<T><<<(unsigned)((a.d + 63) / 64), 1024, 0, s>>>(a.part, (int)a.teams, a.d, (T*)dgamma);
+  if (st || a.few) return st;
+  norm_dgamma_kernel<T><<<(unsigned)((a.d + 63) / 64), 1024, 0, s>>>(a.part, (int)a.teams, a.d, (T*)a.dgamma);
   TRE_LAUNCH_CHECK();
   return MOE_OK;
 }
@@ -452,8 +523,8 @@ int norm_launch(const NormArgs& a, bool f32, hipStream_t s) {
   return f32 ? fwd_type<float>(a, s) : fwd_type<bf16_t>(a, s);
 }
 
-int norm_bwd_launch(const NormBwdArgs& a, bool f32, void* dgamma, hipStream_t s) {
-  return f32 ? bwd_of<float>(a, dgamma, s) : bwd_of<bf16_t>(a, dgamma, s);
+int norm_bwd_launch(const NormBwdArgs& a, bool f32, hipStream_t s) {
+  return f32 ? bwd_of<float>(a, s) : bwd_of<bf16_t>(a, s);
 }
 
 int dequant_rows_launch(const uint8_t* codes, const void* scales, int q_dtype, int64_t rows, int64_t cols, void* dst,

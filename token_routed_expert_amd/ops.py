@@ -645,6 +645,8 @@ def moe_dequantize_rows(codes, scales, q_dtype, dst, stream=None):
     call = "moe_dequantize_rows"
     rows, cols = dst.shape
     code, b = _src_dtype(call, dst), _Bufs(call)
+    if dst.numel() == 0:
+        return
     q, c, sc = _q_rows(b, call, q_dtype, rows * cols, codes, scales)
     _check(N.lib().moe_dequantize_rows(c, sc, q, rows, cols, b("dst", dst, dst.dtype, rows * cols), code,
                                        b.stream(stream)), call)
