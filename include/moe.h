@@ -914,7 +914,7 @@ int moe_add_rms_norm(const void* x, const void* residual, const void* gamma, int
  *   dgamma out [d] = sum over the rows of dy s rstd, in fp32, rounded once (T = 0:
  *          zeros)
  * from the forward's sum and rstd (without a residual: x).  Deterministic.
- * dx may be dy or dsum.  ws_bytes >= moe_workspace_bytes of a shape with this T
+ * dx may be dy, sum or dsum.  ws_bytes >= moe_workspace_bytes of a shape with this T
  * and d, MOE_WS_NORM_BWD.  Types, limits and errors as moe_add_rms_norm.
  */
 int moe_add_rms_norm_bwd(const void* dy, const void* sum, const float* rstd, const void* gamma, const void* dsum,

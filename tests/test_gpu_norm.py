@@ -219,7 +219,7 @@ def test_squares_past_the_range(T, d, dtype):
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("T,d", [(6, 512), (5000, 512), (300, 16384), (3, 40), (200, 9000), (500, 2056)])
 def test_in_place(T, d, dtype):
-    """sum over x or the residual, y over any of them, dx over dy or dsum."""
+    """sum over x or the residual, y over any of them, dx over dy, dsum or sum."""
     import token_routed_expert_amd as tre
     x, r, gamma = stream_rows(T, d, dtype, 11)
     sum_, y, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(T, device="cuda")
@@ -236,10 +236,10 @@ def test_in_place(T, d, dtype):
     ws = bwd_ws(T, d)
     dx, dg = torch.empty_like(x), torch.empty_like(gamma)
     tre.moe_add_rms_norm_bwd(dy, sum_, rstd, gamma, ds, dx, dg, ws)
-    for over in (0, 1):
-        t = [dy.clone(), ds.clone()]
+    for over in (0, 1, 2):
+        t = [dy.clone(), ds.clone(), sum_.clone()]
         dg2 = torch.empty_like(gamma)
-        tre.moe_add_rms_norm_bwd(t[0], sum_, rstd, gamma, t[1], t[over], dg2, ws)
+        tre.moe_add_rms_norm_bwd(t[0], t[2], rstd, gamma, t[1], t[over], dg2, ws)
         assert torch.equal(t[over], dx) and torch.equal(dg, dg2)
 
 

@@ -272,7 +272,7 @@ __device__ __forceinline__ void few_dgamma(const NormBwdArgs& a, int block) {
 // Teams of WPR wavefronts walk the rows with a stride of the number of teams and
 // keep their part of dgamma in registers; the parts, [teams][d] fp32, are summed
 // in order by a second kernel.  PRE: the next row is on its way while the current
-// one is worked on.  dx may be dy or dsum.  Bound by memory: 16384 rows of 7168 bf16 with
+// one is worked on.  dx may be dy, sum or dsum.  Bound by memory: 16384 rows of 7168 bf16 with
 // dsum 178 us (5.3 TB/s) and 5 for dgamma.
 //
 // FEW: one launch for few rows.  Every team has one row, and blocks after theirs take
@@ -453,10 +453,10 @@ int fwd_type(const NormArgs& a, hipStream_t s) {
 // One launch where a row is a team: two launches and one, calls in a row, us: 257 rows of
 // 512 fp32 10.4 and 8.0, 512 of 4096 13.0 / 9.9, 512 of 8192 19.8 / 16.9, 1024 of 1024 11.5 /
 // 10.0, 2048 of 512 14.2 / 15.2; bf16 256 of 16384 19.8 / 12.2.  (Its blocks for dgamma read
-// dy while others write dx, so these may not be one.)
+// dy and sum while others write dx, so dx may be neither.)
 bool few_rows(const NormBwdArgs& a, size_t bytes) {
-  const char *dx = (const char*)a.dx, *dy = (const char*)a.dy;
-  return a.T > 0 && a.T <= 1024 && a.teams == a.T && (dx + bytes <= dy || dy + bytes <= dx);
+  auto apart = [&](const void* p) { return (char*)a.dx + bytes <= (char*)p || (char*)p + bytes <= (char*)a.dx; };
+  return a.T > 0 && a.T <= 1024 && a.teams == a.T && apart(a.dy) && apart(a.sum);
 }
 
 template <typename T, int WPR, int NV>
