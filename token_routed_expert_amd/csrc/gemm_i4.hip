@@ -8,7 +8,8 @@
 // are the first operand (rows of D = C^T: four consecutive output columns per lane),
 // decoded to bf16 in registers: a lane's 16 bytes of a 128-row tile are its operands
 // of four products.  W13 holds W1's and W3's 16-column groups alternately, so a lane
-// holds a and b of the same element.
+// holds a and b of the same element.  h is rounded to bf16 because fc2's instructions
+// read it so, and the bf16 layers store it so: one rounding of the fp32 product.
 #include "gemm_common.h"
 #include "i4.h"
 
