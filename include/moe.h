@@ -842,9 +842,10 @@ int moe_quantize_weights_i4(const void* W, const void* W_pair, int32_t src_dtype
 
 /* moe_pack_weights_i4 -- the same layout from a checkpoint's codes q uint8
  * [E][R][C] (one to a byte, the low four bits count), scales s fp32 [E][R/group][C]
- * (rounded to 20 significant bits; not finite, or 2^124 and more: NaN) and zero points z uint8
- * [E][R/group][C] (the low four bits count; NULL: 8); q_pair, s_pair, z_pair: a second matrix whose
- * groups alternate, or NULL. */
+ * (rounded to 20 significant bits, below 2^-126 to multiples of 2^-145; not finite, or
+ * 2^124 and more after that: NaN) and zero points z uint8 [E][R/group][C] (the low
+ * four bits count; NULL: 8); q_pair, s_pair, z_pair: a second matrix whose groups
+ * alternate, or NULL. */
 int moe_pack_weights_i4(const uint8_t* q, const float* s, const uint8_t* z, const uint8_t* q_pair, const float* s_pair,
                         const uint8_t* z_pair, int64_t group, int64_t E, int64_t R, int64_t C, uint8_t* codes,
                         uint32_t* scales, void* stream);

@@ -186,10 +186,11 @@ __global__ __launch_bounds__(256) void pack_weights_i4_kernel(I4Source a, I4Sour
     const size_t row = ((size_t)t.e * (R / group) + (size_t)t.kt * U + u) * C + col;
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      // the scale to 20 significant bits, to nearest even
-      uint32_t bits = __float_as_uint(in.s[row + p]);
-      const bool fits = (bits & 0x7fffffffu) < i4::kTooLarge - 16;
-      bits = fits ? (bits + 7u + (bits >> 4 & 1u)) & ~15u : 0x7fc00000u;
+      // the scale to 20 significant bits, to nearest even (the carry of a finite number
+      // stays within its magnitude bits), then the border of what a scale may be
+      const uint32_t given = __float_as_uint(in.s[row + p]);
+      uint32_t bits = (given + 7u + (given >> 4 & 1u)) & ~15u;
+      if ((given & 0x7fffffffu) >= 0x7f800000u || (bits & 0x7fffffffu) >= i4::kTooLarge) bits = 0x7fc00000u;
       words[t.word_at(lane >> 3, ((2 * lane) & 15) + p, u, U)] = bits | (in.z ? in.z[row + p] & 15u : 8u);
     }
   }
