@@ -66,7 +66,8 @@ typedef enum {
   MOE_ERR_INVALID = 1,      /* null pointer, inconsistent or out-of-range sizes */
   MOE_ERR_UNSUPPORTED = 2,  /* valid but outside this build's limits (dtype, alignment, sizes
                                whose launch would need 2^32 threads or more) */
-  MOE_ERR_WORKSPACE = 3,    /* ws_bytes smaller than moe_workspace_bytes() */
+  MOE_ERR_WORKSPACE = 3,    /* ws_bytes smaller than moe_workspace_bytes() (or than the
+                               least that a call names) */
   MOE_ERR_HIP = 4           /* a HIP runtime call or kernel launch failed */
 } moe_status;
 
@@ -861,11 +862,25 @@ int moe_dequantize_weights_i4(const uint8_t* codes, const uint32_t* scales, int6
  *   [a|b] = x_r W13_e, h = silu(a) b rounded to bf16, o = h W2_e
  * with fp32 accumulation; o [P][d] is bf16.  Row r is row token_of[r] of x [T][d]
  * (an entry outside [0, T) reads a row of zeros), or, token_of NULL, row r of the
- * permuted x [P][d].  Rows of o from offsets[E] on are not written.  ws_bytes >=
- * moe_workspace_bytes(sh, MOE_WS_GEMM_FWD) (h, and fp32 sums where the rows are too
- * few to fill the chip with whole products).  Errors: MOE_ERR_INVALID for
- * another dtype; MOE_ERR_UNSUPPORTED for d or f not a multiple of 128, another
- * group than 32, 64 or 128, P * max(d, f) >= 2^30 - 2048 or d * f >= 2^31.
+ * permuted x [P][d].  Rows of o from offsets[E] on are not written.
+ *
+ * Workspace: h, P * f * 2 bytes, is the least (MOE_ERR_WORKSPACE below).
+ * moe_workspace_bytes(sh, MOE_WS_GEMM_FWD) adds the fp32 sums over up to four parts of
+ * the contraction (d and f) where the rows are too few to fill the chip with whole
+ * products; calls with more rows may need none, so that number does not always grow
+ * with T.  With less room the call takes as many parts as fit, one at least, and is
+ * slower for it.  So a workspace for the largest T serves every smaller one, and one of
+ * the largest number over the T that are served serves each at its best.  A layer's
+ * workspace likewise: MOE_WS_LAYER_FWD counts the sums, MOE_WS_PERMUTE + 256 + P * f * 2
+ * (with io->aux_loss: + MOE_WS_AUX_LOSS) is the least.
+ *
+ * The order of an element's fp32 sum, and with it the last bits of a result, goes by
+ * the kernel (moe_few_rows) and, in the kernel for many rows, by the parts of the
+ * contraction: by P, E, d, f and by ws_bytes where that holds fewer parts.
+ *
+ * Errors: MOE_ERR_INVALID for another dtype; MOE_ERR_UNSUPPORTED for d or f not a
+ * multiple of 128, another group than 32, 64 or 128, P * max(d, f) >= 2^30 - 2048 or
+ * d * f >= 2^31.
  */
 int moe_grouped_gemm_fwd_i4(const moe_shape* sh, const int32_t* offsets, const int32_t* token_of, const void* x,
                             const moe_i4_weights* w, void* o, void* ws, size_t ws_bytes, void* stream);
@@ -958,9 +973,10 @@ size_t moe_workspace_bytes(const moe_shape* sh, int kind);
 
 /* 1 where the expert products of shape sh run on the kernels for few rows, else
  * 0: moe_grouped_gemm_fwd_mx4 (MOE_MXFP4, MOE_MXFP4_A8), moe_grouped_gemm_fwd_i4
- * (MOE_INT4) and the 8-bit checkpoint calls (MOE_BF16).  Those kernels split the contraction, so results of calls on
- * the two sides differ in the order of their fp32 sums.  0 for other types and
- * for shapes that are refused. */
+ * (MOE_INT4) and the 8-bit checkpoint calls (MOE_BF16).  Those kernels split the
+ * contraction, so results of calls on the two sides differ in the order of their fp32
+ * sums.  (With MOE_INT4 so may those of two calls that both give 0: see
+ * moe_grouped_gemm_fwd_i4.)  0 for other types and for shapes that are refused. */
 int moe_few_rows(const moe_shape* sh);
 
 /* Static, NUL-terminated name of a moe_status value. */

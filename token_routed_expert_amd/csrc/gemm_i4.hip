@@ -633,11 +633,13 @@ struct TileCost {
   int parts;
   double time;
 };
-static TileCost tile_cost(const I4Args& a, int fc) {
+// `room`: bytes for the parts' sums; where the best number does not fit, the best that does.
+static TileCost tile_cost(const I4Args& a, int fc, size_t room) {
   const double K = (double)contraction(a, fc), tiles = blocks_of(a, fc, 128, 256);
   const double values = (double)a.P * (double)stored_columns(a, fc);
   TileCost best = {1, 0.0};
   for (int parts = 1; parts <= 4 && parts * 128 <= K; ++parts) {
+    if (parts > 1 && (size_t)parts * (size_t)a.P * (size_t)stored_columns(a, fc) * 4 > room) break;
     const double r = tiles * parts / 512;
     const double time = (r < 1.0 ? 0.5 + 0.5 * r : r) * K / parts + (parts > 1 ? 160 + 1e-4 * values * parts : 0.0);
     if (parts == 1 || time < best.time) best = {parts, time};
@@ -645,7 +647,7 @@ static TileCost tile_cost(const I4Args& a, int fc) {
   return best;
 }
 
-int gemm_i4_parts(const I4Args& a, int fc) { return gemm_i4_few_rows(a) ? 1 : tile_cost(a, fc).parts; }
+int gemm_i4_parts(const I4Args& a, int fc) { return gemm_i4_few_rows(a) ? 1 : tile_cost(a, fc, a.part_bytes).parts; }
 
 // Which kernel.  The rows kernel's time goes with the rounds of its pieces of 32 rows x
 // 64 columns, three to a compute unit; a step of a chip of tiles takes three times as
@@ -660,7 +662,7 @@ bool gemm_i4_few_rows(const I4Args& a) {
   for (int fc = 1; fc <= 2; ++fc) {
     const double r = blocks_of(a, fc, 32, 64) / 768;
     rows += (r > 0.35 ? r : 0.35) * (double)contraction(a, fc);
-    tiles += tile_cost(a, fc).time;
+    tiles += tile_cost(a, fc, SIZE_MAX).time;  // (whatever this call's workspace: the choice is the shape's)
   }
   return rows <= 3.0 * tiles;
 }

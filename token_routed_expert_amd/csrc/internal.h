@@ -247,8 +247,9 @@ struct I4Args {
   uint16_t* h;
   uint16_t* o;
   float* part;  // fp32 [parts][P][2 f or d], where the parts of K are more than one
+  size_t part_bytes;  // that part may hold
 };
-int gemm_i4_parts(const I4Args& a, int fc);  // parts that a product's K is taken in (E, d, f and P decide)
+int gemm_i4_parts(const I4Args& a, int fc);  // parts that a product's K is taken in (E, d, f, P and part_bytes decide)
 int gemm_i4_launch(int fc, const I4Args& a, hipStream_t s);
 bool gemm_i4_few_rows(const I4Args& a);  // which of its two kernels (E, d, f and P decide)
 

@@ -170,10 +170,13 @@ int check_mx4_dims(const moe_shape* sh) {
 }
 
 // Integer weights: the workspace holds h and, where K is taken in parts, those
-// sums; 32-bit byte offsets as for MXFP4, of rows of two bytes a value.
+// sums; 32-bit byte offsets as for MXFP4, of rows of two bytes a value.  h alone is
+// enough (and grows with T, unlike the sums, which calls with more rows may not
+// need): K is then taken in as many parts as there is room for.
 I4Args i4_sizes(const moe_shape* sh) {
   I4Args a = {};
   a.E = (int)sh->E; a.d = (int)sh->d; a.f = (int)sh->f; a.P = (int)(sh->T * sh->k); a.T = (int)sh->T;
+  a.part_bytes = SIZE_MAX;
   return a;
 }
 size_t i4_h_bytes(const moe_shape* sh) { return align_up((size_t)(sh->T * sh->k * sh->f) * 2, 256); }
@@ -1183,8 +1186,9 @@ int moe_grouped_gemm_fwd_i4(const moe_shape* sh, const int32_t* offsets, const i
   if ((st = check_weights(w))) return st;
   if (!aligned(16, (const char*)x, (const char*)o, (const char*)ws) || !aligned(4, offsets, token_of))
     return MOE_ERR_UNSUPPORTED;
-  if (!ws || ws_bytes < i4_ws_bytes(sh)) return MOE_ERR_WORKSPACE;
+  if (!ws || ws_bytes < i4_h_bytes(sh)) return MOE_ERR_WORKSPACE;
   I4Args a = i4_sizes(sh);
+  a.part_bytes = ws_bytes - i4_h_bytes(sh);
   a.offsets = offsets; a.token_of = token_of;
   a.group = (int)w->group;
   a.a = (const uint16_t*)x; a.w = w->W13; a.ws = w->W13s;
@@ -1408,15 +1412,15 @@ int layer_fwd_i4(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t w
   if (!aligned(16, (const char*)io->x, (const char*)io->o, (const char*)io->y, (const char*)ws))
     return MOE_ERR_UNSUPPORTED;
   const size_t pws = permute_ws_bytes(sh->T, sh->E);
-  const size_t gws = i4_ws_bytes(sh);
-  if (!ws || ws_bytes < pws + 256 + gws || !aux_ws_ok(sh, io, ws_bytes)) return MOE_ERR_WORKSPACE;
+  if (!ws || ws_bytes < pws + 256 + i4_h_bytes(sh) || !aux_ws_ok(sh, io, ws_bytes)) return MOE_ERR_WORKSPACE;
   if ((st = layer_route(sh, io, ws, ws_bytes, stream))) return st;
   if ((st = moe_permute(sh, nullptr, io->topk_idx, nullptr, 1, io->counts, io->offsets, io->row_of,
                         io->token_of, nullptr, ws, pws, stream)))
     return st;
   if ((st = layer_aux_loss(sh, io, ws, ws_bytes, stream))) return st;
+  // the rest of the workspace, the aux loss's part (read above) among it
   if ((st = moe_grouped_gemm_fwd_i4(sh, io->offsets, io->token_of, io->x, io->wi4, io->o,
-                                    (char*)ws + pws + 256, gws, stream)))
+                                    (char*)ws + pws + 256, ws_bytes - pws - 256, stream)))
     return st;
   const void* add = nullptr;
   if (sh->f_shared) {
@@ -1519,20 +1523,24 @@ int layer_bwd_e4m3(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t
 
 namespace {
 
-// the aux loss's workspace follows the layer's forward workspace
+// Where the aux loss's part of a layer's forward workspace begins: behind the
+// MOE_WS_LAYER_FWD bytes; with integer weights behind the least that the layer needs
+size_t aux_ws_at(const moe_shape* sh) {
+  if (is_i4(sh)) return permute_ws_bytes(sh->T, sh->E) + 256 + i4_h_bytes(sh);
+  return moe_workspace_bytes(sh, MOE_WS_LAYER_FWD);
+}
 bool aux_ws_ok(const moe_shape* sh, const moe_layer_io* io, size_t ws_bytes) {
-  return !io->aux_loss ||
-         ws_bytes >= moe_workspace_bytes(sh, MOE_WS_LAYER_FWD) + aux_ws_bytes(sh->T, sh->E);
+  return !io->aux_loss || ws_bytes >= aux_ws_at(sh) + aux_ws_bytes(sh->T, sh->E);
 }
 
 // Routing of a layer; when io->aux_loss is set, fused with the loss's
 // softmax column sums, which go to the aux region of the forward workspace
-// (after the MOE_WS_LAYER_FWD bytes, untouched by the permutation).
+// (untouched by the permutation).
 int layer_route(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t ws_bytes,
                 void* stream) {
   if (!io->aux_loss)
     return moe_route(io->logits, sh->T, sh->E, sh->k, io->topk_idx, io->topk_prob, stream);
-  const size_t base = moe_workspace_bytes(sh, MOE_WS_LAYER_FWD);
+  const size_t base = aux_ws_at(sh);
   const size_t need = aux_ws_bytes(sh->T, sh->E);
   if (ws_bytes < base + need) return MOE_ERR_WORKSPACE;
   return moe_route_aux(io->logits, sh->T, sh->E, sh->k, io->topk_idx, io->topk_prob,
@@ -1543,7 +1551,7 @@ int layer_route(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t ws
 int layer_aux_loss(const moe_shape* sh, const moe_layer_io* io, void* ws, size_t ws_bytes,
                    void* stream) {
   if (!io->aux_loss) return MOE_OK;
-  const size_t base = moe_workspace_bytes(sh, MOE_WS_LAYER_FWD);
+  const size_t base = aux_ws_at(sh);
   if (ws_bytes < base + aux_ws_bytes(sh->T, sh->E)) return MOE_ERR_WORKSPACE;
   return moe_aux_loss_final((char*)ws + base, sh->T, sh->E, sh->k, io->counts, io->aux_alpha,
                             io->aux_loss, stream);
