@@ -98,7 +98,8 @@ typedef enum {
   MOE_WS_AUX_LOSS = 5,
   MOE_WS_GEMM_BWD_ROWSCALED = 6,
   MOE_WS_LAYER_BWD_ROWSCALED = 7,
-  MOE_WS_NORM_BWD = 8 /* moe_add_rms_norm_bwd: the shape's T and d count */
+  MOE_WS_NORM_BWD = 8,     /* moe_add_rms_norm_bwd: the shape's T and d count */
+  MOE_WS_NORM_BWD_MAX = 9  /* the same, enough for every T up to the shape's */
 } moe_ws_kind;
 
 /*
@@ -931,7 +932,10 @@ int moe_add_rms_norm(const void* x, const void* residual, const void* gamma, int
  *          zeros)
  * from the forward's sum and rstd (without a residual: x).  Deterministic.
  * dx may be dy, sum or dsum.  ws_bytes >= moe_workspace_bytes of a shape with this T
- * and d, MOE_WS_NORM_BWD.  Types, limits and errors as moe_add_rms_norm.
+ * and d (E = k = 1 and any f do), MOE_WS_NORM_BWD.  That number falls where T passes
+ * what the chip takes at once, since the rows are then dealt out evenly; a program that
+ * keeps one workspace asks for MOE_WS_NORM_BWD_MAX with its largest T.  Types, limits
+ * and errors as moe_add_rms_norm.
  */
 int moe_add_rms_norm_bwd(const void* dy, const void* sum, const float* rstd, const void* gamma, const void* dsum,
                          int32_t dtype, int64_t T, int64_t d, void* dx, void* dgamma, void* ws, size_t ws_bytes,

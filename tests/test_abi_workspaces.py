@@ -60,3 +60,30 @@ def test_int4_workspace_of_a_larger_batch(d, E, k, f, top):
     for T in [1, 2, 40, *range(101, top, 101), top - 1, top]:
         sh = make_shape(T, d, E, k, f, dtype="int4")
         assert lib.moe_grouped_gemm_fwd_i4(C.byref(sh), P, None, P, C.byref(w), P, P, nb, None) == N.MOE_ERR_HIP
+
+
+@pytest.mark.parametrize("d", [8, 512, 1024, 1032, 4096, 8192, 8200, 32768])
+def test_norm_backward_workspace_of_a_larger_batch(d):
+    """MOE_WS_NORM_BWD_MAX grows with T and holds what every smaller T needs; MOE_WS_NORM_BWD alone does not."""
+    lib = N.lib()
+    need = most = 0
+    fell = False
+    for T in [*range(1, 4200), 16384, 16385, 100000, (1 << 31) - 1]:
+        sh = make_shape(T, d, 1, 1, 128, dtype="f32")
+        now, top = (moe_workspace_bytes(sh, k) for k in (N.MOE_WS_NORM_BWD, N.MOE_WS_NORM_BWD_MAX))
+        fell = fell or now < need
+        need = max(need, now)
+        assert top == need and top >= most
+        most = top
+    assert fell
+    for T in (1, 7, 255, 256, 257, 511, 512, 513, 2047, 2048, 2049, 4100):
+        assert lib.moe_add_rms_norm_bwd(*[P] * 5, N.MOE_F32, T, d, P, P, P,
+                                        moe_workspace_bytes(make_shape(T, d, 1, 1, 128), N.MOE_WS_NORM_BWD) - 1, None) == WS
+
+
+@pytest.mark.skipif(torch.cuda.device_count() > 0, reason="takes calls up to their launch, which only fails without a GPU")
+@pytest.mark.parametrize("d,top", [(512, 5000), (1024, 2049), (4096, 513), (7168, 16384), (16384, 300)])
+def test_norm_backward_takes_the_larger_workspace(d, top):
+    nb = moe_workspace_bytes(make_shape(top, d, 1, 1, 128), N.MOE_WS_NORM_BWD_MAX)
+    for T in sorted({1, 2, 100, 256, 257, 512, 513, 1024, 2048, top - 1, top} & set(range(top + 1))):
+        assert N.lib().moe_add_rms_norm_bwd(*[P] * 5, N.MOE_BF16, T, d, P, P, P, nb, None) == N.MOE_ERR_HIP

@@ -6,7 +6,7 @@ this package only marshals torch tensors into its calls.
 from . import _native
 from ._native import (MOE_WS_AUX_LOSS, MOE_WS_GEMM_BWD, MOE_WS_GEMM_BWD_ROWSCALED, MOE_WS_GEMM_FWD,
                       MOE_WS_LAYER_BWD, MOE_WS_LAYER_BWD_ROWSCALED, MOE_WS_LAYER_FWD,
-                      MOE_WS_NORM_BWD, MOE_WS_PERMUTE)
+                      MOE_WS_NORM_BWD, MOE_WS_NORM_BWD_MAX, MOE_WS_PERMUTE)
 from .ops import (E4M3Weights, I4Weights, MX4Weights, MXWeights, MoeError, make_shape, moe_aux_loss, moe_combine_bwd,
                   moe_quantize_rows_mx, moe_quantize_weights_mx, moe_quantize_token_blocks_mx,
                   moe_permute_mx, moe_grouped_gemm_fwd_mx, moe_grouped_gemm_bwd_mx,
@@ -42,7 +42,7 @@ __all__ = ["MoeError", "make_shape", "moe_route", "moe_permute", "moe_unpermute"
            "moe_grouped_gemm_fwd_ckpt8", "moe_grouped_gemm_bwd_ckpt8", "moe_few_rows",
            "MOE_WS_PERMUTE", "MOE_WS_GEMM_FWD", "MOE_WS_GEMM_BWD", "MOE_WS_LAYER_FWD",
            "MOE_WS_LAYER_BWD", "MOE_WS_AUX_LOSS", "MOE_WS_GEMM_BWD_ROWSCALED",
-           "MOE_WS_LAYER_BWD_ROWSCALED", "MOE_WS_NORM_BWD", "moe_add_rms_norm",
+           "MOE_WS_LAYER_BWD_ROWSCALED", "MOE_WS_NORM_BWD", "MOE_WS_NORM_BWD_MAX", "moe_add_rms_norm",
            "moe_add_rms_norm_bwd", "moe_dequantize_rows", "I4Weights",
            "moe_quantize_weights_i4", "moe_pack_weights_i4", "moe_dequantize_weights_i4",
            "moe_grouped_gemm_fwd_i4", "_native"]

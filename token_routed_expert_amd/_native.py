@@ -14,7 +14,7 @@ MOE_OK, MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = r
 MOE_F32, MOE_BF16, MOE_E4M3, MOE_MXFP8, MOE_MXFP4, MOE_MXFP4_A8, MOE_INT4 = range(7)
 (MOE_WS_PERMUTE, MOE_WS_GEMM_FWD, MOE_WS_GEMM_BWD, MOE_WS_LAYER_FWD,
  MOE_WS_LAYER_BWD, MOE_WS_AUX_LOSS, MOE_WS_GEMM_BWD_ROWSCALED,
- MOE_WS_LAYER_BWD_ROWSCALED, MOE_WS_NORM_BWD) = range(9)
+ MOE_WS_LAYER_BWD_ROWSCALED, MOE_WS_NORM_BWD, MOE_WS_NORM_BWD_MAX) = range(10)
 
 
 class moe_shape(C.Structure):

@@ -215,6 +215,7 @@ struct NormBwdArgs {
   bool few;     // (the launch's own choice)
 };
 int64_t norm_bwd_teams(int64_t T, int64_t d);
+int64_t norm_bwd_most_teams(int64_t T, int64_t d);  // of T rows or fewer
 int norm_bwd_launch(const NormBwdArgs& a, bool f32, hipStream_t s);
 int dequant_rows_launch(const uint8_t* codes, const void* scales, int q_dtype, int64_t rows, int64_t cols, void* dst,
                         bool f32, hipStream_t s);

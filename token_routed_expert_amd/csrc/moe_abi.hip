@@ -505,6 +505,7 @@ int moe_few_rows(const moe_shape* sh) {
 size_t moe_workspace_bytes(const moe_shape* sh, int kind) {
   if (check_shape(sh) != MOE_OK) return 0;
   if (kind == MOE_WS_NORM_BWD) return (size_t)(norm_bwd_teams(sh->T, sh->d) * sh->d) * 4;
+  if (kind == MOE_WS_NORM_BWD_MAX) return (size_t)(norm_bwd_most_teams(sh->T, sh->d) * sh->d) * 4;
   if (is_fp8(sh)) {
     switch (kind) {
       case MOE_WS_AUX_LOSS: return aux_ws_bytes(sh->T, sh->E);

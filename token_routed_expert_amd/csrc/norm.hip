@@ -511,9 +511,11 @@ int dequant_as(const uint8_t* codes, const void* scales, int64_t rows, int64_t c
 
 // Teams of the backward: as many as keep the chip busy, each with as many rows as
 // the others or one fewer.
+static int64_t most_teams(int64_t d) { return d <= 1024 ? 2048 : d <= 8192 ? 512 : 256; }
+int64_t norm_bwd_most_teams(int64_t T, int64_t d) { return T < most_teams(d) ? T : most_teams(d); }
 int64_t norm_bwd_teams(int64_t T, int64_t d) {
   if (T < 1) return 0;
-  const int64_t most = d <= 1024 ? 2048 : d <= 8192 ? 512 : 256;
+  const int64_t most = most_teams(d);
   const int64_t rows = (T + most - 1) / most;
   return (T + rows - 1) / rows;
 }
