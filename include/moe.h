@@ -916,8 +916,8 @@ int moe_grouped_gemm_fwd_i4(const moe_shape* sh, const int32_t* offsets, const i
  * as rstd is.  T = 0 does nothing.  Errors:
  * MOE_ERR_INVALID for null x or gamma, no output, codes without scales, T < 0, d
  * < 1, eps negative or not finite; MOE_ERR_UNSUPPORTED for d not a multiple of 8
- * (128 for E4M3 rows, 32 for MX rows) or above 32768, T >= 2^31, other types,
- * misaligned pointers.
+ * (128 for E4M3 rows, 32 for MX rows) or above 32768, T >= 2^31 (2^26, 2^24 and 2^22 for
+ * d up to 1024, up to 8192 and above: 2^32 threads), other types, misaligned pointers.
  */
 int moe_add_rms_norm(const void* x, const void* residual, const void* gamma, int32_t dtype, int64_t T, int64_t d,
                      float eps, void* sum, void* y, float* rstd, int32_t q_dtype, uint8_t* codes, void* scales,
@@ -935,7 +935,7 @@ int moe_add_rms_norm(const void* x, const void* residual, const void* gamma, int
  * and d (E = k = 1 and any f do), MOE_WS_NORM_BWD.  That number falls where T passes
  * what the chip takes at once, since the rows are then dealt out evenly; a program that
  * keeps one workspace asks for MOE_WS_NORM_BWD_MAX with its largest T.  Types, limits
- * and errors as moe_add_rms_norm.
+ * and errors as moe_add_rms_norm (T < 2^31 for every d).
  */
 int moe_add_rms_norm_bwd(const void* dy, const void* sum, const float* rstd, const void* gamma, const void* dsum,
                          int32_t dtype, int64_t T, int64_t d, void* dx, void* dgamma, void* ws, size_t ws_bytes,

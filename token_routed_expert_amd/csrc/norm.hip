@@ -10,8 +10,8 @@
 //
 // Bound by memory: a row is read once, held in registers as fp32, and everything
 // that is asked for of it leaves in one pass.  16384 rows of 7168 bf16 with residual,
-// sum, y and MXFP8 rows 184 us (5.8 TB/s), 8200 of 4096 fp32 with E4M3 rows 112 us (5.1);
-// one row 3.0 us.
+// sum, y and MXFP8 rows 184 us (5.8 TB/s), with MXFP4 rows 176 (5.7); 8200 of 4096 fp32
+// with E4M3 rows 112 us (5.1); 8192 of 16384 bf16 without rows 190 (5.7); one row 3.0 us.
 #include <type_traits>
 
 #include "common.h"
@@ -189,8 +189,10 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_kernel(NormArg
     }
   }
   // Eight sums a lane, then a tree, and the root in 64 bits: an error of rstd moves a
-  // whole row's values over rounding borders of the codes (one sum and fp32: 1.6 times
-  // the error of the MXFP8 values of 7168 columns).
+  // whole row's values towards rounding borders of the codes.  Its relative error is
+  // 3.5e-8 (root mean square over 16384 rows of 7168; elementwise fp32 operations: 4.4e-8).
+  // Codes that differ from those of the exact v are next to a tie of the format: 57, 70
+  // and 84 of 117 million values over three inputs (elementwise: 55, 81, 112).
   float v[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -274,6 +276,12 @@ __device__ __forceinline__ void few_dgamma(const NormBwdArgs& a, int block) {
 // in order by a second kernel.  PRE: the next row is on its way while the current
 // one is worked on.  dx may be dy, sum or dsum.  Bound by memory: 16384 rows of 7168 bf16 with
 // dsum 178 us (5.3 TB/s) and 5 for dgamma.
+//
+// Rows of more than 8192 values take sixteen wavefronts, whose 128 registers a lane do not
+// hold the row, the next one and dgamma: 19 (bf16, two vectors a lane) to 229 (bf16, four)
+// of them lie in scratch memory, which bounds these rows: 8192 of 16384 bf16 299 us (3.6
+// TB/s), 4096 of 16384 fp32 488 (2.2), 2048 of 32768 fp32 468 (2.3), 4096 of 32768 bf16
+// 1090 (1.0).
 //
 // FEW: one launch for few rows.  Every team has one row, and blocks after theirs take
 // dgamma from dy, sum and rstd again.
@@ -431,10 +439,12 @@ int fwd_of(const NormArgs& a, hipStream_t s) {
   // 16384 rows of 7168: 214 us against 187; 8200 of 4096, fp32: 123 against 111), and
   // sixteen where there are too few rows for the chip (177 of 7168: 5.4 us against 7.2)
   // or a row is longer than four hold.
-  // sum and y of 32 MB and more, all L2s together, are written past the caches: 5000
-  // rows of 4096 36.0 us against 28.1, 4096 of 7168 56 / 46, 40000 of 512 34.8 / 28.2.
-  // (The codes, which the layer reads next, are not: it would cost their reader more
-  // than it saves here.)
+  // sum and y of 32 MB and more, all L2s together, are written past the caches by the
+  // forms of one and four wavefronts: 5000 rows of 4096 36.0 us against 28.1, 4096 of 7168
+  // 56 / 46, 40000 of 512 34.8 / 28.2.  (Sixteen wavefronts store through them: 8192 rows of
+  // 16384 190 us, 5.7 TB/s, which is what the others reach past them.  The codes, which
+  // the layer reads next, are not written past them either: it would cost their reader
+  // more than it saves here.)
   const int nvec = a.d / 8;
   const bool past = a.T * a.d * (int64_t)sizeof(T) >= (int64_t)1 << 25;
   if (nvec <= 128) return past ? fwd_as<T, Q, 1, 2, true>(a, s) : fwd_as<T, Q, 1, 2>(a, s);
@@ -459,6 +469,9 @@ bool few_rows(const NormBwdArgs& a, size_t bytes) {
   return a.T > 0 && a.T <= 1024 && a.teams == a.T && apart(a.dy) && apart(a.sum);
 }
 
+// PRE where a lane has 64 bytes of each tensor or less: without it and with it, us: 16384
+// rows of 4096 bf16 103.7 and 100.3, fp32 207.4 / 204.6, 4096 of 7168 bf16 44.0 / 42.9, 16384
+// of 1024 as long; fp32 of 8192 (not taken) 400 / 396.
 template <typename T, int WPR, int NV>
 int bwd_as(const NormBwdArgs& a, hipStream_t s) {
   constexpr int THREADS = WPR == 1 ? 256 : 64 * WPR;
