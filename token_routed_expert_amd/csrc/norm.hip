@@ -191,8 +191,8 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void norm_kernel(NormArg
   // Eight sums a lane, then a tree, and the root in 64 bits: an error of rstd moves a
   // whole row's values towards rounding borders of the codes.  Its relative error is
   // 3.5e-8 (root mean square over 16384 rows of 7168; elementwise fp32 operations: 4.4e-8).
-  // Codes that differ from those of the exact v are next to a tie of the format: 57, 70
-  // and 84 of 117 million values over three inputs (elementwise: 55, 81, 112).
+  // MXFP8 codes that differ from those of the exact v are next to a tie: 57, 70 and 84 of
+  // those 117 million values over three inputs (elementwise: 55, 81, 112).
   float v[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
